@@ -85,9 +85,38 @@ class LnParamsC(ctypes.Structure):
     ]
 
 
-# Every symbol include/gbattn.h and include/gbln.h declare, with its ctypes signature.
+class Kv4ParamsC(ctypes.Structure):
+    """attn_kv4_params_t of include/gbkv4.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("heads_q", ctypes.c_int32),
+        ("heads_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("seqlen", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("lens", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("x_stride_b", ctypes.c_int64),
+        ("x_stride_h", ctypes.c_int64),
+        ("x_stride_s", ctypes.c_int64),
+        ("y_stride_b", ctypes.c_int64),
+        ("y_stride_h", ctypes.c_int64),
+        ("y_stride_s", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+    ]
+
+
+# Every symbol the headers under include/ declare, with its ctypes signature.
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(ParamsC)
+_KP = ctypes.POINTER(Kv4ParamsC)
 SIGNATURES = {
     "attn_fwd_workspace_size": (ctypes.c_size_t, [_PP]),
     "attn_bwd_workspace_size": (ctypes.c_size_t, [_PP]),
@@ -104,6 +133,10 @@ SIGNATURES = {
     "attn_set_timing_events": (ctypes.c_int, [ctypes.c_int, _VP, _VP]),
     "attn_version": (ctypes.c_char_p, []),
     "attn_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint, _VP]),
+    "attn_kv4_write": (ctypes.c_int, [_KP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "attn_kv4_read": (ctypes.c_int, [_KP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "attn_kv4_workspace_size": (ctypes.c_size_t, [_KP]),
+    "attn_fwd_kv4": (ctypes.c_int, [_KP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "ln_residual_fwd": (ctypes.c_int, [ctypes.POINTER(LnParamsC), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
 }
 

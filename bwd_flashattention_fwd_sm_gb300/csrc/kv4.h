@@ -1,0 +1,98 @@
+// The 4-bit key/value cache: what its kernels share.  Internal to the library
+// (the public interface is include/gbkv4.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace gbattn {
+
+constexpr int kKv4Group = 64;  // values that share one (s, b) pair
+
+// Everything a kernel needs, resolved on the host.  Strides in elements.
+struct Kv4Args {
+  uint8_t* kc;   // codes [n_pages, heads_kv, page, D / 2]
+  uint8_t* vc;
+  uint32_t* ks;  // (s, b) pairs [n_pages, heads_kv, page, D / 64], s in the low half
+  uint32_t* vs;
+  const int* table;
+  long long table_stride;
+  const int* lens;
+  const int* cu;         // NULL: fixed length
+  long long total;       // packed rows
+  int batch, heads_q, heads_kv, group, seqlen, page, n_pages, max_pages;
+  void* x;
+  void* y;
+  float* lse;
+  long long x_sb, x_sh, x_ss, y_sb, y_sh, y_ss;
+  float scale_log2;  // scale * log2(e)
+  int causal;
+  int* status;
+};
+
+// One sequence's rows in x and y and its length in the cache.
+struct Kv4Seq {
+  int n;           // rows; row i sits at position len - n + i
+  int len;         // positions, cut to what the page list can hold
+  long long row0;  // packed: first row
+};
+
+// What only the device knows is checked by the two functions below: *bad is set,
+// and the sequence has no rows, or the row is -1.
+__host__ __device__ inline Kv4Seq kv4_seq_of(const Kv4Args& a, int b, bool* bad) {
+  Kv4Seq s;
+  s.n = a.seqlen;
+  s.row0 = 0;
+  if (a.cu) {
+    const int r0 = a.cu[b], r1 = a.cu[b + 1];
+    const bool ok = r0 >= 0 && r1 >= r0 && r1 <= a.total && r1 - r0 <= a.seqlen;
+    if (!ok) *bad = true;
+    s.n = ok ? r1 - r0 : 0;
+    s.row0 = r0;
+  }
+  const long long room = (long long)a.max_pages * a.page, most = room < 0x7FFFFFFF ? room : 0x7FFFFFFF;
+  const int len = a.lens[b];
+  if (len < 0 || len > most) *bad = true;
+  s.len = len < 0 ? 0 : (len > most ? (int)most : len);
+  return s;
+}
+
+// Row of position `pos` (below the sequence's length) and head h in the cache, as
+// an index over [n_pages, heads_kv, page].
+__host__ __device__ inline long long kv4_row_index(const Kv4Args& a, int b, int h, int pos, bool* bad) {
+  const int pid = a.table[b * a.table_stride + pos / a.page];
+  if (pid < 0 || pid >= a.n_pages) {
+    *bad = true;
+    return -1;
+  }
+  return ((long long)pid * a.heads_kv + h) * a.page + pos % a.page;
+}
+
+__device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Args& a, int b) {
+  bool bad = false;
+  const Kv4Seq s = kv4_seq_of(a, b, &bad);
+  if (bad) set_status(a.status, kStatusBounds);
+  return s;
+}
+
+__device__ __forceinline__ long long kv4_row(const Kv4Args& a, int b, int h, int pos) {
+  bool bad = false;
+  const long long row = kv4_row_index(a, b, h, pos, &bad);
+  if (bad) set_status(a.status, kStatusBounds);
+  return row;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+cudaError_t launch_kv4_write(const Kv4Args& a, int head_dim, bool bf16, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4Args& a, int head_dim, bool bf16, cudaStream_t st);
+
+// Attention over the cache: device scratch for these shapes, and the launch.
+size_t kv4_attn_workspace(const Kv4Args& a, int head_dim, bool bf16);
+cudaError_t launch_kv4_attn(const Kv4Args& a, int head_dim, bool bf16, void* workspace, cudaStream_t st);
+
+}  // namespace gbattn
