@@ -1,81 +1,902 @@
 // Attention over the 4-bit key/value cache.
 //
-// One warp per query row: its lanes hold the row's values and take the keys one
-// after the other, with the running maximum and sum of an online softmax, all in
-// float32.
+// Few query rows meet many keys: the kernel is bound by the cache's bytes, and next
+// by the instructions that turn codes into operands.  So keys take the place of the
+// rows of a matrix product and the queries of one KV head (its group's heads times
+// the new tokens) that of the columns: S^T = K Q^T and O^T = V^T P^T on
+// m16n8k16 instructions, 16 keys (16 values of the head) by 8 queries.  A lane then
+// needs whole code words of a key, in the order in which the cache holds them, and
+// every operand is unpacked once however many columns there are.
+//
+//   K: word & 0x000F000F is a pair of codes u 2^-24 as float16 subnormals, word &
+//      0x00F000F0 a pair u 2^-20: no conversion at all.  Q is held in float16, each
+//      row scaled by its own power of two (two parts for float32 queries), those of
+//      the second kind of pair by 1/16 more.  With s, b a key's step and offset of a
+//      group, its part of the score is s sum(q u) + (b - 8 s) sum(q), in float32.
+//   V: codes as bfloat16 integers -8 .. 7 (128 + u by bit operations, minus 136, both
+//      exact).  The weights p s are rounded to bfloat16, whose range holds them whatever
+//      the steps are (float32 queries: three parts, 24 bits); the offsets' part
+//      sum(p b) stays in float32.
+//
+// Work.  A tile is the keys that a block's warps take at a time; the tiles of all
+// sequences, KV heads and row tiles stand in one line that is cut into equal
+// stretches, one a block, whatever the lengths are: the blocks read the lengths
+// themselves.  A stretch that ends inside a row tile's keys leaves its partial
+// result, which a second kernel joins in order, so results do not vary.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
 #include "kv4.h"
 
 namespace gbattn {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kSms = 152;  // a fixed count, so that the workspace size needs no device query
 
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads) k_kv4_attn(const __grid_constant__ Kv4Args a) {
-  constexpr int G = D / kKv4Group, E = D / 32;  // values of a lane
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (w >= (long long)a.batch * a.heads_q * a.seqlen) return;
-  const int i = (int)(w % a.seqlen), hq = (int)(w / a.seqlen % a.heads_q), b = (int)(w / a.seqlen / a.heads_q);
-  const Kv4Seq s = kv4_seq(a, b);
-  if (i >= s.n) return;
-  const int pos = s.len - s.n + i, last = a.causal ? pos + 1 : (pos < 0 ? 0 : s.len);
-  const T* q = static_cast<const T*>(a.x) + (a.cu ? (s.row0 + i) * a.x_ss : b * a.x_sb + i * a.x_ss) + hq * a.x_sh;
-  float qv[E], o[E];
-  const int d0 = lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = to_f32(q[d0 + e]), o[e] = 0.f;
-  const int g = d0 / kKv4Group, word = (d0 % kKv4Group) / 8 * G + g, shift = d0 % 8 * 4;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < last; ++j) {
-    const long long row = kv4_row(a, b, hq / a.group, j);
-    if (row < 0) continue;
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(a.kc + row * (D / 2) + word * 4) >> shift;
-    const uint32_t vw = *reinterpret_cast<const uint32_t*>(a.vc + row * (D / 2) + word * 4) >> shift;
-    const uint32_t ks = a.ks[row * G + g], vs = a.vs[row * G + g];
-    float t = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      t = fmaf(qv[e], fmaf(bf16_lo(ks), (float)(int)((kw >> (4 * e)) & 15u) - 8.f, bf16_hi(ks)), t);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-    t *= a.scale_log2;
-    const float mn = fmaxf(m, t), c = exp2f(m - mn), p = exp2f(t - mn);
-    m = mn;
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(p, fmaf(bf16_lo(vs), (float)(int)((vw >> (4 * e)) & 15u) - 8.f, bf16_hi(vs)), o[e] * c);
-  }
-  T* y = static_cast<T*>(a.y) + (a.cu ? (s.row0 + i) * a.y_ss : b * a.y_sb + i * a.y_ss) + hq * a.y_sh;
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[d0 + e] = from_f32<T>(l != 0.f ? o[e] / l : 0.f);
-  if (lane == 0)
-    a.lse[a.cu ? (long long)hq * a.total + s.row0 + i : ((long long)b * a.heads_q + hq) * a.seqlen + i] =
-        l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+// n / d for 0 <= n < 2^31: (n * mul) >> shift with mul = floor(2^shift / d) + 1.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+FastDiv fast_div(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  return {(uint32_t)((1ull << (31 + l)) / (uint32_t)d + 1), (uint32_t)(31 + l)};
+}
+__device__ __forceinline__ int div_by(int n, FastDiv d) {
+  return (int)(((unsigned long long)(uint32_t)n * d.mul) >> d.shift);
 }
 
-template <class T, int D>
-cudaError_t launch(const Kv4Args& a, cudaStream_t st) {
-  const long long rows = (long long)a.batch * a.heads_q * a.seqlen, per = kThreads / 32;
-  k_kv4_attn<T, D><<<(unsigned)((rows + per - 1) / per), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+constexpr int kNoRow = 0x7FFFFFFF;  // the limit of a column without a query: it masks nothing
+
+struct AttnArgs {
+  Kv4Args a;
+  FastDiv page_div;
+  float* part_o;   // [blocks][2][row tile's accumulators]
+  float* part_ml;  // [blocks][2][rows][2]: row maximum (log2 units) and sum
+};
+
+template <int D, int NT, bool F32>
+struct Shape {
+  static constexpr int G = D / kKv4Group;
+  static constexpr int R = 8 * NT;                      // query rows of a row tile
+  static constexpr int CH = (D == 256 || NT == 4) ? 1 : 2;  // 16-key chunks of a warp at a time
+  static constexpr int KT = kWarps * CH * 16;           // keys of a tile
+  static constexpr int QP = F32 ? 2 : 1;                // float16 parts of Q
+  static constexpr int PP = F32 ? 3 : 1;                // bfloat16 parts of P
+  static constexpr int ACC = G * 4 * NT * 4;            // accumulators of a lane
+  static constexpr int QREGS = G * 4 * NT * QP * 2;
+  static constexpr bool QSMEM = QREGS > 32;             // Q operands read from shared memory each time
+  static constexpr int BLOCKS = (NT == 1 && D <= 128 && !F32) ? 3 : 2;  // blocks of an SM
+  static constexpr int GRID = kSms * BLOCKS;
+  static constexpr size_t Q_BYTES = (size_t)G * 4 * NT * QP * 32 * 8;
+  static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4;
+  static constexpr size_t SMEM = Q_BYTES + MERGE_BYTES;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8x8 matrix of 16-bit elements (lane l holds row l / 4, columns 2 (l % 4) and + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// (x & 0x000F000F) as a pair of bfloat16 u - 8: 0x4300 is 128, whose last bit counts 1.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(r) : "r"(x));
+  const uint32_t off = 0xC308C308u;  // -136
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(off));
+  return r;
+}
+
+// N words from global memory, each used once by this block.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
+  static_assert(N == 1 || N == 2 || N % 4 == 0, "vector loads");
+  if constexpr (N == 1) {
+    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "l"(static_cast<const char*>(p) + 4 * i));
+  }
+}
+
+// A sequence's share of the line of tiles: heads_kv * row tiles * key tiles.  A row
+// tile has one tile at least, so that rows that see nothing are written too.
+struct SeqWork {
+  Kv4Seq s;
+  int row_tiles, key_tiles;
+};
+template <int R, int KT>
+__device__ __forceinline__ SeqWork seq_work(const Kv4Args& a, int b) {
+  SeqWork w;
+  w.s = kv4_seq(a, b);
+  w.row_tiles = (int)(((long long)w.s.n * a.group + R - 1) / R);
+  w.key_tiles = max(1, (w.s.len + (KT - 1)) / KT);
+  return w;
+}
+
+// The block whose stretch holds tile x of `total` tiles cut over n <= total blocks
+// (block i: i * total / n up to (i + 1) * total / n).
+__device__ __forceinline__ int owner(long long x, long long total, long long n) {
+  return (int)(((x + 1) * n - 1) / total);
+}
+
+// Inclusive prefix sums over the block's threads.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sums[w];
+    all += warp_sums[w];
+  }
+  *total = all;
+  return v + before;
+}
+
+// This block's stretch [*tile, *tile_end) of the line, the sequence that holds its
+// first tile and the first of that sequence's tiles.  The line has as many
+// stretches as there are blocks, or tiles where those are fewer: none is empty.
+// False for a block without a stretch.
+template <int R, int KT>
+__device__ __forceinline__ bool find_stretch(const Kv4Args& a, long long* tile, long long* tile_end, int* seq,
+                                             long long* first) {
+  __shared__ long long warp_sums[kWarps];
+  __shared__ long long found_first;
+  __shared__ int found_seq;
+  long long all = 0;
+  const bool one_pass = a.batch <= kThreads;
+  long long mine = 0, incl = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    mine = 0;
+    if (b < a.batch) {
+      const SeqWork w = seq_work<R, KT>(a, b);
+      mine = (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+    }
+    long long sum;
+    incl = block_scan(mine, warp_sums, &sum);
+    all += sum;
+  }
+  const long long n = min(all, (long long)gridDim.x);
+  if (blockIdx.x >= n) return false;
+  const long long want = blockIdx.x * all / n;
+  *tile = want;
+  *tile_end = (blockIdx.x + 1) * all / n;
+  long long before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    if (!one_pass) {
+      mine = 0;
+      if (b < a.batch) {
+        const SeqWork w = seq_work<R, KT>(a, b);
+        mine = (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+      }
+      long long sum;
+      incl = block_scan(mine, warp_sums, &sum) + before;
+      before += sum;
+    }
+    if (b < a.batch && want < incl && want >= incl - mine) {
+      found_seq = b;
+      found_first = incl - mine;
+    }
+  }
+  __syncthreads();
+  *seq = found_seq;
+  *first = found_first;
+  return true;
+}
+
+// Where a row tile's query rows lie: row r of the tile is query row r0 + r of the
+// (sequence, KV head), token (r0 + r) / group, head h * group + (r0 + r) % group.
+struct RowPlace {
+  int token, head;
+};
+__device__ __forceinline__ RowPlace row_place(const Kv4Args& a, int h, int row) {
+  RowPlace p;
+  p.token = row / a.group;
+  p.head = h * a.group + (row - p.token * a.group);
+  return p;
+}
+__device__ __forceinline__ long long x_row(const Kv4Args& a, const Kv4Seq& s, int b, RowPlace p) {
+  return (a.cu ? (s.row0 + p.token) * a.x_ss : b * a.x_sb + p.token * a.x_ss) + p.head * a.x_sh;
+}
+__device__ __forceinline__ long long y_row(const Kv4Args& a, const Kv4Seq& s, int b, RowPlace p) {
+  return (a.cu ? (s.row0 + p.token) * a.y_ss : b * a.y_sb + p.token * a.y_ss) + p.head * a.y_sh;
+}
+__device__ __forceinline__ long long lse_row(const Kv4Args& a, const Kv4Seq& s, int b, RowPlace p) {
+  return a.cu ? (long long)p.head * a.total + s.row0 + p.token
+              : ((long long)b * a.heads_q + p.head) * a.seqlen + p.token;
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y);
+}
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+
+// One row's log of the sum: m in log2 units.  A row that saw nothing has l = 0.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// The quarter of a row tile's accumulators that warp w of a block joins and stores:
+// accumulator e of tile j = (g, mt, nt) stands for row nt * 8 + 2 t + e % 2 and
+// value 64 g + 8 (lane / 4) + 2 mt + e / 2 of the head.
+template <class T, int NT>
+__device__ __forceinline__ void store_tile(const Kv4Args& a, const Kv4Seq& s, int b, int h, int r0, int rows, int j,
+                                           const float (&acc)[4], const float (&l)[2], int lane) {
+  const int nt = j % NT, mt = j / NT % 4, g = j / NT / 4;
+  const int d = g * kKv4Group + (lane >> 2) * 8 + 2 * mt;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int row = r0 + nt * 8 + 2 * (lane & 3) + e;
+    if (row < rows) {
+      const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
+      T* y = static_cast<T*>(a.y) + y_row(a, s, b, row_place(a, h, row)) + d;
+      store2(y, acc[e] * inv, acc[2 + e] * inv);
+    }
+  }
+}
+
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCKS))
+    k_kv4_attn(const __grid_constant__ AttnArgs args) {
+  constexpr bool F32 = sizeof(T) == 4;
+  using S = Shape<D, NT, F32>;
+  constexpr int G = S::G, R = S::R, CH = S::CH, KT = S::KT, QP = S::QP, PP = S::PP;
+  const Kv4Args& a = args.a;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint2* qfrag = reinterpret_cast<uint2*>(smem);  // [g][s][part][nt][lane] (b0, b1)
+  float* merge = reinterpret_cast<float*>(smem + S::Q_BYTES);
+  __shared__ float row_f[R], row_z[G][R];
+  __shared__ int row_lim[R];
+  __shared__ float warp_m[kWarps][R], warp_l[kWarps][R];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
+  long long tile, tile_end, first;
+  int b;
+  if (!find_stretch<R, KT>(a, &tile, &tile_end, &b, &first)) return;
+  SeqWork w = seq_work<R, KT>(a, b);
+
+  // a lane's own place in a key's row: K words 2 t, 2 t + 1 of every group, V word g8
+  const uint8_t* kc = a.kc + g8 * (D / 2) + t4 * (8 * G);
+  const uint8_t* vc = a.vc + 2 * t4 * (D / 2) + g8 * (4 * G);
+  const uint32_t* ks = a.ks + g8 * G;
+  const uint32_t* vs = a.vs + g8 * G;
+
+  while (tile < tile_end) {
+    // skip to the sequence that holds the tile
+    while (tile - first >= (long long)a.heads_kv * w.row_tiles * w.key_tiles) {
+      if (b + 1 >= a.batch) return;  // lengths that changed under the kernel
+      first += (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+      w = seq_work<R, KT>(a, ++b);
+    }
+    const int in_seq = (int)((tile - first) / w.key_tiles);  // (head, row tile)
+    const int t0 = (int)(tile - first - (long long)in_seq * w.key_tiles);
+    const int t1 = (int)min((long long)w.key_tiles, t0 + (tile_end - tile));
+    const int h = in_seq / w.row_tiles, r0 = (in_seq - h * w.row_tiles) * R;
+    const int rows = w.s.n * a.group;  // of the (sequence, KV head)
+    tile += t1 - t0;
+
+    // ---- Q: each row's power of two, group sums and operands
+    __syncthreads();  // the last row tile's are no longer read
+    for (int r = warp; r < R; r += kWarps) {
+      constexpr int E = D / 32;
+      float q[E];
+      const int row = r0 + r;
+      const RowPlace pl = row_place(a, h, row);
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] = 0.f;
+      if (row < rows) {
+        const T* p = static_cast<const T*>(a.x) + x_row(a, w.s, b, pl) + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[e] = to_f32(p[e]);
+      }
+      float big = 0.f, sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(q[e])), sum += q[e];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+#pragma unroll
+      for (int o = 32 / G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      int ex = 0;  // |q| < 2^ex: scaled below 2^14
+      if (big > 0.f && big < INFINITY) frexpf(big, &ex);
+      ex -= 14;
+      if (lane % (32 / G) == 0) row_z[lane / (32 / G)][r] = ldexpf(sum, -(24 + ex));
+      if (lane == 0) {
+        row_f[r] = ldexpf(a.scale_log2, 24 + ex);
+        const int pos = w.s.len - w.s.n + pl.token;
+        row_lim[r] = row >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : w.s.len;
+      }
+      __half* qh = reinterpret_cast<__half*>(qfrag);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int d = lane * E + e, g = d / 64, i = d % 64 / 8, n = d % 8;
+        const int st = (i & 1) * 2 + (n & 3) / 2, reg = n & 1, half = n >> 2;
+        float v = ldexpf(q[e], reg ? -ex - 4 : -ex);
+#pragma unroll
+        for (int part = 0; part < QP; ++part) {
+          const __half hv = __float2half_rn(v);
+          v -= __half2float(hv);
+          qh[(((((g * 4 + st) * QP + part) * NT + r / 8) * 32 + (r & 7) * 4 + i / 2) * 2 + reg) * 2 + half] = hv;
+        }
+      }
+    }
+    __syncthreads();
+    int klen = 0, all_see = kNoRow;  // keys that any row sees; that all rows see
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      klen = max(klen, row_lim[r] == kNoRow ? 0 : row_lim[r]);
+      all_see = min(all_see, row_lim[r]);
+    }
+
+    uint32_t qr[S::QSMEM ? 1 : G * 4][QP][NT][2];
+    if constexpr (!S::QSMEM) {
+#pragma unroll
+      for (int x = 0; x < G * 4; ++x)
+#pragma unroll
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 v = qfrag[((x * QP + part) * NT + nt) * 32 + lane];
+            qr[x][part][nt][0] = v.x, qr[x][part][nt][1] = v.y;
+          }
+    }
+    float rf[NT][2], rz[G][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rf[nt][e] = row_f[nt * 8 + 2 * t4 + e];
+#pragma unroll
+        for (int g = 0; g < G; ++g) rz[g][nt][e] = row_z[g][nt * 8 + 2 * t4 + e];
+      }
+
+    float acc[G][4][NT][4], accb[G][NT][2], m[NT][2], mu[NT][2], l[NT][2];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[g][mt][nt][e] = 0.f;
+        accb[g][nt][0] = accb[g][nt][1] = 0.f;
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, mu[nt][e] = l[nt][e] = 0.f;
+
+    // ---- keys
+    uint32_t kw[CH][2][2 * G], ksw[CH][2][G], vw[CH][4][G], vsw[CH][2][G];
+    const int* table = a.table + b * a.table_stride;
+    int pid[CH];
+    long long row[CH], next_row[CH];
+    // the page of a chunk of 16 keys; -2: no row sees the chunk
+    auto load_ids = [&](int t) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int k0 = t * KT + (warp * CH + c) * 16;
+        pid[c] = t < t1 && k0 < klen ? table[div_by(k0, args.page_div)] : -2;
+      }
+    };
+    auto rows_of = [&](int t) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int k0 = t * KT + (warp * CH + c) * 16;
+        const bool ok = pid[c] >= 0 && pid[c] < a.n_pages;
+        if (!ok && pid[c] != -2) set_status(a.status, kStatusBounds);
+        next_row[c] = ok ? ((long long)pid[c] * a.heads_kv + h) * a.page + (k0 - div_by(k0, args.page_div) * a.page) : -1;
+      }
+    };
+    auto load_k = [&]() {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (next_row[c] >= 0) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            load_words(kw[c][x], kc + next_row[c] * (D / 2) + x * 8 * (D / 2));
+            load_words(ksw[c][x], ks + next_row[c] * G + x * 8 * G);
+          }
+        }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (row[c] >= 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            load_words(vw[c][x], vc + row[c] * (D / 2) + ((x >> 1) * 8 + (x & 1)) * (D / 2));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) load_words(vsw[c][x], vs + row[c] * G + x * 8 * G);
+        }
+    };
+    load_ids(t0);
+    rows_of(t0);
+    load_k();
+#pragma unroll
+    for (int c = 0; c < CH; ++c) row[c] = next_row[c];
+    load_v();
+    load_ids(t0 + 1);
+
+    for (int t = t0; t < t1; ++t) {
+      const int k0 = t * KT + warp * CH * 16;
+      if (k0 >= klen) break;  // nor does any later tile hold keys for this warp
+      // S^T, in log2 units
+      float x[CH][NT][4];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[c][nt][e] = 0.f;
+        if (row[c] < 0) continue;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float sc[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            const uint32_t wa = kw[c][0][(st >> 1) * G + g] >> (8 * (st & 1));
+            const uint32_t wb = kw[c][1][(st >> 1) * G + g] >> (8 * (st & 1));
+#pragma unroll
+            for (int part = 0; part < QP; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t b0, b1;
+                if constexpr (S::QSMEM) {
+                  const uint2 v = qfrag[(((g * 4 + st) * QP + part) * NT + nt) * 32 + lane];
+                  b0 = v.x, b1 = v.y;
+                } else {
+                  b0 = qr[g * 4 + st][part][nt][0], b1 = qr[g * 4 + st][part][nt][1];
+                }
+                mma_f16(sc[nt], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, b0, b1);
+              }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float s = bf16_lo(ksw[c][y][g]), z = fmaf(-8.f, s, bf16_hi(ksw[c][y][g]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                x[c][nt][2 * y + e] = fmaf(s, sc[nt][2 * y + e], fmaf(z, rz[g][nt][e], x[c][nt][2 * y + e]));
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[c][nt][e] *= rf[nt][e & 1];
+      }
+      // K's registers are free: the next tile's loads
+      rows_of(t + 1);
+      load_k();
+
+      // keys that not all rows see: by their places
+      if (k0 + CH * 16 > all_see || row[0] < 0 || row[CH - 1] < 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int key = k0 + c * 16 + y * 8 + g8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (row[c] < 0 || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
+            if (row[c] < 0 || key >= w.s.len) {  // what no position holds may be anything: not into the sums
+#pragma unroll
+              for (int g = 0; g < G; ++g) vsw[c][y][g] = 0;
+            }
+          }
+      }
+      // running maximum: raised only when a score is above it by more than 2^8
+      bool over = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) v = fmaxf(v, fmaxf(x[c][nt][e], x[c][nt][2 + e]));
+          top[nt][e] = v;
+          over |= v > m[nt][e] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = top[nt][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            v = fmaxf(v, m[nt][e]);
+            const float nu = v == -INFINITY ? 0.f : v;
+            const float f = fast_exp2(mu[nt][e] - nu);  // nothing summed yet: any finite factor will do
+            const float ff = m[nt][e] == -INFINITY ? 1.f : f;
+            m[nt][e] = v;
+            mu[nt][e] = nu;
+            l[nt][e] *= ff;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              accb[g][nt][e] *= ff;
+#pragma unroll
+              for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] *= ff, acc[g][mt][nt][2 + e] *= ff;
+            }
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[c][nt][e] = fast_exp2(x[c][nt][e] - mu[nt][e & 1]);
+            l[nt][e & 1] += x[c][nt][e];
+          }
+
+      // O^T += V^T (p s), and the offsets' sums
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (row[c] < 0) continue;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          uint32_t pb[PP][NT][2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float s = bf16_lo(vsw[c][y][g]), o = bf16_hi(vsw[c][y][g]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float p0 = x[c][nt][2 * y] * s, p1 = x[c][nt][2 * y + 1] * s;
+              accb[g][nt][0] = fmaf(x[c][nt][2 * y], o, accb[g][nt][0]);
+              accb[g][nt][1] = fmaf(x[c][nt][2 * y + 1], o, accb[g][nt][1]);
+#pragma unroll
+              for (int part = 0; part < PP; ++part) {
+                const uint32_t v = pack_bf16(p0, p1);
+                pb[part][nt][y] = transpose8(v);
+                if (part + 1 < PP) p0 -= bf16_lo(v), p1 -= bf16_hi(v);
+              }
+            }
+          }
+          // keys 2 t and 2 t + 1 (2 t + 8 and + 9) side by side, values 0 .. 3 and 4 .. 7 of the word
+          uint32_t va[2][2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            va[y][0] = __byte_perm(vw[c][2 * y][g], vw[c][2 * y + 1][g], 0x5410);
+            va[y][1] = __byte_perm(vw[c][2 * y][g], vw[c][2 * y + 1][g], 0x7632);
+          }
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            uint32_t av[4];
+            const int half = mt >> 1, sh = (mt & 1) * 8;
+            av[0] = codes_bf16(va[0][half] >> sh);
+            av[1] = codes_bf16(va[0][half] >> (sh + 4));
+            av[2] = codes_bf16(va[1][half] >> sh);
+            av[3] = codes_bf16(va[1][half] >> (sh + 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int part = 0; part < PP; ++part) mma_bf16(acc[g][mt][nt], av, pb[part][nt][0], pb[part][nt][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) row[c] = next_row[c];
+      load_v();
+      load_ids(t + 2);
+    }
+
+    // ---- the warps' results joined
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+#pragma unroll
+          for (int g = 0; g < G; ++g) accb[g][nt][e] += __shfl_xor_sync(0xffffffffu, accb[g][nt][e], o);
+        }
+        if (g8 == 0) {
+          warp_m[warp][nt * 8 + 2 * t4 + e] = m[nt][e];
+          warp_l[warp][nt * 8 + 2 * t4 + e] = l[nt][e];
+        }
+      }
+    __syncthreads();
+    float rm[NT][2], rl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t4 + e;
+        float v = warp_m[0][r];
+#pragma unroll
+        for (int y = 1; y < kWarps; ++y) v = fmaxf(v, warp_m[y][r]);
+        rm[nt][e] = v;
+        const float u = v == -INFINITY ? 0.f : v;
+        rl[nt][e] = 0.f;
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y)
+          rl[nt][e] += warp_m[y][r] == -INFINITY ? warp_l[y][r] : warp_l[y][r] * fast_exp2(warp_m[y][r] - u);
+        const float f = m[nt][e] == -INFINITY ? 1.f : fast_exp2(m[nt][e] - u);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            acc[g][mt][nt][e] = (acc[g][mt][nt][e] + accb[g][nt][e]) * f;
+            acc[g][mt][nt][2 + e] = (acc[g][mt][nt][2 + e] + accb[g][nt][e]) * f;
+          }
+      }
+#pragma unroll
+    for (int j = 0; j < G * 4 * NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        merge[(warp * S::ACC + j * 4 + e) * 32 + lane] = acc[j / NT / 4][j / NT % 4][j % NT][e];
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == w.key_tiles;
+    const long long slot = blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int jj = 0; jj < G * NT; ++jj) {
+      const int j = warp * G * NT + jj;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = 0.f;
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) v[e] += merge[(y * S::ACC + j * 4 + e) * 32 + lane];
+      }
+      if (whole) {
+        store_tile<T, NT>(a, w.s, b, h, r0, rows, j, v, rl[j % NT], lane);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) args.part_o[(slot * S::ACC + j * 4 + e) * 32 + lane] = v[e];
+      }
+    }
+    if (warp == 0 && g8 == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * t4 + e;
+          if (whole) {
+            if (r0 + r < rows) a.lse[lse_row(a, w.s, b, row_place(a, h, r0 + r))] = row_lse(rm[nt][e], rl[nt][e]);
+          } else {
+            args.part_ml[(slot * R + r) * 2] = rm[nt][e];
+            args.part_ml[(slot * R + r) * 2 + 1] = rl[nt][e];
+          }
+        }
+    }
+  }
+}
+
+// Joins the parts of row tiles whose keys several blocks shared, in the blocks'
+// order.  One block for a (sequence, KV head, row tile) and a quarter of its
+// accumulators: each warp takes every fourth part.
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ AttnArgs args, int n_blocks,
+                                                       int max_row_tiles) {
+  using S = Shape<D, NT, sizeof(T) == 4>;
+  constexpr int R = S::R, KT = S::KT, G = S::G;
+  const Kv4Args& a = args.a;
+  __shared__ long long warp_sums[kWarps];
+  __shared__ float sm[kWarps][G * NT * 4][32], sml[kWarps][NT][2][32], smm[kWarps][NT][2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t4 = lane & 3;
+  const int rt = blockIdx.x % max_row_tiles, h = blockIdx.x / max_row_tiles % a.heads_kv;
+  const int b = blockIdx.x / max_row_tiles / a.heads_kv, quarter = blockIdx.y;
+  // tiles before this sequence, and all of them
+  long long before = 0, total = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int x = b0 + threadIdx.x;
+    long long mine = 0;
+    if (x < a.batch) {
+      const SeqWork w = seq_work<R, KT>(a, x);
+      mine = (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+    }
+    long long sum;
+    block_scan(mine, warp_sums, &sum);
+    total += sum;
+    block_scan(x < b ? mine : 0, warp_sums, &sum);
+    before += sum;
+  }
+  const SeqWork w = seq_work<R, KT>(a, b);
+  if (rt >= w.row_tiles) return;
+  const long long n = min(total, (long long)n_blocks);
+  const long long x0 = before + ((long long)h * w.row_tiles + rt) * w.key_tiles;
+  const int i0 = owner(x0, total, n), i1 = owner(x0 + w.key_tiles - 1, total, n);
+  if (i0 == i1) return;  // one block had all of it and stored it
+
+  float acc[G * NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int j = 0; j < G * NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+  for (int i = i0 + warp; i <= i1; i += kWarps) {
+    const long long slot = (long long)i * 2 + (i == i0 ? 1 : 0);
+    float v[G * NT][4], pm[NT][2], pl[NT][2];
+#pragma unroll
+    for (int j = 0; j < G * NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[j][e] = __ldcg(&args.part_o[(slot * S::ACC + (quarter * G * NT + j) * 4 + e) * 32 + lane]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.part_ml + (slot * R + nt * 8 + 2 * t4 + e) * 2));
+        pm[nt][e] = ml.x, pl[nt][e] = ml.y;
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float top = fmaxf(m[nt][e], pm[nt][e]), u = top == -INFINITY ? 0.f : top;
+        const float f = m[nt][e] == -INFINITY ? 1.f : fast_exp2(m[nt][e] - u);
+        const float fp = pm[nt][e] == -INFINITY ? 1.f : fast_exp2(pm[nt][e] - u);
+        m[nt][e] = top;
+        l[nt][e] = l[nt][e] * f + pl[nt][e] * fp;
+#pragma unroll
+        for (int j = nt; j < G * NT; j += NT) {
+          acc[j][e] = acc[j][e] * f + v[j][e] * fp;
+          acc[j][2 + e] = acc[j][2 + e] * f + v[j][2 + e] * fp;
+        }
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < G * NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sm[warp][j * 4 + e][lane] = acc[j][e];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) smm[warp][nt][e][lane] = m[nt][e], sml[warp][nt][e][lane] = l[nt][e];
+  __syncthreads();
+  float f[NT][2][kWarps];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) top = fmaxf(top, smm[y][nt][e][lane]);
+      const float u = top == -INFINITY ? 0.f : top;
+      m[nt][e] = top;
+      l[nt][e] = 0.f;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) {
+        f[nt][e][y] = smm[y][nt][e][lane] == -INFINITY ? 1.f : fast_exp2(smm[y][nt][e][lane] - u);
+        l[nt][e] += sml[y][nt][e][lane] * f[nt][e][y];
+      }
+    }
+  const int rows = w.s.n * a.group, r0 = rt * R;
+#pragma unroll
+  for (int j = 0; j < G * NT; ++j) {
+    if (j % kWarps != warp) continue;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = 0.f;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) v[e] += sm[y][j * 4 + e][lane] * f[j % NT][e & 1][y];
+    }
+    store_tile<T, NT>(a, w.s, b, h, r0, rows, quarter * G * NT + j, v, l[j % NT], lane);
+  }
+  if (quarter == 0 && warp == 0 && lane < 4) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = r0 + nt * 8 + 2 * t4 + e;
+        if (row < rows) a.lse[lse_row(a, w.s, b, row_place(a, h, row))] = row_lse(m[nt][e], l[nt][e]);
+      }
+  }
+}
+
+template <class T, int D, int NT>
+struct Launch {
+  using S = Shape<D, NT, sizeof(T) == 4>;
+  // Blocks: no more than there can be tiles.
+  static int grid(const Kv4Args& a) {
+    const long long row_tiles = ((long long)a.seqlen * a.group + S::R - 1) / S::R;
+    const long long key_tiles = std::max(1ll, ((long long)a.max_pages * a.page + S::KT - 1) / S::KT);
+    const long long most = (long long)a.batch * a.heads_kv * row_tiles;
+    return (int)(most >= S::GRID ? S::GRID : std::min<long long>(S::GRID, most * std::min(key_tiles, (long long)S::GRID)));
+  }
+  static size_t o_bytes(const Kv4Args& a) { return (size_t)grid(a) * 2 * S::ACC * 32 * 4; }
+  static size_t workspace(const Kv4Args& a) { return o_bytes(a) + (size_t)grid(a) * 2 * S::R * 8; }
+  static cudaError_t run(const Kv4Args& a, void* ws, cudaStream_t st) {
+    AttnArgs args;
+    args.a = a;
+    args.page_div = fast_div(a.page);
+    args.part_o = static_cast<float*>(ws);
+    args.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + o_bytes(a));
+    cudaError_t e = cudaFuncSetAttribute(k_kv4_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    if (e != cudaSuccess) return e;
+    const int n = grid(a);
+    k_kv4_attn<T, D, NT><<<n, kThreads, S::SMEM, st>>>(args);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((long long)a.max_pages * a.page <= S::KT) return cudaSuccess;  // a row tile has one tile of keys
+    const long long row_tiles = ((long long)a.seqlen * a.group + S::R - 1) / S::R;
+    const long long blocks = (long long)a.batch * a.heads_kv * row_tiles;
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    k_kv4_join<T, D, NT><<<dim3((unsigned)blocks, 4), kThreads, 0, st>>>(args, n, (int)row_tiles);
+    return cudaGetLastError();
+  }
+};
+
+// Row tiles of 8, 16 or 32 queries: the least that hold all of a KV head's, else the
+// widest that the registers hold (accumulators: D / 16 * 4 a lane and 8 queries).
+template <class T, int D, class F>
+auto with_width(const Kv4Args& a, F&& f) {
+  const long long rows = (long long)a.seqlen * a.group;
+  if (rows <= 8) return f(Launch<T, D, 1>());
+  if (rows <= 16 || D == 256 || sizeof(T) == 4) return f(Launch<T, D, 2>());
+  return f(Launch<T, D, D == 256 || sizeof(T) == 4 ? 2 : 4>());
+}
+template <class F>
+auto with_shape(const Kv4Args& a, int head_dim, bool bf16, F&& f) {
+  if (bf16) {
+    if (head_dim == 64) return with_width<__nv_bfloat16, 64>(a, f);
+    if (head_dim == 128) return with_width<__nv_bfloat16, 128>(a, f);
+    return with_width<__nv_bfloat16, 256>(a, f);
+  }
+  if (head_dim == 64) return with_width<float, 64>(a, f);
+  if (head_dim == 128) return with_width<float, 128>(a, f);
+  return with_width<float, 256>(a, f);
 }
 
 }  // namespace
 
-size_t kv4_attn_workspace(const Kv4Args&, int, bool) { return 0; }
+size_t kv4_attn_workspace(const Kv4Args& a, int head_dim, bool bf16) {
+  return with_shape(a, head_dim, bf16, [&](auto k) { return decltype(k)::workspace(a); });
+}
 
-cudaError_t launch_kv4_attn(const Kv4Args& a, int head_dim, bool bf16, void*, cudaStream_t st) {
-  if (bf16) {
-    if (head_dim == 64) return launch<__nv_bfloat16, 64>(a, st);
-    if (head_dim == 128) return launch<__nv_bfloat16, 128>(a, st);
-    return launch<__nv_bfloat16, 256>(a, st);
-  }
-  if (head_dim == 64) return launch<float, 64>(a, st);
-  if (head_dim == 128) return launch<float, 128>(a, st);
-  return launch<float, 256>(a, st);
+cudaError_t launch_kv4_attn(const Kv4Args& a, int head_dim, bool bf16, void* workspace, cudaStream_t st) {
+  return with_shape(a, head_dim, bf16, [&](auto k) { return decltype(k)::run(a, workspace, st); });
 }
 
 }  // namespace gbattn
