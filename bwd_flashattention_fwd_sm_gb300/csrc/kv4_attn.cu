@@ -13,10 +13,13 @@
 //      row scaled by its own power of two (two parts for float32 queries), those of
 //      the second kind of pair by 1/16 more.  With s, b a key's step and offset of a
 //      group, its part of the score is s sum(q u) + (b - 8 s) sum(q), in float32.
-//   V: codes as bfloat16 integers -8 .. 7 (128 + u by bit operations, minus 136, both
-//      exact).  The weights p s are rounded to bfloat16, whose range holds them whatever
-//      the steps are (float32 queries: three parts, 24 bits); the offsets' part
-//      sum(p b) stays in float32.
+//   V: the same pairs, two keys side by side.  The weights p s are float16 too, in units
+//      of a power of two that follows the largest step seen, so that the largest is below
+//      2^15: 11 bits down to 2^-29 of that, and off by at most 2^-40 of it below
+//      (float32 queries: two parts, 22 bits).  Sums of u instead of u - 8 would cancel
+//      against 8 sum(p s) over long contexts, so a ninth product counts -8 sum(p s)
+//      beside them and is folded in every 128 keys; the offsets' part sum(p b) stays in
+//      float32.
 //
 // Work.  A tile is the keys that a block's warps take at a time; the tiles of all
 // sequences, KV heads and row tiles stand in one line that is cut into equal
@@ -49,7 +52,13 @@ __device__ __forceinline__ int div_by(int n, FastDiv d) {
   return (int)(((unsigned long long)(uint32_t)n * d.mul) >> d.shift);
 }
 
+constexpr uint32_t kNone = 0xFFFFFFFFu;  // no row of the cache
+constexpr int kLeastUnit = -119;  // 2^(7 - unit) is a float32
 constexpr int kNoRow = 0x7FFFFFFF;  // the limit of a column without a query: it masks nothing
+
+// What a row tile costs beside its keys (queries into operands, the warps' results
+// joined), in tiles: the line has that many empty places before a row tile's keys.
+constexpr int kEmpty = 3;
 
 struct AttnArgs {
   Kv4Args a;
@@ -62,30 +71,27 @@ template <int D, int NT, bool F32>
 struct Shape {
   static constexpr int G = D / kKv4Group;
   static constexpr int R = 8 * NT;                      // query rows of a row tile
-  static constexpr int CH = (D == 256 || NT == 4) ? 1 : 2;  // 16-key chunks of a warp at a time
+  static constexpr int CH = (D == 256 || NT >= 3) ? 1 : 2;  // 16-key chunks of a warp at a time
   static constexpr int KT = kWarps * CH * 16;           // keys of a tile
   static constexpr int QP = F32 ? 2 : 1;                // float16 parts of Q
-  static constexpr int PP = F32 ? 3 : 1;                // bfloat16 parts of P
+  static constexpr int PP = F32 ? 2 : 1;                // float16 parts of the weights
+  static constexpr int FOLD = 8 / CH;                   // tiles between two folds: 128 keys of a warp
   static constexpr int ACC = G * 4 * NT * 4;            // accumulators of a lane
   static constexpr int QREGS = G * 4 * NT * QP * 2;
   static constexpr bool QSMEM = QREGS > 32;             // Q operands read from shared memory each time
   static constexpr int BLOCKS = (NT == 1 && D <= 128 && !F32) ? 3 : 2;  // blocks of an SM
+  // Sums of u beside a count of -8 sum(p s): cheaper than subtracting 8 from each
+  // code while there are few columns and registers for the count.
+  static constexpr bool COUNT = NT == 1;
   static constexpr int GRID = kSms * BLOCKS;
   static constexpr size_t Q_BYTES = (size_t)G * 4 * NT * QP * 32 * 8;
   static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4;
   static constexpr size_t SMEM = Q_BYTES + MERGE_BYTES;
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -105,13 +111,43 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// (x & 0x000F000F) as a pair of bfloat16 u - 8: 0x4300 is 128, whose last bit counts 1.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
+__device__ __forceinline__ float f16_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)w)); }
+__device__ __forceinline__ float f16_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
+__device__ __forceinline__ uint32_t add_f16(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(r) : "r"(x));
-  const uint32_t off = 0xC308C308u;  // -136
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(off));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// N values of a query row.
+template <int N>
+__device__ __forceinline__ void load_q(float (&q)[N], const float* p) {
+  if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    q[0] = v.x, q[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      q[i] = v.x, q[i + 1] = v.y, q[i + 2] = v.z, q[i + 3] = v.w;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_q(float (&q)[N], const __nv_bfloat16* p) {
+  uint32_t w[N / 2];
+  if constexpr (N == 2) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) q[2 * i] = bf16_lo(w[i]), q[2 * i + 1] = bf16_hi(w[i]);
 }
 
 // N words from global memory, each used once by this block.
@@ -131,11 +167,12 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
   }
 }
 
-// A sequence's share of the line of tiles: heads_kv * row tiles * key tiles.  A row
+// A sequence's share of the line: heads_kv * row tiles * (kEmpty + key tiles).  A row
 // tile has one tile at least, so that rows that see nothing are written too.
 struct SeqWork {
   Kv4Seq s;
   int row_tiles, key_tiles;
+  __device__ __forceinline__ int places() const { return key_tiles + kEmpty; }  // of a row tile in the line
 };
 template <int R, int KT>
 __device__ __forceinline__ SeqWork seq_work(const Kv4Args& a, int b) {
@@ -191,7 +228,7 @@ __device__ __forceinline__ bool find_stretch(const Kv4Args& a, long long* tile, 
     mine = 0;
     if (b < a.batch) {
       const SeqWork w = seq_work<R, KT>(a, b);
-      mine = (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+      mine = (long long)a.heads_kv * w.row_tiles * w.places();
     }
     long long sum;
     incl = block_scan(mine, warp_sums, &sum);
@@ -209,7 +246,7 @@ __device__ __forceinline__ bool find_stretch(const Kv4Args& a, long long* tile, 
       mine = 0;
       if (b < a.batch) {
         const SeqWork w = seq_work<R, KT>(a, b);
-        mine = (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+        mine = (long long)a.heads_kv * w.row_tiles * w.places();
       }
       long long sum;
       incl = block_scan(mine, warp_sums, &sum) + before;
@@ -295,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   int b;
   if (!find_stretch<R, KT>(a, &tile, &tile_end, &b, &first)) return;
   SeqWork w = seq_work<R, KT>(a, b);
+  const float q_sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
 
   // a lane's own place in a key's row: K words 2 t, 2 t + 1 of every group, V word g8
   const uint8_t* kc = a.kc + g8 * (D / 2) + t4 * (8 * G);
@@ -304,113 +342,31 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 
   while (tile < tile_end) {
     // skip to the sequence that holds the tile
-    while (tile - first >= (long long)a.heads_kv * w.row_tiles * w.key_tiles) {
+    while (tile - first >= (long long)a.heads_kv * w.row_tiles * w.places()) {
       if (b + 1 >= a.batch) return;  // lengths that changed under the kernel
-      first += (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+      first += (long long)a.heads_kv * w.row_tiles * w.places();
       w = seq_work<R, KT>(a, ++b);
     }
-    const int in_seq = (int)((tile - first) / w.key_tiles);  // (head, row tile)
-    const int t0 = (int)(tile - first - (long long)in_seq * w.key_tiles);
-    const int t1 = (int)min((long long)w.key_tiles, t0 + (tile_end - tile));
+    const int in_seq = (int)((tile - first) / w.places());  // (head, row tile)
+    const int at = (int)(tile - first - (long long)in_seq * w.places());
+    const int t0 = max(at - kEmpty, 0), t1 = (int)min((long long)w.key_tiles, at - kEmpty + (tile_end - tile));
     const int h = in_seq / w.row_tiles, r0 = (in_seq - h * w.row_tiles) * R;
     const int rows = w.s.n * a.group;  // of the (sequence, KV head)
-    tile += t1 - t0;
-
-    // ---- Q: each row's power of two, group sums and operands
-    __syncthreads();  // the last row tile's are no longer read
-    for (int r = warp; r < R; r += kWarps) {
-      constexpr int E = D / 32;
-      float q[E];
-      const int row = r0 + r;
-      const RowPlace pl = row_place(a, h, row);
-#pragma unroll
-      for (int e = 0; e < E; ++e) q[e] = 0.f;
-      if (row < rows) {
-        const T* p = static_cast<const T*>(a.x) + x_row(a, w.s, b, pl) + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = to_f32(p[e]);
-      }
-      float big = 0.f, sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(q[e])), sum += q[e];
-#pragma unroll
-      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-#pragma unroll
-      for (int o = 32 / G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      int ex = 0;  // |q| < 2^ex: scaled below 2^14
-      if (big > 0.f && big < INFINITY) frexpf(big, &ex);
-      ex -= 14;
-      if (lane % (32 / G) == 0) row_z[lane / (32 / G)][r] = ldexpf(sum, -(24 + ex));
-      if (lane == 0) {
-        row_f[r] = ldexpf(a.scale_log2, 24 + ex);
-        const int pos = w.s.len - w.s.n + pl.token;
-        row_lim[r] = row >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : w.s.len;
-      }
-      __half* qh = reinterpret_cast<__half*>(qfrag);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e, g = d / 64, i = d % 64 / 8, n = d % 8;
-        const int st = (i & 1) * 2 + (n & 3) / 2, reg = n & 1, half = n >> 2;
-        float v = ldexpf(q[e], reg ? -ex - 4 : -ex);
-#pragma unroll
-        for (int part = 0; part < QP; ++part) {
-          const __half hv = __float2half_rn(v);
-          v -= __half2float(hv);
-          qh[(((((g * 4 + st) * QP + part) * NT + r / 8) * 32 + (r & 7) * 4 + i / 2) * 2 + reg) * 2 + half] = hv;
-        }
-      }
-    }
-    __syncthreads();
-    int klen = 0, all_see = kNoRow;  // keys that any row sees; that all rows see
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      klen = max(klen, row_lim[r] == kNoRow ? 0 : row_lim[r]);
-      all_see = min(all_see, row_lim[r]);
+    tile += w.places() - at;
+    if (t1 <= 0) break;  // the stretch ends before the row tile's keys
+    // keys that any of the tile's rows sees, and that all of them see
+    int klen, all_see;
+    {
+      const int low = w.s.len - w.s.n + r0 / a.group, high = w.s.len - w.s.n + (min(r0 + R, rows) - 1) / a.group;
+      klen = high < 0 ? 0 : a.causal ? high + 1 : w.s.len;
+      all_see = low < 0 ? 0 : a.causal ? low + 1 : w.s.len;
     }
 
-    uint32_t qr[S::QSMEM ? 1 : G * 4][QP][NT][2];
-    if constexpr (!S::QSMEM) {
-#pragma unroll
-      for (int x = 0; x < G * 4; ++x)
-#pragma unroll
-        for (int part = 0; part < QP; ++part)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 v = qfrag[((x * QP + part) * NT + nt) * 32 + lane];
-            qr[x][part][nt][0] = v.x, qr[x][part][nt][1] = v.y;
-          }
-    }
-    float rf[NT][2], rz[G][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        rf[nt][e] = row_f[nt * 8 + 2 * t4 + e];
-#pragma unroll
-        for (int g = 0; g < G; ++g) rz[g][nt][e] = row_z[g][nt * 8 + 2 * t4 + e];
-      }
-
-    float acc[G][4][NT][4], accb[G][NT][2], m[NT][2], mu[NT][2], l[NT][2];
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[g][mt][nt][e] = 0.f;
-        accb[g][nt][0] = accb[g][nt][1] = 0.f;
-      }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, mu[nt][e] = l[nt][e] = 0.f;
-
-    // ---- keys
+    // ---- keys: where they lie, and the first loads
     uint32_t kw[CH][2][2 * G], ksw[CH][2][G], vw[CH][4][G], vsw[CH][2][G];
     const int* table = a.table + b * a.table_stride;
     int pid[CH];
-    long long row[CH], next_row[CH];
+    uint32_t row[CH], next_row[CH];
     // the page of a chunk of 16 keys; -2: no row sees the chunk
     auto load_ids = [&](int t) {
 #pragma unroll
@@ -425,29 +381,32 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         const int k0 = t * KT + (warp * CH + c) * 16;
         const bool ok = pid[c] >= 0 && pid[c] < a.n_pages;
         if (!ok && pid[c] != -2) set_status(a.status, kStatusBounds);
-        next_row[c] = ok ? ((long long)pid[c] * a.heads_kv + h) * a.page + (k0 - div_by(k0, args.page_div) * a.page) : -1;
+        next_row[c] = ok ? ((uint32_t)pid[c] * a.heads_kv + h) * a.page + (k0 - div_by(k0, args.page_div) * a.page) : kNone;
       }
     };
     auto load_k = [&]() {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        if (next_row[c] >= 0) {
+        if (next_row[c] != kNone) {
+          const uint8_t* k = kc + (unsigned long long)next_row[c] * (D / 2);
+          const uint32_t* sc = ks + (unsigned long long)next_row[c] * G;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            load_words(kw[c][x], kc + next_row[c] * (D / 2) + x * 8 * (D / 2));
-            load_words(ksw[c][x], ks + next_row[c] * G + x * 8 * G);
+            load_words(kw[c][x], k + x * 8 * (D / 2));
+            load_words(ksw[c][x], sc + x * 8 * G);
           }
         }
     };
     auto load_v = [&]() {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        if (row[c] >= 0) {
+        if (row[c] != kNone) {
+          const uint8_t* v = vc + (unsigned long long)row[c] * (D / 2);
+          const uint32_t* sc = vs + (unsigned long long)row[c] * G;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            load_words(vw[c][x], vc + row[c] * (D / 2) + ((x >> 1) * 8 + (x & 1)) * (D / 2));
+          for (int x = 0; x < 4; ++x) load_words(vw[c][x], v + ((x >> 1) * 8 + (x & 1)) * (D / 2));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) load_words(vsw[c][x], vs + row[c] * G + x * 8 * G);
+          for (int x = 0; x < 2; ++x) load_words(vsw[c][x], sc + x * 8 * G);
         }
     };
     load_ids(t0);
@@ -458,10 +417,123 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     load_v();
     load_ids(t0 + 1);
 
+    // ---- Q: each row's power of two, group sums and operands
+    __syncthreads();  // the last row tile's are no longer read
+    constexpr int E = D / 32;
+    float q[R / kWarps][E];
+#pragma unroll
+    for (int y = 0; y < R / kWarps; ++y)
+      if (r0 + y * kWarps + warp < rows)
+        load_q(q[y], static_cast<const T*>(a.x) + x_row(a, w.s, b, row_place(a, h, r0 + y * kWarps + warp)) + lane * E);
+#pragma unroll
+    for (int y = 0; y < R / kWarps; ++y) {
+      const int r = y * kWarps + warp;
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[y][e] = r0 + r < rows ? q[y][e] * q_sign : 0.f;
+      float big = 0.f, sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(q[y][e])), sum += q[y][e];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+#pragma unroll
+      for (int o = 32 / G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      int ex = 0;  // |q| < 2^ex: scaled below 2^14
+      if (big > 0.f && big < INFINITY) frexpf(big, &ex);
+      ex -= 14;
+      if (lane % (32 / G) == 0) row_z[lane / (32 / G)][r] = ldexpf(sum, -(24 + ex));
+      if (lane == 0) {
+        // at least 2^-126, at most the largest float32: scores of 0 times it stay 0
+        row_f[r] = a.scale_log2 != 0.f
+                       ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), 24 + ex), 1.17549435e-38f), 3.40282347e38f)
+                       : 1.f;
+        const int pos = w.s.len - w.s.n + (r0 + r) / a.group;
+        row_lim[r] = r0 + r >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : w.s.len;
+      }
+      __half* qh = reinterpret_cast<__half*>(qfrag);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int d = lane * E + e, g = d / 64, i = d % 64 / 8, n = d % 8;
+        const int st = (i & 1) * 2 + (n & 3) / 2, reg = n & 1, half = n >> 2;
+        float v = ldexpf(q[y][e], reg ? -ex - 4 : -ex);
+#pragma unroll
+        for (int part = 0; part < QP; ++part) {
+          const __half hv = __float2half_rn(v);
+          v -= __half2float(hv);
+          qh[(((((g * 4 + st) * QP + part) * NT + r / 8) * 32 + (r & 7) * 4 + i / 2) * 2 + reg) * 2 + half] = hv;
+        }
+      }
+    }
+    __syncthreads();
+
+    uint32_t qr[S::QSMEM ? 1 : G * 4][QP][NT][2];
+    if constexpr (!S::QSMEM) {
+#pragma unroll
+      for (int x = 0; x < G * 4; ++x)
+#pragma unroll
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 v = qfrag[((x * QP + part) * NT + nt) * 32 + lane];
+            qr[x][part][nt][0] = v.x, qr[x][part][nt][1] = v.y;
+          }
+    }
+    float rf[NT][2], rz[G][NT][2];
+    if constexpr (!S::QSMEM) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          rf[nt][e] = row_f[nt * 8 + 2 * t4 + e];
+#pragma unroll
+          for (int g = 0; g < G; ++g) rz[g][nt][e] = row_z[g][nt * 8 + 2 * t4 + e];
+        }
+    }
+
+    // sums in units of 2^(unit[g] - 7 - 24) (values 0, 2, 4, 6 of a word) and 2^4 of it (1, 3, 5, 7);
+    // minus[g]: -8 sum(p s) since it was last folded in
+    float acc[G][4][NT][4], minus[S::COUNT ? G : 1][NT][4], accb[G][NT][2], bar[NT][2], mu[NT][2], l[NT][2];
+    int unit[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      unit[g] = kLeastUnit;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (S::COUNT) minus[g][nt][e] = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] = 0.f;
+        }
+        accb[g][nt][0] = accb[g][nt][1] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) bar[nt][e] = -INFINITY, mu[nt][e] = l[nt][e] = 0.f;
+    auto fold = [&]() {
+      if constexpr (S::COUNT) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int mt = 0; mt < 4; ++mt) {
+                acc[g][mt][nt][e] += minus[g][nt][e];
+                acc[g][mt][nt][2 + e] = fmaf(16.f, minus[g][nt][e], acc[g][mt][nt][2 + e]);
+              }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) minus[g][nt][e] = 0.f;
+          }
+      }
+    };
+
     for (int t = t0; t < t1; ++t) {
       const int k0 = t * KT + warp * CH * 16;
       if (k0 >= klen) break;  // nor does any later tile hold keys for this warp
-      // S^T, in log2 units
+      // S^T, in units of 1 / rf
       float x[CH][NT][4];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -469,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[c][nt][e] = 0.f;
-        if (row[c] < 0) continue;
+        if (row[c] == kNone) continue;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           float sc[NT][4];
@@ -481,18 +553,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           for (int st = 0; st < 4; ++st) {
             const uint32_t wa = kw[c][0][(st >> 1) * G + g] >> (8 * (st & 1));
             const uint32_t wb = kw[c][1][(st >> 1) * G + g] >> (8 * (st & 1));
+            const uint32_t ak[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
 #pragma unroll
             for (int part = 0; part < QP; ++part)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                uint32_t b0, b1;
                 if constexpr (S::QSMEM) {
                   const uint2 v = qfrag[(((g * 4 + st) * QP + part) * NT + nt) * 32 + lane];
-                  b0 = v.x, b1 = v.y;
+                  mma_f16(sc[nt], ak, v.x, v.y);
                 } else {
-                  b0 = qr[g * 4 + st][part][nt][0], b1 = qr[g * 4 + st][part][nt][1];
+                  mma_f16(sc[nt], ak, qr[g * 4 + st][part][nt][0], qr[g * 4 + st][part][nt][1]);
                 }
-                mma_f16(sc[nt], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, b0, b1);
               }
           }
 #pragma unroll
@@ -501,21 +572,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                x[c][nt][2 * y + e] = fmaf(s, sc[nt][2 * y + e], fmaf(z, rz[g][nt][e], x[c][nt][2 * y + e]));
+              for (int e = 0; e < 2; ++e) {
+                const float sum = S::QSMEM ? row_z[g][nt * 8 + 2 * t4 + e] : rz[g][nt][e];
+                x[c][nt][2 * y + e] = fmaf(s, sc[nt][2 * y + e], fmaf(z, sum, x[c][nt][2 * y + e]));
+              }
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[c][nt][e] *= rf[nt][e & 1];
       }
       // K's registers are free: the next tile's loads
       rows_of(t + 1);
       load_k();
 
       // keys that not all rows see: by their places
-      if (k0 + CH * 16 > all_see || row[0] < 0 || row[CH - 1] < 0) {
+      if (k0 + CH * 16 > all_see || row[0] == kNone || row[CH - 1] == kNone) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -525,46 +594,71 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (row[c] < 0 || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
-            if (row[c] < 0 || key >= w.s.len) {  // what no position holds may be anything: not into the sums
+                if (row[c] == kNone || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
+            if (row[c] == kNone || key >= w.s.len) {  // what no position holds may be anything: not into the sums
 #pragma unroll
               for (int g = 0; g < G; ++g) vsw[c][y][g] = 0;
             }
           }
       }
-      // running maximum: raised only when a score is above it by more than 2^8
+      // The running maximum is raised only when a score is above it by more than 2^8,
+      // the unit only when a step is above it.
+      float high[NT][2], step[G];
       bool over = false;
-      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = -INFINITY;
+          float v = fmaxf(x[0][nt][e], x[0][nt][2 + e]);
 #pragma unroll
-          for (int c = 0; c < CH; ++c) v = fmaxf(v, fmaxf(x[c][nt][e], x[c][nt][2 + e]));
-          top[nt][e] = v;
-          over |= v > m[nt][e] + 8.f;
+          for (int c = 1; c < CH; ++c) v = fmax3f(v, x[c][nt][e], x[c][nt][2 + e]);
+          high[nt][e] = v;
+          over |= v > bar[nt][e];
         }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float v = fmaxf(bf16_lo(vsw[0][0][g]), bf16_lo(vsw[0][1][g]));
+#pragma unroll
+        for (int c = 1; c < CH; ++c) v = fmax3f(v, bf16_lo(vsw[c][0][g]), bf16_lo(vsw[c][1][g]));
+        step[g] = v;
+        over |= v > pow2(unit[g]);
+      }
       if (__any_sync(0xffffffffu, over)) {
+        float fg[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float v = step[g];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          const int nu = max(unit[g], min((int)(__float_as_uint(v) >> 23) - 126, 127));  // v < 2^nu
+          fg[g] = unit[g] - nu < -126 ? 0.f : pow2(unit[g] - nu);
+          unit[g] = nu;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = top[nt][e];
+            float v = high[nt][e];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            v = fmaxf(v, m[nt][e]);
-            const float nu = v == -INFINITY ? 0.f : v;
-            const float f = fast_exp2(mu[nt][e] - nu);  // nothing summed yet: any finite factor will do
-            const float ff = m[nt][e] == -INFINITY ? 1.f : f;
-            m[nt][e] = v;
-            mu[nt][e] = nu;
-            l[nt][e] *= ff;
+            float f = 1.f;
+            if (v > -INFINITY) {
+              const float r = S::QSMEM ? row_f[nt * 8 + 2 * t4 + e] : rf[nt][e];
+              v *= r;
+              if (bar[nt][e] > -INFINITY) {
+                v = fmaxf(v, mu[nt][e]);
+                f = fast_exp2(mu[nt][e] - v);
+              }
+              mu[nt][e] = v;
+              bar[nt][e] = (v + 8.f) / r;
+            }
+            l[nt][e] *= f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              accb[g][nt][e] *= ff;
+              accb[g][nt][e] *= f;
+              if constexpr (S::COUNT) minus[g][nt][e] *= f * fg[g];
 #pragma unroll
-              for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] *= ff, acc[g][mt][nt][2 + e] *= ff;
+              for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] *= f * fg[g], acc[g][mt][nt][2 + e] *= f * fg[g];
             }
           }
       }
@@ -574,20 +668,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[c][nt][e] = fast_exp2(x[c][nt][e] - mu[nt][e & 1]);
+            x[c][nt][e] = fast_exp2(fmaf(x[c][nt][e], S::QSMEM ? row_f[nt * 8 + 2 * t4 + (e & 1)] : rf[nt][e & 1],
+                                         -mu[nt][e & 1]));
             l[nt][e & 1] += x[c][nt][e];
           }
 
       // O^T += V^T (p s), and the offsets' sums
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        if (row[c] < 0) continue;
+        if (row[c] == kNone) continue;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           uint32_t pb[PP][NT][2];
+          const float per_unit = pow2(7 - unit[g]);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float s = bf16_lo(vsw[c][y][g]), o = bf16_hi(vsw[c][y][g]);
+            const float s = bf16_lo(vsw[c][y][g]) * per_unit, o = bf16_hi(vsw[c][y][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float p0 = x[c][nt][2 * y] * s, p1 = x[c][nt][2 * y + 1] * s;
@@ -595,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
               accb[g][nt][1] = fmaf(x[c][nt][2 * y + 1], o, accb[g][nt][1]);
 #pragma unroll
               for (int part = 0; part < PP; ++part) {
-                const uint32_t v = pack_bf16(p0, p1);
+                const uint32_t v = pack_f16(p0, p1);
                 pb[part][nt][y] = transpose8(v);
-                if (part + 1 < PP) p0 -= bf16_lo(v), p1 -= bf16_hi(v);
+                if (part + 1 < PP) p0 -= f16_lo(v), p1 -= f16_hi(v);
               }
             }
           }
@@ -608,18 +704,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             va[y][0] = __byte_perm(vw[c][2 * y][g], vw[c][2 * y + 1][g], 0x5410);
             va[y][1] = __byte_perm(vw[c][2 * y][g], vw[c][2 * y + 1][g], 0x7632);
           }
+          if constexpr (S::COUNT) {
+            const uint32_t eight[4] = {0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u};  // -8 2^-24
+#pragma unroll
+            for (int part = 0; part < PP; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(minus[g][nt], eight, pb[part][nt][0], pb[part][nt][1]);
+          }
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            uint32_t av[4];
-            const int half = mt >> 1, sh = (mt & 1) * 8;
-            av[0] = codes_bf16(va[0][half] >> sh);
-            av[1] = codes_bf16(va[0][half] >> (sh + 4));
-            av[2] = codes_bf16(va[1][half] >> sh);
-            av[3] = codes_bf16(va[1][half] >> (sh + 4));
+            const uint32_t a0 = va[0][mt >> 1] >> (8 * (mt & 1)), a1 = va[1][mt >> 1] >> (8 * (mt & 1));
+            uint32_t av[4] = {a0 & 0x000F000Fu, a0 & 0x00F000F0u, a1 & 0x000F000Fu, a1 & 0x00F000F0u};
+            if constexpr (!S::COUNT) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+              for (int e = 0; e < 4; ++e) av[e] = add_f16(av[e], (e & 1) ? 0x80808080u : 0x80088008u);  // -8: exact
+            }
 #pragma unroll
-              for (int part = 0; part < PP; ++part) mma_bf16(acc[g][mt][nt], av, pb[part][nt][0], pb[part][nt][1]);
+            for (int part = 0; part < PP; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[g][mt][nt], av, pb[part][nt][0], pb[part][nt][1]);
           }
         }
       }
@@ -627,19 +730,34 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
       for (int c = 0; c < CH; ++c) row[c] = next_row[c];
       load_v();
       load_ids(t + 2);
+      if ((t - t0) % S::FOLD == S::FOLD - 1) fold();
     }
+    fold();
+    // to the values' own units, the offsets' part added
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) accb[g][nt][e] += __shfl_xor_sync(0xffffffffu, accb[g][nt][e], o);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p17f, pow2(unit[g]), accb[g][nt][e]);
+            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p13f, pow2(unit[g]), accb[g][nt][e]);
+          }
+        }
 
     // ---- the warps' results joined
+    float m[NT][2];  // in log2 units
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        m[nt][e] = bar[nt][e] == -INFINITY ? -INFINITY : mu[nt][e];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
-#pragma unroll
-          for (int g = 0; g < G; ++g) accb[g][nt][e] += __shfl_xor_sync(0xffffffffu, accb[g][nt][e], o);
-        }
+        for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
         if (g8 == 0) {
           warp_m[warp][nt * 8 + 2 * t4 + e] = m[nt][e];
           warp_l[warp][nt * 8 + 2 * t4 + e] = l[nt][e];
@@ -665,10 +783,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            acc[g][mt][nt][e] = (acc[g][mt][nt][e] + accb[g][nt][e]) * f;
-            acc[g][mt][nt][2 + e] = (acc[g][mt][nt][2 + e] + accb[g][nt][e]) * f;
-          }
+          for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] *= f, acc[g][mt][nt][2 + e] *= f;
       }
 #pragma unroll
     for (int j = 0; j < G * 4 * NT; ++j)
@@ -733,7 +848,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ A
     long long mine = 0;
     if (x < a.batch) {
       const SeqWork w = seq_work<R, KT>(a, x);
-      mine = (long long)a.heads_kv * w.row_tiles * w.key_tiles;
+      mine = (long long)a.heads_kv * w.row_tiles * w.places();
     }
     long long sum;
     block_scan(mine, warp_sums, &sum);
@@ -744,7 +859,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ A
   const SeqWork w = seq_work<R, KT>(a, b);
   if (rt >= w.row_tiles) return;
   const long long n = min(total, (long long)n_blocks);
-  const long long x0 = before + ((long long)h * w.row_tiles + rt) * w.key_tiles;
+  const long long x0 = before + ((long long)h * w.row_tiles + rt) * w.places() + kEmpty;
   const int i0 = owner(x0, total, n), i1 = owner(x0 + w.key_tiles - 1, total, n);
   if (i0 == i1) return;  // one block had all of it and stored it
 
@@ -868,14 +983,16 @@ struct Launch {
   }
 };
 
-// Row tiles of 8, 16 or 32 queries: the least that hold all of a KV head's, else the
+// Row tiles of 8, 16, 24 or 32 queries: the least that hold all of a KV head's, else the
 // widest that the registers hold (accumulators: D / 16 * 4 a lane and 8 queries).
 template <class T, int D, class F>
 auto with_width(const Kv4Args& a, F&& f) {
+  constexpr int kMost = D == 256 || sizeof(T) == 4 ? 2 : 4;
   const long long rows = (long long)a.seqlen * a.group;
   if (rows <= 8) return f(Launch<T, D, 1>());
-  if (rows <= 16 || D == 256 || sizeof(T) == 4) return f(Launch<T, D, 2>());
-  return f(Launch<T, D, D == 256 || sizeof(T) == 4 ? 2 : 4>());
+  if (rows <= 16 || kMost == 2) return f(Launch<T, D, 2>());
+  if (rows <= 24) return f(Launch<T, D, kMost == 2 ? 2 : 3>());
+  return f(Launch<T, D, kMost>());
 }
 template <class F>
 auto with_shape(const Kv4Args& a, int head_dim, bool bf16, F&& f) {

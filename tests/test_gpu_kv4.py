@@ -9,9 +9,12 @@ is a float32 sum of D / 64 group sums of 64 products plus offsets: off by at mos
 (D + 16) eps W with W = scale sum |q| (16 s + |b|); exp2's approximation adds 2^-21
 and sums over n positions n eps.  So each p is off by d = (D + 16) eps W + n eps +
 2^-21 of itself, O by at most 2 d A (numerator and sum) with A = sum p (|s (u - 8)| +
-|b|), LSE by d + 4 eps |LSE|.  bfloat16: the weights p s are rounded once to bf16 (2^-8
-of themselves at most, the part R = sum p |s (u - 8)| of O), and O once (2^-8 |O|).
-float32: the weights are taken in three bf16 parts (2^-24), and O is rounded by eps |O|.
+|b|), LSE by d + 4 eps |LSE|.  The weights p s are float16 in units of 2^e / 2^7, 2^(e - 1)
+<= the largest step s of the head: off by 2^-11 of themselves (float32: two parts, 2^-23),
+and below float16's normal range by half its least step, 2^-25 units <= 2^-31 of the
+largest s.  With |u - 8| <= 8 and sum p >= 1 in the units that the maximum sets: 2^-11
+R (2^-23 R), R = sum p |s (u - 8)|, and n 2^-28 max s.  O is rounded once: 2^-8 |O| for
+bfloat16, eps |O| for float32.
 """
 
 import numpy as np
@@ -82,7 +85,9 @@ def check_attend(c, q, o, lse, scale, causal, dtype, name):
         empty = np.isneginf(rl)
         assert np.all(go[empty] == 0)
         tol = 2 * d[..., None] * A
-        tol += 2.0 ** -8 * (R * (1 + 2.0 ** -8) + np.abs(ro)) if dtype == "bf16" else EPS * (R + np.abs(ro))
+        tol += 2.0 ** -11 * R + 2.0 ** -8 * np.abs(ro) * (1 + 2.0 ** -8) if dtype == "bf16" else 2 * EPS * (R + np.abs(ro))
+        if c.lens[n]:
+            tol += c.lens[n] * 2.0 ** -28 * np.repeat(vu[1].max((1, 2)), go.shape[0] // c.Hkv)[:, None, None]
         err = np.abs(go - ro)
         lerr = np.abs(np.where(empty, 0, gl) - np.where(empty, 0, rl))[~empty]
         ltol = (d + 4 * EPS * np.abs(np.where(empty, 0, rl)))[~empty]
