@@ -52,7 +52,6 @@ __device__ __forceinline__ int div_by(int n, FastDiv d) {
   return (int)(((unsigned long long)(uint32_t)n * d.mul) >> d.shift);
 }
 
-constexpr uint32_t kNone = 0xFFFFFFFFu;  // no row of the cache
 constexpr int kLeastUnit = -119;  // 2^(7 - unit) is a float32
 constexpr int kNoRow = 0x7FFFFFFF;  // the limit of a column without a query: it masks nothing
 
@@ -65,6 +64,9 @@ struct AttnArgs {
   FastDiv page_div;
   float* part_o;   // [blocks][2][row tile's accumulators]
   float* part_ml;  // [blocks][2][rows][2]: row maximum (log2 units) and sum
+  // [blocks]: the row tile whose keys begin in the block's stretch and end in block
+  // w's: (sequence, KV head, row tile, w); w = -1: there is none
+  int4* shared;
 };
 
 template <int D, int NT, bool F32>
@@ -213,10 +215,10 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 // This block's stretch [*tile, *tile_end) of the line, the sequence that holds its
 // first tile and the first of that sequence's tiles.  The line has as many
 // stretches as there are blocks, or tiles where those are fewer: none is empty.
-// False for a block without a stretch.
+// Returns the number of stretches, 0 to a block that has none; *total: the line's places.
 template <int R, int KT>
-__device__ __forceinline__ bool find_stretch(const Kv4Args& a, long long* tile, long long* tile_end, int* seq,
-                                             long long* first) {
+__device__ __forceinline__ long long find_stretch(const Kv4Args& a, long long* tile, long long* tile_end, long long* total,
+                                                  int* seq, long long* first) {
   __shared__ long long warp_sums[kWarps];
   __shared__ long long found_first;
   __shared__ int found_seq;
@@ -235,7 +237,8 @@ __device__ __forceinline__ bool find_stretch(const Kv4Args& a, long long* tile, 
     all += sum;
   }
   const long long n = min(all, (long long)gridDim.x);
-  if (blockIdx.x >= n) return false;
+  if (blockIdx.x >= n) return 0;
+  *total = all;
   const long long want = blockIdx.x * all / n;
   *tile = want;
   *tile_end = (blockIdx.x + 1) * all / n;
@@ -260,7 +263,7 @@ __device__ __forceinline__ bool find_stretch(const Kv4Args& a, long long* tile, 
   __syncthreads();
   *seq = found_seq;
   *first = found_first;
-  return true;
+  return n;
 }
 
 // Where a row tile's query rows lie: row r of the tile is query row r0 + r of the
@@ -294,8 +297,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// The quarter of a row tile's accumulators that warp w of a block joins and stores:
-// accumulator e of tile j = (g, mt, nt) stands for row nt * 8 + 2 t + e % 2 and
+// Stores a 16 by 8 tile of a row tile's accumulators: accumulator e of tile j = (g, mt, nt) stands for row nt * 8 + 2 t + e % 2 and
 // value 64 g + 8 (lane / 4) + 2 mt + e / 2 of the head.
 template <class T, int NT>
 __device__ __forceinline__ void store_tile(const Kv4Args& a, const Kv4Seq& s, int b, int h, int r0, int rows, int j,
@@ -327,18 +329,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   __shared__ int row_lim[R];
   __shared__ float warp_m[kWarps][R], warp_l[kWarps][R];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
-  long long tile, tile_end, first;
+  // the warp's number by a shuffle: what follows from it alone is computed once a warp
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int g8 = lane >> 2, t4 = lane & 3;
+  long long tile, tile_end, total, first;
   int b;
-  if (!find_stretch<R, KT>(a, &tile, &tile_end, &b, &first)) return;
+  const long long n = find_stretch<R, KT>(a, &tile, &tile_end, &total, &b, &first);
+  if (threadIdx.x == 0) args.shared[blockIdx.x] = make_int4(0, 0, 0, -1);
+  if (n == 0) return;
   SeqWork w = seq_work<R, KT>(a, b);
   const float q_sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
 
   // a lane's own place in a key's row: K words 2 t, 2 t + 1 of every group, V word g8
-  const uint8_t* kc = a.kc + g8 * (D / 2) + t4 * (8 * G);
-  const uint8_t* vc = a.vc + 2 * t4 * (D / 2) + g8 * (4 * G);
-  const uint32_t* ks = a.ks + g8 * G;
-  const uint32_t* vs = a.vs + g8 * G;
+  const uint32_t k_lane = g8 * (D / 2) + t4 * (8 * G), v_lane = 2 * t4 * (D / 2) + g8 * (4 * G), s_lane = g8 * G * 4;
 
   while (tile < tile_end) {
     // skip to the sequence that holds the tile
@@ -363,59 +366,71 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     }
 
     // ---- keys: where they lie, and the first loads
+    // This warp's tiles end where no row sees its keys; a cache without a page shows none.
+    if (a.n_pages == 0 && klen > 0) {
+      set_status(a.status, kStatusBounds);
+      klen = 0;
+    }
+    const int te = klen > warp * CH * 16 ? min(t1, (klen - warp * CH * 16 + KT - 1) / KT) : 0;
     uint32_t kw[CH][2][2 * G], ksw[CH][2][G], vw[CH][4][G], vsw[CH][2][G];
     const int* table = a.table + b * a.table_stride;
-    int pid[CH];
-    uint32_t row[CH], next_row[CH];
-    // the page of a chunk of 16 keys; -2: no row sees the chunk
+    // A chunk is 16 keys, in one page.  One whose page is none, or that no row sees, is
+    // `dead`: a row of the cache that does exist is loaded in its place, and masked.
+    int pid[CH], off[CH];
+    uint32_t row[CH];
+    unsigned dead = 0, next_dead = 0;  // a bit a chunk
+    bool bad = false, next_bad = false;
     auto load_ids = [&](int t) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int k0 = t * KT + (warp * CH + c) * 16;
-        pid[c] = t < t1 && k0 < klen ? table[div_by(k0, args.page_div)] : -2;
+        const int k0 = min(t * KT + (warp * CH + c) * 16, (klen - 1) & ~15), pg = div_by(k0, args.page_div);
+        off[c] = k0 - pg * a.page;
+        pid[c] = table[pg];
       }
     };
     auto rows_of = [&](int t) {
+      next_dead = 0;
+      next_bad = false;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int k0 = t * KT + (warp * CH + c) * 16;
-        const bool ok = pid[c] >= 0 && pid[c] < a.n_pages;
-        if (!ok && pid[c] != -2) set_status(a.status, kStatusBounds);
-        next_row[c] = ok ? ((uint32_t)pid[c] * a.heads_kv + h) * a.page + (k0 - div_by(k0, args.page_div) * a.page) : kNone;
+        const int id = __shfl_sync(0xffffffffu, pid[c], 0);
+        const bool ok = (unsigned)id < (unsigned)a.n_pages;
+        next_bad |= !ok;
+        if (!ok || t * KT + (warp * CH + c) * 16 >= klen) next_dead |= 1u << c;
+        row[c] = ((uint32_t)(ok ? id : 0) * a.heads_kv + h) * a.page + off[c];
       }
     };
     auto load_k = [&]() {
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (next_row[c] != kNone) {
-          const uint8_t* k = kc + (unsigned long long)next_row[c] * (D / 2);
-          const uint32_t* sc = ks + (unsigned long long)next_row[c] * G;
+      for (int c = 0; c < CH; ++c) {
+        const uint8_t* k = a.kc + (unsigned long long)row[c] * (D / 2);
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(a.ks) + (unsigned long long)row[c] * (4 * G);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            load_words(kw[c][x], k + x * 8 * (D / 2));
-            load_words(ksw[c][x], sc + x * 8 * G);
-          }
+        for (int x = 0; x < 2; ++x) {
+          load_words(kw[c][x], k + k_lane + x * 8 * (D / 2));
+          load_words(ksw[c][x], sc + s_lane + x * 8 * G * 4);
         }
+      }
     };
     auto load_v = [&]() {
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (row[c] != kNone) {
-          const uint8_t* v = vc + (unsigned long long)row[c] * (D / 2);
-          const uint32_t* sc = vs + (unsigned long long)row[c] * G;
+      for (int c = 0; c < CH; ++c) {
+        const uint8_t* v = a.vc + (unsigned long long)row[c] * (D / 2);
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(a.vs) + (unsigned long long)row[c] * (4 * G);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) load_words(vw[c][x], v + ((x >> 1) * 8 + (x & 1)) * (D / 2));
+        for (int x = 0; x < 4; ++x) load_words(vw[c][x], v + v_lane + ((x >> 1) * 8 + (x & 1)) * (D / 2));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) load_words(vsw[c][x], sc + x * 8 * G);
-        }
+        for (int x = 0; x < 2; ++x) load_words(vsw[c][x], sc + s_lane + x * 8 * G * 4);
+      }
     };
-    load_ids(t0);
-    rows_of(t0);
-    load_k();
-#pragma unroll
-    for (int c = 0; c < CH; ++c) row[c] = next_row[c];
-    load_v();
-    load_ids(t0 + 1);
+    if (t0 < te) {
+      load_ids(t0);
+      rows_of(t0);
+      load_k();
+      load_v();
+      dead = next_dead, bad = next_bad;
+      load_ids(t0 + 1);
+    }
 
     // ---- Q: each row's power of two, group sums and operands
     __syncthreads();  // the last row tile's are no longer read
@@ -493,9 +508,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     // minus[g]: -8 sum(p s) since it was last folded in
     float acc[G][4][NT][4], minus[S::COUNT ? G : 1][NT][4], accb[G][NT][2], bar[NT][2], mu[NT][2], l[NT][2];
     int unit[G];
+    float cap[G], per_unit[G];  // 2^unit, 2^(7 - unit)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       unit[g] = kLeastUnit;
+      cap[g] = pow2(kLeastUnit);
+      per_unit[g] = pow2(7 - kLeastUnit);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -530,9 +548,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
       }
     };
 
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0; t < te; ++t) {
       const int k0 = t * KT + warp * CH * 16;
-      if (k0 >= klen) break;  // nor does any later tile hold keys for this warp
       // S^T, in units of 1 / rf
       float x[CH][NT][4];
 #pragma unroll
@@ -541,7 +558,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[c][nt][e] = 0.f;
-        if (row[c] == kNone) continue;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           float sc[NT][4];
@@ -580,11 +596,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         }
       }
       // K's registers are free: the next tile's loads
-      rows_of(t + 1);
-      load_k();
+      if (t + 1 < te) {
+        rows_of(t + 1);
+        load_k();
+      }
 
       // keys that not all rows see: by their places
-      if (k0 + CH * 16 > all_see || row[0] == kNone || row[CH - 1] == kNone) {
+      if (k0 + CH * 16 > all_see || bad) {
+        if (bad) set_status(a.status, kStatusBounds);
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -594,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (row[c] == kNone || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
-            if (row[c] == kNone || key >= w.s.len) {  // what no position holds may be anything: not into the sums
+                if ((dead >> c & 1) || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
+            if ((dead >> c & 1) || key >= w.s.len) {  // what no position holds may be anything: not into the sums
 #pragma unroll
               for (int g = 0; g < G; ++g) vsw[c][y][g] = 0;
             }
@@ -621,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
         for (int c = 1; c < CH; ++c) v = fmax3f(v, bf16_lo(vsw[c][0][g]), bf16_lo(vsw[c][1][g]));
         step[g] = v;
-        over |= v > pow2(unit[g]);
+        over |= v > cap[g];
       }
       if (__any_sync(0xffffffffu, over)) {
         float fg[G];
@@ -633,6 +652,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           const int nu = max(unit[g], min((int)(__float_as_uint(v) >> 23) - 126, 127));  // v < 2^nu
           fg[g] = unit[g] - nu < -126 ? 0.f : pow2(unit[g] - nu);
           unit[g] = nu;
+          cap[g] = pow2(nu);
+          per_unit[g] = pow2(7 - nu);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -676,14 +697,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
       // O^T += V^T (p s), and the offsets' sums
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        if (row[c] == kNone) continue;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           uint32_t pb[PP][NT][2];
-          const float per_unit = pow2(7 - unit[g]);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float s = bf16_lo(vsw[c][y][g]) * per_unit, o = bf16_hi(vsw[c][y][g]);
+            const float s = bf16_lo(vsw[c][y][g]) * per_unit[g], o = bf16_hi(vsw[c][y][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float p0 = x[c][nt][2 * y] * s, p1 = x[c][nt][2 * y + 1] * s;
@@ -726,10 +745,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           }
         }
       }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) row[c] = next_row[c];
-      load_v();
-      load_ids(t + 2);
+      if (t + 1 < te) {
+        load_v();
+        load_ids(t + 2);
+      }
+      dead = next_dead, bad = next_bad;
       if ((t - t0) % S::FOLD == S::FOLD - 1) fold();
     }
     fold();
@@ -744,8 +764,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           for (int o = 4; o < 32; o <<= 1) accb[g][nt][e] += __shfl_xor_sync(0xffffffffu, accb[g][nt][e], o);
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p17f, pow2(unit[g]), accb[g][nt][e]);
-            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p13f, pow2(unit[g]), accb[g][nt][e]);
+            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p17f, cap[g], accb[g][nt][e]);
+            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p13f, cap[g], accb[g][nt][e]);
           }
         }
 
@@ -792,6 +812,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         merge[(warp * S::ACC + j * 4 + e) * 32 + lane] = acc[j / NT / 4][j / NT % 4][j % NT][e];
     __syncthreads();
     const bool whole = t0 == 0 && t1 == w.key_tiles;
+    if (t0 == 0 && !whole && threadIdx.x == 0) {
+      const long long last = first + (long long)(in_seq + 1) * w.places() - 1;
+      args.shared[blockIdx.x] = make_int4(b, h, r0 / R, (int)owner(last, total, n));
+    }
     const long long slot = blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
 #pragma unroll
     for (int jj = 0; jj < G * NT; ++jj) {
@@ -827,127 +851,73 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   }
 }
 
-// Joins the parts of row tiles whose keys several blocks shared, in the blocks'
-// order.  One block for a (sequence, KV head, row tile) and a quarter of its
-// accumulators: each warp takes every fourth part.
+// Joins the parts of row tiles whose keys several blocks shared, in a fixed order: a
+// block for each 16 by 8 tile of a row tile's accumulators, a warp for every eighth
+// part, four parts' loads at a time.
+constexpr int kJoinWarps = 8;
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ AttnArgs args, int n_blocks,
-                                                       int max_row_tiles) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const __grid_constant__ AttnArgs args) {
   using S = Shape<D, NT, sizeof(T) == 4>;
-  constexpr int R = S::R, KT = S::KT, G = S::G;
+  constexpr int R = S::R, kAhead = 4;
   const Kv4Args& a = args.a;
-  __shared__ long long warp_sums[kWarps];
-  __shared__ float sm[kWarps][G * NT * 4][32], sml[kWarps][NT][2][32], smm[kWarps][NT][2][32];
+  __shared__ float sm[kJoinWarps][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t4 = lane & 3;
-  const int rt = blockIdx.x % max_row_tiles, h = blockIdx.x / max_row_tiles % a.heads_kv;
-  const int b = blockIdx.x / max_row_tiles / a.heads_kv, quarter = blockIdx.y;
-  // tiles before this sequence, and all of them
-  long long before = 0, total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int x = b0 + threadIdx.x;
-    long long mine = 0;
-    if (x < a.batch) {
-      const SeqWork w = seq_work<R, KT>(a, x);
-      mine = (long long)a.heads_kv * w.row_tiles * w.places();
-    }
-    long long sum;
-    block_scan(mine, warp_sums, &sum);
-    total += sum;
-    block_scan(x < b ? mine : 0, warp_sums, &sum);
-    before += sum;
-  }
-  const SeqWork w = seq_work<R, KT>(a, b);
-  if (rt >= w.row_tiles) return;
-  const long long n = min(total, (long long)n_blocks);
-  const long long x0 = before + ((long long)h * w.row_tiles + rt) * w.places() + kEmpty;
-  const int i0 = owner(x0, total, n), i1 = owner(x0 + w.key_tiles - 1, total, n);
-  if (i0 == i1) return;  // one block had all of it and stored it
+  const int i0 = blockIdx.x, j = blockIdx.y, nt = j % NT;
+  const int4 tile = __ldcg(&args.shared[i0]);
+  const int b = tile.x, h = tile.y, rt = tile.z, i1 = tile.w;
+  if (i1 < 0) return;
 
-  float acc[G * NT][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int j = 0; j < G * NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-  for (int i = i0 + warp; i <= i1; i += kWarps) {
-    const long long slot = (long long)i * 2 + (i == i0 ? 1 : 0);
-    float v[G * NT][4], pm[NT][2], pl[NT][2];
-#pragma unroll
-    for (int j = 0; j < G * NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[j][e] = __ldcg(&args.part_o[(slot * S::ACC + (quarter * G * NT + j) * 4 + e) * 32 + lane]);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.part_ml + (slot * R + nt * 8 + 2 * t4 + e) * 2));
-        pm[nt][e] = ml.x, pl[nt][e] = ml.y;
-      }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float top = fmaxf(m[nt][e], pm[nt][e]), u = top == -INFINITY ? 0.f : top;
-        const float f = m[nt][e] == -INFINITY ? 1.f : fast_exp2(m[nt][e] - u);
-        const float fp = pm[nt][e] == -INFINITY ? 1.f : fast_exp2(pm[nt][e] - u);
-        m[nt][e] = top;
-        l[nt][e] = l[nt][e] * f + pl[nt][e] * fp;
-#pragma unroll
-        for (int j = nt; j < G * NT; j += NT) {
-          acc[j][e] = acc[j][e] * f + v[j][e] * fp;
-          acc[j][2 + e] = acc[j][2 + e] * f + v[j][2 + e] * fp;
-        }
-      }
-  }
-#pragma unroll
-  for (int j = 0; j < G * NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sm[warp][j * 4 + e][lane] = acc[j][e];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) smm[warp][nt][e][lane] = m[nt][e], sml[warp][nt][e][lane] = l[nt][e];
-  __syncthreads();
-  float f[NT][2][kWarps];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  auto add = [&](const float (&v)[4], const float (&pm)[2], const float (&pl)[2]) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float top = -INFINITY;
+      const float top = fmaxf(m[e], pm[e]), u = top == -INFINITY ? 0.f : top;
+      const float f = m[e] == -INFINITY ? 1.f : fast_exp2(m[e] - u);
+      const float fp = pm[e] == -INFINITY ? 1.f : fast_exp2(pm[e] - u);
+      m[e] = top;
+      l[e] = l[e] * f + pl[e] * fp;
+      acc[e] = acc[e] * f + v[e] * fp;
+      acc[2 + e] = acc[2 + e] * f + v[2 + e] * fp;
+    }
+  };
+  for (int i = i0 + warp; i <= i1; i += kJoinWarps * kAhead) {
+    float v[kAhead][4], pm[kAhead][2], pl[kAhead][2];
 #pragma unroll
-      for (int y = 0; y < kWarps; ++y) top = fmaxf(top, smm[y][nt][e][lane]);
-      const float u = top == -INFINITY ? 0.f : top;
-      m[nt][e] = top;
-      l[nt][e] = 0.f;
+    for (int k = 0; k < kAhead; ++k) {
+      const int part = i + k * kJoinWarps;
+      if (part <= i1) {
+        const long long slot = (long long)part * 2 + (part == i0 ? 1 : 0);
 #pragma unroll
-      for (int y = 0; y < kWarps; ++y) {
-        f[nt][e][y] = smm[y][nt][e][lane] == -INFINITY ? 1.f : fast_exp2(smm[y][nt][e][lane] - u);
-        l[nt][e] += sml[y][nt][e][lane] * f[nt][e][y];
+        for (int e = 0; e < 4; ++e) v[k][e] = __ldcg(&args.part_o[(slot * S::ACC + j * 4 + e) * 32 + lane]);
+        const float4 ml = __ldcg(reinterpret_cast<const float4*>(args.part_ml + (slot * R + nt * 8 + 2 * t4) * 2));
+        pm[k][0] = ml.x, pl[k][0] = ml.y, pm[k][1] = ml.z, pl[k][1] = ml.w;
       }
     }
-  const int rows = w.s.n * a.group, r0 = rt * R;
 #pragma unroll
-  for (int j = 0; j < G * NT; ++j) {
-    if (j % kWarps != warp) continue;
-    float v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = 0.f;
-#pragma unroll
-      for (int y = 0; y < kWarps; ++y) v[e] += sm[y][j * 4 + e][lane] * f[j % NT][e & 1][y];
-    }
-    store_tile<T, NT>(a, w.s, b, h, r0, rows, quarter * G * NT + j, v, l[j % NT], lane);
+    for (int k = 0; k < kAhead; ++k)
+      if (i + k * kJoinWarps <= i1) add(v[k], pm[k], pl[k]);
   }
-  if (quarter == 0 && warp == 0 && lane < 4) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+  for (int e = 0; e < 4; ++e) sm[warp][e][lane] = acc[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = r0 + nt * 8 + 2 * t4 + e;
-        if (row < rows) a.lse[lse_row(a, w.s, b, row_place(a, h, row))] = row_lse(m[nt][e], l[nt][e]);
-      }
+  for (int e = 0; e < 2; ++e) sm[warp][4 + e][lane] = m[e], sm[warp][6 + e][lane] = l[e];
+  __syncthreads();
+  if (warp) return;
+  const Kv4Seq seq = kv4_seq(a, b);
+#pragma unroll
+  for (int y = 1; y < kJoinWarps; ++y) {
+    const float v[4] = {sm[y][0][lane], sm[y][1][lane], sm[y][2][lane], sm[y][3][lane]};
+    const float pm[2] = {sm[y][4][lane], sm[y][5][lane]}, pl[2] = {sm[y][6][lane], sm[y][7][lane]};
+    add(v, pm, pl);
+  }
+  const int rows = seq.n * a.group, r0 = rt * R;
+  store_tile<T, NT>(a, seq, b, h, r0, rows, j, acc, l, lane);
+  if (j < NT && lane < 4) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = r0 + nt * 8 + 2 * t4 + e;
+      if (row < rows) a.lse[lse_row(a, seq, b, row_place(a, h, row))] = row_lse(m[e], l[e]);
+    }
   }
 }
 
@@ -962,23 +932,22 @@ struct Launch {
     return (int)(most >= S::GRID ? S::GRID : std::min<long long>(S::GRID, most * std::min(key_tiles, (long long)S::GRID)));
   }
   static size_t o_bytes(const Kv4Args& a) { return (size_t)grid(a) * 2 * S::ACC * 32 * 4; }
-  static size_t workspace(const Kv4Args& a) { return o_bytes(a) + (size_t)grid(a) * 2 * S::R * 8; }
+  static size_t ml_bytes(const Kv4Args& a) { return (size_t)grid(a) * 2 * S::R * 8; }
+  static size_t workspace(const Kv4Args& a) { return o_bytes(a) + ml_bytes(a) + (size_t)grid(a) * sizeof(int4); }
   static cudaError_t run(const Kv4Args& a, void* ws, cudaStream_t st) {
     AttnArgs args;
     args.a = a;
     args.page_div = fast_div(a.page);
     args.part_o = static_cast<float*>(ws);
     args.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + o_bytes(a));
+    args.shared = reinterpret_cast<int4*>(static_cast<char*>(ws) + o_bytes(a) + ml_bytes(a));
     cudaError_t e = cudaFuncSetAttribute(k_kv4_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
     if (e != cudaSuccess) return e;
     const int n = grid(a);
     k_kv4_attn<T, D, NT><<<n, kThreads, S::SMEM, st>>>(args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((long long)a.max_pages * a.page <= S::KT) return cudaSuccess;  // a row tile has one tile of keys
-    const long long row_tiles = ((long long)a.seqlen * a.group + S::R - 1) / S::R;
-    const long long blocks = (long long)a.batch * a.heads_kv * row_tiles;
-    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    k_kv4_join<T, D, NT><<<dim3((unsigned)blocks, 4), kThreads, 0, st>>>(args, n, (int)row_tiles);
+    k_kv4_join<T, D, NT><<<dim3(n, S::ACC / 4), kJoinWarps * 32, 0, st>>>(args);
     return cudaGetLastError();
   }
 };
