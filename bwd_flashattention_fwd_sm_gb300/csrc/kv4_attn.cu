@@ -31,12 +31,13 @@
 #include <algorithm>
 
 #include "kv4.h"
+#include "ptx.cuh"
 
 namespace gbattn {
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32;  // each warp joins and stores a quarter of a row tile's sums
 constexpr int kSms = 152;  // a fixed count, so that the workspace size needs no device query
 
 // n / d for 0 <= n < 2^31: (n * mul) >> shift with mul = floor(2^shift / d) + 1.
@@ -57,7 +58,7 @@ constexpr int kNoRow = 0x7FFFFFFF;  // the limit of a column without a query: it
 
 // What a row tile costs beside its keys (queries into operands, the warps' results
 // joined), in tiles: the line has that many empty places before a row tile's keys.
-constexpr int kEmpty = 3;
+constexpr int kEmpty = 6;
 
 struct AttnArgs {
   Kv4Args a;
@@ -79,28 +80,34 @@ struct Shape {
   static constexpr int PP = F32 ? 2 : 1;                // float16 parts of the weights
   static constexpr int FOLD = 8 / CH;                   // tiles between two folds: 128 keys of a warp
   static constexpr int ACC = G * 4 * NT * 4;            // accumulators of a lane
-  static constexpr int QREGS = G * 4 * NT * QP * 2;
-  static constexpr bool QSMEM = QREGS > 32;             // Q operands read from shared memory each time
-  static constexpr int BLOCKS = (NT == 1 && D <= 128 && !F32) ? 3 : 2;  // blocks of an SM
+  static constexpr int BLOCKS = 2;                      // of an SM
+  static constexpr int STAGES = 3;                      // tiles in a warp's ring
+  static constexpr int CHUNK_BYTES = 16 * (D + 8 * G);  // K codes, V codes, K scales, V scales of 16 keys
+  static constexpr int STAGE_BYTES = CH * CHUNK_BYTES;
   // Sums of u beside a count of -8 sum(p s): cheaper than subtracting 8 from each
   // code while there are few columns and registers for the count.
   static constexpr bool COUNT = NT == 1;
   static constexpr int GRID = kSms * BLOCKS;
   static constexpr size_t Q_BYTES = (size_t)G * 4 * NT * QP * 32 * 8;
-  static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4;
-  static constexpr size_t SMEM = Q_BYTES + MERGE_BYTES;
+  static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4, RING_BYTES = (size_t)kWarps * STAGES * STAGE_BYTES;
+  static constexpr size_t SMEM = Q_BYTES + (MERGE_BYTES > RING_BYTES ? MERGE_BYTES : RING_BYTES);
 };
 
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+      "%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // An 8x8 matrix of 16-bit elements (lane l holds row l / 4, columns 2 (l % 4) and + 1) transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -152,21 +159,31 @@ __device__ __forceinline__ void load_q(float (&q)[N], const __nv_bfloat16* p) {
   for (int i = 0; i < N / 2; ++i) q[2 * i] = bf16_lo(w[i]), q[2 * i + 1] = bf16_hi(w[i]);
 }
 
-// N words from global memory, each used once by this block.
+// N words from shared memory.
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
   static_assert(N == 1 || N == 2 || N % 4 == 0, "vector loads");
   if constexpr (N == 1) {
-    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (N == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "l"(static_cast<const char*>(p) + 4 * i));
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
   }
+}
+// 16 bytes from global to shared memory, asynchronously; groups complete in order.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A sequence's share of the line: heads_kv * row tiles * (kEmpty + key tiles).  A row
@@ -320,18 +337,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     k_kv4_attn(const __grid_constant__ AttnArgs args) {
   constexpr bool F32 = sizeof(T) == 4;
   using S = Shape<D, NT, F32>;
-  constexpr int G = S::G, R = S::R, CH = S::CH, KT = S::KT, QP = S::QP, PP = S::PP;
+  constexpr int G = S::G, R = S::R, CH = S::CH, KT = S::KT, QP = S::QP, PP = S::PP, ST = S::STAGES;
   const Kv4Args& a = args.a;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   uint2* qfrag = reinterpret_cast<uint2*>(smem);  // [g][s][part][nt][lane] (b0, b1)
-  float* merge = reinterpret_cast<float*>(smem + S::Q_BYTES);
-  __shared__ float row_f[R], row_z[G][R];
+  float* merge = reinterpret_cast<float*>(smem + S::Q_BYTES);  // over the rings, between row tiles
+  __shared__ __align__(16) float row_f[R], row_z[G][R];  // read in pairs
   __shared__ int row_lim[R];
   __shared__ float warp_m[kWarps][R], warp_l[kWarps][R];
 
-  // the warp's number by a shuffle: what follows from it alone is computed once a warp
-  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  const int g8 = lane >> 2, t4 = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
   long long tile, tile_end, total, first;
   int b;
   const long long n = find_stretch<R, KT>(a, &tile, &tile_end, &total, &b, &first);
@@ -340,8 +355,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   SeqWork w = seq_work<R, KT>(a, b);
   const float q_sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
 
-  // a lane's own place in a key's row: K words 2 t, 2 t + 1 of every group, V word g8
-  const uint32_t k_lane = g8 * (D / 2) + t4 * (8 * G), v_lane = 2 * t4 * (D / 2) + g8 * (4 * G), s_lane = g8 * G * 4;
+  // Copies into a warp's ring, 16 bytes a lane: codes in order, and the scales of a tile by
+  // one copy (chunk lane / 8 G, K's in the first half of the 8 G lanes, V's in the second).
+  uint8_t* ring = smem + S::Q_BYTES + warp * (ST * S::STAGE_BYTES);
+  const uint8_t* k_from = a.kc + lane * 16;
+  const uint8_t* v_from = a.vc + lane * 16;
+  const uint8_t* s_from =
+      reinterpret_cast<const uint8_t*>((lane / (4 * G) & 1) ? a.vs : a.ks) + lane % (4 * G) * 16;
+  const uint32_t to = ptx::smem_u32(ring) + lane * 16;
+  const uint32_t s_to = ptx::smem_u32(ring) + lane / (8 * G) * S::CHUNK_BYTES + 16 * D + lane % (8 * G) * 16;
+  // Row r of eight keys is key r ^ (r >> 1 & 1): neighbours in K's reads and every second
+  // row in V's then lie in both halves of the shared-memory banks.
+  const int key8 = g8 ^ (g8 >> 1 & 1);
+  const uint32_t k_lane = key8 * (D / 2) + t4 * (8 * G), s_lane = 16 * D + key8 * (4 * G);
+  const uint32_t v_lane0 = 8 * D + ((2 * t4) ^ (t4 & 1)) * (D / 2) + g8 * (4 * G);
+  const uint32_t v_lane1 = 8 * D + ((2 * t4 + 1) ^ (t4 & 1)) * (D / 2) + g8 * (4 * G);
 
   while (tile < tile_end) {
     // skip to the sequence that holds the tile
@@ -372,68 +400,57 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
       klen = 0;
     }
     const int te = klen > warp * CH * 16 ? min(t1, (klen - warp * CH * 16 + KT - 1) / KT) : 0;
-    uint32_t kw[CH][2][2 * G], ksw[CH][2][G], vw[CH][4][G], vsw[CH][2][G];
+    // Chunks of 16 keys, each in one page, in batches of 8: lane 4 x knows chunk x's row of
+    // the cache.  Where the page is none, or no row sees the chunk, a row that does exist
+    // is copied in its place, and masked.
+    constexpr int kBatch = 8 / CH;  // tiles
     const int* table = a.table + b * a.table_stride;
-    // A chunk is 16 keys, in one page.  One whose page is none, or that no row sees, is
-    // `dead`: a row of the cache that does exist is loaded in its place, and masked.
-    int pid[CH], off[CH];
-    uint32_t row[CH];
-    unsigned dead = 0, next_dead = 0;  // a bit a chunk
-    bool bad = false, next_bad = false;
-    auto load_ids = [&](int t) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int k0 = min(t * KT + (warp * CH + c) * 16, (klen - 1) & ~15), pg = div_by(k0, args.page_div);
-        off[c] = k0 - pg * a.page;
-        pid[c] = table[pg];
+    const int my_step = (lane >> 2) / CH, my_chunk = (lane >> 2) % CH;
+    auto key_of = [&](int t) { return min((t + my_step) * KT + (warp * CH + my_chunk) * 16, (klen - 1) & ~15); };
+    auto id_of = [&](int t) { return table[div_by(key_of(t), args.page_div)]; };
+    bool bad = false;  // a chunk's page was none
+    auto rows_of = [&](int t, int id) {
+      const int k0 = key_of(t), pg = div_by(k0, args.page_div);
+      const bool ok = (unsigned)id < (unsigned)a.n_pages;
+      if (!__all_sync(0xffffffffu, ok)) {
+        bad = true;
+        set_status(a.status, kStatusBounds);
       }
+      return ((uint32_t)(ok ? id : 0) * a.heads_kv + h) * a.page + (k0 - pg * a.page);
     };
-    auto rows_of = [&](int t) {
-      next_dead = 0;
-      next_bad = false;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int id = __shfl_sync(0xffffffffu, pid[c], 0);
-        const bool ok = (unsigned)id < (unsigned)a.n_pages;
-        next_bad |= !ok;
-        if (!ok || t * KT + (warp * CH + c) * 16 >= klen) next_dead |= 1u << c;
-        row[c] = ((uint32_t)(ok ? id : 0) * a.heads_kv + h) * a.page + off[c];
+    uint32_t rows_now = 0;
+    int ids = 0;
+    auto issue = [&](int t) {  // tile t into its stage; tiles in order
+      const int x = (t - t0) % kBatch;
+      if (x == 0) {
+        rows_now = rows_of(t, ids);
+        ids = id_of(t + kBatch);
       }
-    };
-    auto load_k = [&]() {
+      const uint32_t stage = (uint32_t)((t - t0) % ST) * S::STAGE_BYTES;
+      uint32_t row[CH];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const uint8_t* k = a.kc + (unsigned long long)row[c] * (D / 2);
-        const uint8_t* sc = reinterpret_cast<const uint8_t*>(a.ks) + (unsigned long long)row[c] * (4 * G);
+        row[c] = __shfl_sync(0xffffffffu, rows_now, (x * CH + c) * 4);
+        const uint8_t* k = k_from + (unsigned long long)row[c] * (D / 2);
+        const uint8_t* v = v_from + (unsigned long long)row[c] * (D / 2);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          load_words(kw[c][x], k + k_lane + x * 8 * (D / 2));
-          load_words(ksw[c][x], sc + s_lane + x * 8 * G * 4);
+        for (int i = 0; i < D / 64; ++i) {
+          copy16(to + stage + c * S::CHUNK_BYTES + i * 512, k + i * 512);
+          copy16(to + stage + c * S::CHUNK_BYTES + 8 * D + i * 512, v + i * 512);
         }
       }
+      if (CH * 8 * G >= 32 || lane < CH * 8 * G)
+        copy16(s_to + stage, s_from + (unsigned long long)(CH == 2 && lane >= 8 * G ? row[CH - 1] : row[0]) * (4 * G));
     };
-    auto load_v = [&]() {
+    __syncthreads();  // nobody still reads the last row tile's operands or sums
+    if (t0 < te) ids = id_of(t0);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const uint8_t* v = a.vc + (unsigned long long)row[c] * (D / 2);
-        const uint8_t* sc = reinterpret_cast<const uint8_t*>(a.vs) + (unsigned long long)row[c] * (4 * G);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) load_words(vw[c][x], v + v_lane + ((x >> 1) * 8 + (x & 1)) * (D / 2));
-#pragma unroll
-        for (int x = 0; x < 2; ++x) load_words(vsw[c][x], sc + s_lane + x * 8 * G * 4);
-      }
-    };
-    if (t0 < te) {
-      load_ids(t0);
-      rows_of(t0);
-      load_k();
-      load_v();
-      dead = next_dead, bad = next_bad;
-      load_ids(t0 + 1);
+    for (int x = 0; x < ST; ++x) {
+      if (t0 + x < te) issue(t0 + x);
+      copy_commit();
     }
 
     // ---- Q: each row's power of two, group sums and operands
-    __syncthreads();  // the last row tile's are no longer read
     constexpr int E = D / 32;
     float q[R / kWarps][E];
 #pragma unroll
@@ -464,12 +481,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         const int pos = w.s.len - w.s.n + (r0 + r) / a.group;
         row_lim[r] = r0 + r >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : w.s.len;
       }
+      // 2^-ex in two factors that are float32 numbers for every ex
+      const float up = pow2(-ex / 2), up2 = pow2(-ex - -ex / 2);
       __half* qh = reinterpret_cast<__half*>(qfrag);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e, g = d / 64, i = d % 64 / 8, n = d % 8;
-        const int st = (i & 1) * 2 + (n & 3) / 2, reg = n & 1, half = n >> 2;
-        float v = ldexpf(q[y][e], reg ? -ex - 4 : -ex);
+        const int d = lane * E + e, g = d / 64, i = d % 64 / 8, n8 = d % 8;
+        const int st = (i & 1) * 2 + (n8 & 3) / 2, reg = n8 & 1, half = n8 >> 2;
+        float v = q[y][e] * up * up2;
+        if (reg) v *= 0.0625f;
 #pragma unroll
         for (int part = 0; part < QP; ++part) {
           const __half hv = __float2half_rn(v);
@@ -480,40 +500,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     }
     __syncthreads();
 
-    uint32_t qr[S::QSMEM ? 1 : G * 4][QP][NT][2];
-    if constexpr (!S::QSMEM) {
-#pragma unroll
-      for (int x = 0; x < G * 4; ++x)
-#pragma unroll
-        for (int part = 0; part < QP; ++part)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 v = qfrag[((x * QP + part) * NT + nt) * 32 + lane];
-            qr[x][part][nt][0] = v.x, qr[x][part][nt][1] = v.y;
-          }
-    }
-    float rf[NT][2], rz[G][NT][2];
-    if constexpr (!S::QSMEM) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          rf[nt][e] = row_f[nt * 8 + 2 * t4 + e];
-#pragma unroll
-          for (int g = 0; g < G; ++g) rz[g][nt][e] = row_z[g][nt * 8 + 2 * t4 + e];
-        }
-    }
-
     // sums in units of 2^(unit[g] - 7 - 24) (values 0, 2, 4, 6 of a word) and 2^4 of it (1, 3, 5, 7);
     // minus[g]: -8 sum(p s) since it was last folded in
     float acc[G][4][NT][4], minus[S::COUNT ? G : 1][NT][4], accb[G][NT][2], bar[NT][2], mu[NT][2], l[NT][2];
     int unit[G];
-    float cap[G], per_unit[G];  // 2^unit, 2^(7 - unit)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       unit[g] = kLeastUnit;
-      cap[g] = pow2(kLeastUnit);
-      per_unit[g] = pow2(7 - kLeastUnit);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -550,75 +543,95 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 
     for (int t = t0; t < te; ++t) {
       const int k0 = t * KT + warp * CH * 16;
+      const uint8_t* stage = ring + (uint32_t)((t - t0) % ST) * S::STAGE_BYTES;
+      copy_wait<ST - 1>();
+      __syncwarp();
       // S^T, in units of 1 / rf
       float x[CH][NT][4];
+      {
+        uint32_t kw[CH][2][2 * G];
+        float sc[G][CH][NT][4];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int y = 0; y < 2; ++y) lds_words(kw[c][y], stage + c * S::CHUNK_BYTES + k_lane + y * (4 * D));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[c][nt][e] = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float sc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+        for (int g = 0; g < G; ++g)
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
-            const uint32_t wa = kw[c][0][(st >> 1) * G + g] >> (8 * (st & 1));
-            const uint32_t wb = kw[c][1][(st >> 1) * G + g] >> (8 * (st & 1));
-            const uint32_t ak[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
+            uint2 bq[QP][NT];
 #pragma unroll
             for (int part = 0; part < QP; ++part)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if constexpr (S::QSMEM) {
-                  const uint2 v = qfrag[(((g * 4 + st) * QP + part) * NT + nt) * 32 + lane];
-                  mma_f16(sc[nt], ak, v.x, v.y);
-                } else {
-                  mma_f16(sc[nt], ak, qr[g * 4 + st][part][nt][0], qr[g * 4 + st][part][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                bq[part][nt] = qfrag[(((g * 4 + st) * QP + part) * NT + nt) * 32 + lane];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              const uint32_t wa = kw[c][0][(st >> 1) * G + g] >> (8 * (st & 1));
+              const uint32_t wb = kw[c][1][(st >> 1) * G + g] >> (8 * (st & 1));
+              const uint32_t ak[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
+#pragma unroll
+              for (int part = 0; part < QP; ++part)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (st == 0 && part == 0) mma_f16_first(sc[g][c][nt], ak, bq[part][nt].x, bq[part][nt].y);
+                  else mma_f16(sc[g][c][nt], ak, bq[part][nt].x, bq[part][nt].y);
                 }
-              }
+            }
           }
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float s = bf16_lo(ksw[c][y][g]), z = fmaf(-8.f, s, bf16_hi(ksw[c][y][g]));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float sum = S::QSMEM ? row_z[g][nt * 8 + 2 * t4 + e] : rz[g][nt][e];
-                x[c][nt][2 * y + e] = fmaf(s, sc[nt][2 * y + e], fmaf(z, sum, x[c][nt][2 * y + e]));
-              }
-          }
-        }
-      }
-      // K's registers are free: the next tile's loads
-      if (t + 1 < te) {
-        rows_of(t + 1);
-        load_k();
-      }
-
-      // keys that not all rows see: by their places
-      if (k0 + CH * 16 > all_see || bad) {
-        if (bad) set_status(a.status, kStatusBounds);
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int key = k0 + c * 16 + y * 8 + g8;
+            uint32_t ksw[G];
+            lds_words(ksw, stage + c * S::CHUNK_BYTES + s_lane + y * (32 * G));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const float st = bf16_lo(ksw[g]), z = fmaf(-8.f, st, bf16_hi(ksw[g]));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 sum = *reinterpret_cast<const float2*>(&row_z[g][nt * 8 + 2 * t4]);
+                const float p0 = g ? fmaf(z, sum.x, x[c][nt][2 * y]) : z * sum.x;
+                const float p1 = g ? fmaf(z, sum.y, x[c][nt][2 * y + 1]) : z * sum.y;
+                x[c][nt][2 * y] = fmaf(st, sc[g][c][nt][2 * y], p0);
+                x[c][nt][2 * y + 1] = fmaf(st, sc[g][c][nt][2 * y + 1], p1);
+              }
+            }
+          }
+      }
+      uint32_t vw[CH][4][G], vsw[CH][2][G];
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          lds_words(vw[c][2 * y], stage + c * S::CHUNK_BYTES + v_lane0 + y * (4 * D));
+          lds_words(vw[c][2 * y + 1], stage + c * S::CHUNK_BYTES + v_lane1 + y * (4 * D));
+          lds_words(vsw[c][y], stage + c * S::CHUNK_BYTES + s_lane + 64 * G + y * (32 * G));
+        }
+      __syncwarp();  // the stage is read: the tile ST ahead may come
+      if (t + ST < te) issue(t + ST);
+      copy_commit();
+
+      // keys that not all rows see: by their places
+      if (k0 + CH * 16 > all_see || bad) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int kc0 = min(k0 + c * 16, (klen - 1) & ~15);
+          const bool dead = k0 + c * 16 >= klen || (bad && (unsigned)table[div_by(kc0, args.page_div)] >= (unsigned)a.n_pages);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int key = k0 + c * 16 + y * 8 + key8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if ((dead >> c & 1) || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
-            if ((dead >> c & 1) || key >= w.s.len) {  // what no position holds may be anything: not into the sums
+                if (dead || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
+            if (dead || key >= w.s.len) {  // what no position holds may be anything: not into the sums
 #pragma unroll
               for (int g = 0; g < G; ++g) vsw[c][y][g] = 0;
             }
           }
+        }
       }
       // The running maximum is raised only when a score is above it by more than 2^8,
       // the unit only when a step is above it.
@@ -640,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
         for (int c = 1; c < CH; ++c) v = fmax3f(v, bf16_lo(vsw[c][0][g]), bf16_lo(vsw[c][1][g]));
         step[g] = v;
-        over |= v > cap[g];
+        over |= v > pow2(unit[g]);
       }
       if (__any_sync(0xffffffffu, over)) {
         float fg[G];
@@ -652,8 +665,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           const int nu = max(unit[g], min((int)(__float_as_uint(v) >> 23) - 126, 127));  // v < 2^nu
           fg[g] = unit[g] - nu < -126 ? 0.f : pow2(unit[g] - nu);
           unit[g] = nu;
-          cap[g] = pow2(nu);
-          per_unit[g] = pow2(7 - nu);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
             float f = 1.f;
             if (v > -INFINITY) {
-              const float r = S::QSMEM ? row_f[nt * 8 + 2 * t4 + e] : rf[nt][e];
+              const float r = row_f[nt * 8 + 2 * t4 + e];
               v *= r;
               if (bar[nt][e] > -INFINITY) {
                 v = fmaxf(v, mu[nt][e]);
@@ -684,28 +695,30 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           }
       }
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 rf = *reinterpret_cast<const float2*>(&row_f[nt * 8 + 2 * t4]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[c][nt][e] = fast_exp2(fmaf(x[c][nt][e], S::QSMEM ? row_f[nt * 8 + 2 * t4 + (e & 1)] : rf[nt][e & 1],
-                                         -mu[nt][e & 1]));
+            x[c][nt][e] = fast_exp2(fmaf(x[c][nt][e], (e & 1) ? rf.y : rf.x, -mu[nt][e & 1]));
             l[nt][e & 1] += x[c][nt][e];
           }
+      }
 
       // O^T += V^T (p s), and the offsets' sums
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           uint32_t pb[PP][NT][2];
+          const float per_unit = pow2(7 - unit[g]);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float s = bf16_lo(vsw[c][y][g]) * per_unit[g], o = bf16_hi(vsw[c][y][g]);
+            const float st = bf16_lo(vsw[c][y][g]) * per_unit, o = bf16_hi(vsw[c][y][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float p0 = x[c][nt][2 * y] * s, p1 = x[c][nt][2 * y + 1] * s;
+              float p0 = x[c][nt][2 * y] * st, p1 = x[c][nt][2 * y + 1] * st;
               accb[g][nt][0] = fmaf(x[c][nt][2 * y], o, accb[g][nt][0]);
               accb[g][nt][1] = fmaf(x[c][nt][2 * y + 1], o, accb[g][nt][1]);
 #pragma unroll
@@ -744,12 +757,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
               for (int nt = 0; nt < NT; ++nt) mma_f16(acc[g][mt][nt], av, pb[part][nt][0], pb[part][nt][1]);
           }
         }
-      }
-      if (t + 1 < te) {
-        load_v();
-        load_ids(t + 2);
-      }
-      dead = next_dead, bad = next_bad;
       if ((t - t0) % S::FOLD == S::FOLD - 1) fold();
     }
     fold();
@@ -764,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           for (int o = 4; o < 32; o <<= 1) accb[g][nt][e] += __shfl_xor_sync(0xffffffffu, accb[g][nt][e], o);
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p17f, cap[g], accb[g][nt][e]);
-            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p13f, cap[g], accb[g][nt][e]);
+            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p17f, pow2(unit[g]), accb[g][nt][e]);
+            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p13f, pow2(unit[g]), accb[g][nt][e]);
           }
         }
 
