@@ -1,10 +1,11 @@
 // The 4-bit key/value cache: argument checks of its three operators, and the
 // kernels that quantise rows as they are written and read them back.
 //
-// Both kernels give a thread one 32-bit code word, 8 values: 16 (bf16) or 32
-// (float32) bytes of a row on one side and 4 on the other, so that a warp's loads
-// and stores cover whole rows.  They are bound by device memory: 2 D bytes in and
-// D / 2 + D / 16 out for a bf16 row of D values, or the other way round.
+// Both kernels give a block 16 positions of a few heads, 8 lanes a row: a lane has word i
+// of every group, 8 values each, so that rows are read and written in whole lines, a
+// position's page is looked up once, and neighbouring positions' (s, b) pairs fill
+// their 32-byte sectors.  They are bound by device memory: 2 D bytes in and D / 2 + D / 16
+// out for a bf16 row of D values, or the other way round.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -21,158 +22,238 @@ attn_status_t device_status(int** status, int* sms, unsigned long long* wait_ns)
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRowsPerThread = 4;  // rows whose loads a thread issues before it uses the first
+constexpr int kThreads = 128, kSlots = kThreads / 8;  // positions of a block
+constexpr int kWords = 8;                             // code words of a thread: 8 / (D / 64) heads
 
+__device__ __forceinline__ uint32_t min_bf16(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_bf16(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16(uint32_t x, uint32_t y, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+
+// Eight values of a row, and the least and largest of them as a pair (low, -high) that
+// lanes can join by minima.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+struct Eight;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
+struct Eight<__nv_bfloat16> {
+  using Pair = uint32_t;  // two bf16
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ Pair range() const {
+    const uint32_t lo = min_bf16(min_bf16(u.x, u.y), min_bf16(u.z, u.w));
+    const uint32_t hi = max_bf16(max_bf16(u.x, u.y), max_bf16(u.z, u.w)) ^ 0x80008000u;
+    return min_bf16(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
   }
-}
+  __device__ static __forceinline__ Pair join(Pair a, Pair b) { return min_bf16(a, b); }
+  __device__ static __forceinline__ Pair shuffle(Pair a, int o) { return __shfl_xor_sync(0xffffffffu, a, o); }
+  __device__ static __forceinline__ float low(Pair a) { return bf16_lo(a); }
+  __device__ static __forceinline__ float high(Pair a) { return -bf16_hi(a); }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+    return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+  }
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                                            ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+struct Eight<float> {
+  using Pair = float2;
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ Pair range() const {
+    return make_float2(fminf(fminf(fminf(a.x, a.y), fminf(a.z, a.w)), fminf(fminf(b.x, b.y), fminf(b.z, b.w))),
+                       -fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w))));
+  }
+  __device__ static __forceinline__ Pair join(Pair a, Pair b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
+  __device__ static __forceinline__ Pair shuffle(Pair a, int o) {
+    return make_float2(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o));
+  }
+  __device__ static __forceinline__ float low(Pair a) { return a.x; }
+  __device__ static __forceinline__ float high(Pair a) { return -a.y; }
+  __device__ __forceinline__ float operator[](int i) const {
+    const float4& v = i < 4 ? a : b;
+    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+  }
+};
+
+// round((x - b) / s) + 8 of eight values in the places of a code word.  The sum with
+// 1.5 2^23 + 8 rounds to a whole number, halves to even, and leaves it in the last bits;
+// the sums' first bits are taken off together.
+template <bool kClamp, class T>
+__device__ __forceinline__ uint32_t code_word(const Eight<T>& x, float b, float inv) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float m = __fmul_rn(__fsub_rn(x[k], b), inv);
+    if (kClamp) m = fminf(fmaxf(m, -8.f), 7.f);
+    w += __float_as_uint(__fadd_rn(m, 12582920.f)) << (4 * k);
+  }
+  return w - (0x4B400000u + (0x4B400000u << 4) + (0x4B400000u << 8));
 }
 
-// Row r of a sequence, counted along memory: position-major heads when packed
-// ([tokens, heads, D]), head-major otherwise ([heads, seqlen, D]).
-__device__ __forceinline__ void split_row(const Kv4Args& a, const Kv4Seq& s, int r, int* h, int* i) {
-  if (a.cu) {
-    *i = r / a.heads_kv;
-    *h = r - *i * a.heads_kv;
-  } else {
-    *h = r / s.n;
-    *i = r - *h * s.n;
-  }
+// Where a thread's rows lie: position slot of the block, heads h0 .. h0 + heads - 1.
+struct Place {
+  int i, pos, h0, heads;
+  long long x0;   // first element of head h0's row in x (or y)
+  long long row;  // head h0's row in the cache; -1: none
+};
+template <int kHeads>
+__device__ __forceinline__ Place place_of(const Kv4Args& a, const Kv4Seq& s, int b, int c, long long sb, long long sh,
+                                          long long ss) {
+  const int head_blocks = (a.heads_kv + kHeads - 1) / kHeads, tile = c / head_blocks;
+  Place p;
+  p.h0 = (c - tile * head_blocks) * kHeads;
+  p.i = tile * kSlots + threadIdx.x / 8;
+  p.heads = p.i < s.n ? min(kHeads, a.heads_kv - p.h0) : 0;
+  p.pos = s.len - s.n + p.i;
+  p.x0 = (a.cu ? (s.row0 + p.i) * ss : b * sb + p.i * ss) + p.h0 * sh;
+  p.row = p.heads && p.pos >= 0 ? kv4_row(a, b, p.h0, p.pos) : -1;
+  return p;
 }
 
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads) k_kv4_write(const __grid_constant__ Kv4Args a, int blocks_per_seq) {
-  constexpr int L = D / 8;             // threads of a row
-  constexpr int R = kThreads / L;      // rows of the block at a time
-  constexpr int G = D / kKv4Group;
-  const int b = blockIdx.x / blocks_per_seq;
+  constexpr int G = D / kKv4Group, H = kWords / G;
+  using E = Eight<T>;
+  const int b = blockIdx.x / blocks_per_seq, lane = threadIdx.x & 31, e = lane & 7;
   const Kv4Seq s = kv4_seq(a, b);
-  const int rows = s.n * a.heads_kv;
-  const int r0 = (blockIdx.x - b * blocks_per_seq) * (R * kRowsPerThread) + threadIdx.x / L;
-  const int e = threadIdx.x % L;  // values 8 e .. 8 e + 7: word i = e % 8 of group g = e / 8
   const bool is_v = blockIdx.y != 0;
-  const T* src = static_cast<const T*>(is_v ? a.y : a.x);
-  const long long sb = is_v ? a.y_sb : a.x_sb, sh = is_v ? a.y_sh : a.x_sh, ss = is_v ? a.y_ss : a.x_ss;
+  const long long sh = is_v ? a.y_sh : a.x_sh;
+  const Place p = place_of<H>(a, s, b, blockIdx.x - b * blocks_per_seq, is_v ? a.y_sb : a.x_sb, sh, is_v ? a.y_ss : a.x_ss);
+  const T* src = static_cast<const T*>(is_v ? a.y : a.x) + p.x0 + e * 8;
   uint8_t* codes = is_v ? a.vc : a.kc;
   uint32_t* scale = is_v ? a.vs : a.ks;
 
-  float x[kRowsPerThread][8];
-  long long row[kRowsPerThread];
+  E x[kWords];  // word e of group k % G of head h0 + k / G
 #pragma unroll
-  for (int j = 0; j < kRowsPerThread; ++j) {
-    const int r = r0 + j * R;
-    row[j] = -1;
+  for (int k = 0; k < kWords; ++k) {
+    x[k].clear();
+    if (p.row >= 0 && k / G < p.heads) x[k].load(src + k / G * sh + k % G * kKv4Group);
+  }
+  // The groups' ranges: each exchange of lanes halves the groups a lane still joins, so that
+  // lane e ends with group e's, and works out its step and offset for all eight.
+  typename E::Pair r[kWords];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[j][k] = 0.f;
-    if (r < rows) {
-      int h, i;
-      split_row(a, s, r, &h, &i);
-      const int pos = s.len - s.n + i;
-      if (pos >= 0) {
-        load8(src + (a.cu ? (s.row0 + i) * ss : b * sb + i * ss) + h * sh + e * 8, x[j]);
-        row[j] = kv4_row(a, b, h, pos);
-      }
+  for (int k = 0; k < kWords; ++k) r[k] = x[k].range();
+#pragma unroll
+  for (int o = 4; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const typename E::Pair other = E::shuffle((e & o) ? r[k] : r[k + o], o);
+      r[k] = E::join((e & o) ? r[k + o] : r[k], other);
     }
+  const float lo = E::low(r[0]), hi = E::high(r[0]);
+  float st = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
+  if (st < 1.1754943508222875e-38f) st = 0.f;  // 2^-126: its reciprocal would not be finite
+  const float ce = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * st)));
+  const float inv = st > 0.f ? __frcp_rn(st) : 0.f;
+  const uint32_t sb = (__float_as_uint(st) >> 16) | (__float_as_uint(ce) & 0xFFFF0000u);
+  if (p.row >= 0 && e / G < p.heads) scale[(p.row + (long long)(e / G) * a.page) * G + e % G] = sb;
+  // b's rounding may have moved the ends past the codes: then every value is held to them
+  const bool inside = __fmul_rn(__fsub_rn(lo, ce), inv) >= -8.5f && __fmul_rn(__fsub_rn(hi, ce), inv) < 7.5f;
+  const bool clamp = !__all_sync(0xffffffffu, inside);
+  uint32_t w[kWords];
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    const float bk = bf16_hi(__shfl_sync(0xffffffffu, sb, k, 8)), ik = __shfl_sync(0xffffffffu, inv, k, 8);
+    w[k] = clamp ? code_word<true>(x[k], bk, ik) : code_word<false>(x[k], bk, ik);
   }
 #pragma unroll
-  for (int j = 0; j < kRowsPerThread; ++j) {
-    float lo = x[j][0], hi = x[j][0];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) lo = fminf(lo, x[j][k]), hi = fmaxf(hi, x[j][k]);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {  // the group's 8 threads
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  for (int u = 0; u < H; ++u)
+    if (p.row >= 0 && u < p.heads) {
+      uint8_t* to = codes + (p.row + (long long)u * a.page) * (D / 2) + e * (4 * G);
+      if constexpr (G == 1) *reinterpret_cast<uint32_t*>(to) = w[u];
+      if constexpr (G == 2) *reinterpret_cast<uint2*>(to) = make_uint2(w[2 * u], w[2 * u + 1]);
+      if constexpr (G == 4)
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
     }
-    float st = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
-    if (st < 1.1754943508222875e-38f) st = 0.f;  // 2^-126: its reciprocal would not be finite
-    const float ce = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * st)));
-    const float inv = st > 0.f ? __fdiv_rn(1.f, st) : 0.f;
-    uint32_t w = 0;
+}
+
+// A code word's eight values.
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint32_t sb) {
+  // 0x4300 is 128 in bf16, its last bit 1: codes by bit operations, minus 136, both exact; the
+  // product's sum with b is rounded once
+  const uint32_t s2 = __byte_perm(sb, sb, 0x1010), b2 = __byte_perm(sb, sb, 0x3232);
+  uint32_t v[4];  // values k and k + 4
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float u = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[j][k], ce), inv)) + 8.f, 0.f), 15.f);
-      w |= (uint32_t)u << (4 * k);
-    }
-    if (row[j] >= 0) {
-      *reinterpret_cast<uint32_t*>(codes + row[j] * (D / 2) + ((e & 7) * G + (e >> 3)) * 4) = w;
-      if ((e & 7) == 0) scale[row[j] * G + (e >> 3)] = (__float_as_uint(st) >> 16) | (__float_as_uint(ce) & 0xFFFF0000u);
-    }
-  }
+  for (int k = 0; k < 4; ++k)
+    v[k] = fma_bf16(s2, add_bf16(((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u, 0xC308C308u), b2);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                                                 __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)));
+}
+__device__ __forceinline__ void store_values(float* p, uint32_t w, uint32_t sb) {
+  const float s = bf16_lo(sb), b = bf16_hi(sb);
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)  // 2^23 + u by bit operations, minus 2^23 + 8
+    v[k] = fmaf(s, __uint_as_float(((w >> (4 * k)) & 15u) | 0x4B000000u) - 8388616.f, b);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p + 4), make_float4(v[4], v[5], v[6], v[7]));
 }
 
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads) k_kv4_read(const __grid_constant__ Kv4Args a, int blocks_per_seq) {
-  constexpr int L = D / 8, R = kThreads / L, G = D / kKv4Group;
-  const int b = blockIdx.x / blocks_per_seq;
+  constexpr int G = D / kKv4Group, H = kWords / G;
+  const int b = blockIdx.x / blocks_per_seq, e = threadIdx.x & 7;
   const Kv4Seq s = kv4_seq(a, b);
-  const int rows = s.n * a.heads_kv;
-  const int r0 = (blockIdx.x - b * blocks_per_seq) * (R * kRowsPerThread) + threadIdx.x / L;
-  const int e = threadIdx.x % L;  // stored word e: word i = e / G of group g = e % G
-  const int g = e % G, d0 = g * kKv4Group + e / G * 8;
   const bool is_v = blockIdx.y != 0;
-  T* dst = static_cast<T*>(is_v ? a.y : a.x);
-  const long long sb = is_v ? a.y_sb : a.x_sb, sh = is_v ? a.y_sh : a.x_sh, ss = is_v ? a.y_ss : a.x_ss;
+  const long long sh = is_v ? a.y_sh : a.x_sh;
+  const Place p = place_of<H>(a, s, b, blockIdx.x - b * blocks_per_seq, is_v ? a.y_sb : a.x_sb, sh, is_v ? a.y_ss : a.x_ss);
+  T* dst = static_cast<T*>(is_v ? a.y : a.x) + p.x0 + e * 8;
   const uint8_t* codes = is_v ? a.vc : a.kc;
   const uint32_t* scale = is_v ? a.vs : a.ks;
 
-  uint32_t w[kRowsPerThread], sc[kRowsPerThread];
-  T* out[kRowsPerThread];
+  uint32_t w[kWords], sb[kWords];
 #pragma unroll
-  for (int j = 0; j < kRowsPerThread; ++j) {
-    const int r = r0 + j * R;
-    w[j] = sc[j] = 0;
-    out[j] = nullptr;
-    if (r < rows) {
-      int h, i;
-      split_row(a, s, r, &h, &i);
-      const int pos = s.len - s.n + i;
-      out[j] = dst + (a.cu ? (s.row0 + i) * ss : b * sb + i * ss) + h * sh + d0;
-      const long long row = pos >= 0 ? kv4_row(a, b, h, pos) : -1;
-      if (row >= 0) {
-        w[j] = *reinterpret_cast<const uint32_t*>(codes + row * (D / 2) + e * 4);
-        sc[j] = scale[row * G + g];
+  for (int u = 0; u < H; ++u) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) w[u * G + g] = sb[u * G + g] = 0;  // padding: values 0
+    if (p.row >= 0 && u < p.heads) {
+      const long long row = p.row + (long long)u * a.page;
+      const uint8_t* from = codes + row * (D / 2) + e * (4 * G);
+      if constexpr (G == 1) {
+        w[u] = __ldcs(reinterpret_cast<const uint32_t*>(from));
+        sb[u] = __ldg(scale + row);
+      }
+      if constexpr (G == 2) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(from)), t = __ldg(reinterpret_cast<const uint2*>(scale + row * 2));
+        w[2 * u] = v.x, w[2 * u + 1] = v.y, sb[2 * u] = t.x, sb[2 * u + 1] = t.y;
+      }
+      if constexpr (G == 4) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(from)), t = __ldg(reinterpret_cast<const uint4*>(scale + row * 4));
+        w[4 * u] = v.x, w[4 * u + 1] = v.y, w[4 * u + 2] = v.z, w[4 * u + 3] = v.w;
+        sb[4 * u] = t.x, sb[4 * u + 1] = t.y, sb[4 * u + 2] = t.z, sb[4 * u + 3] = t.w;
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < kRowsPerThread; ++j) {
-    if (!out[j]) continue;
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = fmaf(bf16_lo(sc[j]), (float)(int)((w[j] >> (4 * k)) & 15u) - 8.f, bf16_hi(sc[j]));
-    store8(out[j], v);
-  }
+  for (int k = 0; k < kWords; ++k)
+    if (k / G < p.heads) store_values(dst + k / G * sh + k % G * kKv4Group, w[k], sb[k]);
 }
 
 template <class F>
 cudaError_t launch_rows(const Kv4Args& a, int head_dim, F&& kernel, cudaStream_t st) {
-  const int per_block = kThreads / (head_dim / 8) * kRowsPerThread;
-  const long long rows = (long long)a.seqlen * a.heads_kv, per_seq = (rows + per_block - 1) / per_block;
+  const int heads = kWords / (head_dim / kKv4Group);
+  const long long per_seq = ((long long)a.seqlen + kSlots - 1) / kSlots * ((a.heads_kv + heads - 1) / heads);
   const long long blocks = per_seq * a.batch;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   kernel<<<dim3((unsigned)blocks, 2), kThreads, 0, st>>>(a, (int)per_seq);
