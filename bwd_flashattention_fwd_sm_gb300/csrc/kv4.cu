@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_write(const __grid_constant__ 
   const bool is_v = blockIdx.y != 0;
   const long long sh = is_v ? a.y_sh : a.x_sh;
   const Place p = place_of<H>(a, s, b, blockIdx.x - b * blocks_per_seq, is_v ? a.y_sb : a.x_sb, sh, is_v ? a.y_ss : a.x_ss);
+  if (p.i - (int)threadIdx.x / 8 >= s.n) return;  // the sequence ends before the block
   const T* src = static_cast<const T*>(is_v ? a.y : a.x) + p.x0 + e * 8;
   uint8_t* codes = is_v ? a.vc : a.kc;
   uint32_t* scale = is_v ? a.vs : a.ks;
@@ -172,10 +173,15 @@ __global__ void __launch_bounds__(kThreads) k_kv4_write(const __grid_constant__ 
   const bool inside = __fmul_rn(__fsub_rn(lo, ce), inv) >= -8.5f && __fmul_rn(__fsub_rn(hi, ce), inv) < 7.5f;
   const bool clamp = !__all_sync(0xffffffffu, inside);
   uint32_t w[kWords];
+  float bk[kWords], ik[kWords];
 #pragma unroll
-  for (int k = 0; k < kWords; ++k) {
-    const float bk = bf16_hi(__shfl_sync(0xffffffffu, sb, k, 8)), ik = __shfl_sync(0xffffffffu, inv, k, 8);
-    w[k] = clamp ? code_word<true>(x[k], bk, ik) : code_word<false>(x[k], bk, ik);
+  for (int k = 0; k < kWords; ++k) bk[k] = __shfl_sync(0xffffffffu, ce, k, 8), ik[k] = __shfl_sync(0xffffffffu, inv, k, 8);
+  if (clamp) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = code_word<true>(x[k], bk[k], ik[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = code_word<false>(x[k], bk[k], ik[k]);
   }
 #pragma unroll
   for (int u = 0; u < H; ++u)
@@ -218,6 +224,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_read(const __grid_constant__ K
   const bool is_v = blockIdx.y != 0;
   const long long sh = is_v ? a.y_sh : a.x_sh;
   const Place p = place_of<H>(a, s, b, blockIdx.x - b * blocks_per_seq, is_v ? a.y_sb : a.x_sb, sh, is_v ? a.y_ss : a.x_ss);
+  if (p.i - (int)threadIdx.x / 8 >= s.n) return;  // the sequence ends before the block
   T* dst = static_cast<T*>(is_v ? a.y : a.x) + p.x0 + e * 8;
   const uint8_t* codes = is_v ? a.vc : a.kc;
   const uint32_t* scale = is_v ? a.vs : a.ks;

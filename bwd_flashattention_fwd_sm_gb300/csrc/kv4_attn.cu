@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kv4.h"
 #include "ptx.cuh"
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   __shared__ float warp_m[kWarps][R], warp_l[kWarps][R];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long tile, tile_end, total, first;
   int b;
   const long long n = find_stretch<R, KT>(a, &tile, &tile_end, &total, &b, &first);
@@ -870,9 +872,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const __grid_const
   __shared__ float sm[kJoinWarps][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t4 = lane & 3;
   const int i0 = blockIdx.x, j = blockIdx.y, nt = j % NT;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
   const int4 tile = __ldcg(&args.shared[i0]);
   const int b = tile.x, h = tile.y, rt = tile.z, i1 = tile.w;
   if (i1 < 0) return;
+  const Kv4Seq seq = kv4_seq(a, b);
 
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   auto add = [&](const float (&v)[4], const float (&pm)[2], const float (&pl)[2]) {
@@ -910,7 +914,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv4_join(const __grid_const
   for (int e = 0; e < 2; ++e) sm[warp][4 + e][lane] = m[e], sm[warp][6 + e][lane] = l[e];
   __syncthreads();
   if (warp) return;
-  const Kv4Seq seq = kv4_seq(a, b);
 #pragma unroll
   for (int y = 1; y < kJoinWarps; ++y) {
     const float v[4] = {sm[y][0][lane], sm[y][1][lane], sm[y][2][lane], sm[y][3][lane]};
@@ -948,14 +951,33 @@ struct Launch {
     args.part_o = static_cast<float*>(ws);
     args.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + o_bytes(a));
     args.shared = reinterpret_cast<int4*>(static_cast<char*>(ws) + o_bytes(a) + ml_bytes(a));
-    cudaError_t e = cudaFuncSetAttribute(k_kv4_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    // the kernel's shared-memory limit, once a device
+    static std::atomic<unsigned long long> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(k_kv4_attn<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+      if (e != cudaSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
     const int n = grid(a);
     k_kv4_attn<T, D, NT><<<n, kThreads, S::SMEM, st>>>(args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((long long)a.max_pages * a.page <= S::KT) return cudaSuccess;  // a row tile has one tile of keys
-    k_kv4_join<T, D, NT><<<dim3(n, S::ACC / 4), kJoinWarps * 32, 0, st>>>(args);
-    return cudaGetLastError();
+    // The join may be set up while the first kernel still runs: its blocks wait for that
+    // kernel's end themselves.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n, S::ACC / 4);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_kv4_join<T, D, NT>, args);
   }
 };
 

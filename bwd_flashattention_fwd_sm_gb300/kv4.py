@@ -22,8 +22,6 @@ Tensors may be views: any strides whose last one is 1 and whose others are whole
 
 from __future__ import annotations
 
-import contextlib
-import ctypes
 import math
 
 import torch
@@ -61,6 +59,7 @@ class Kv4Cache:
             if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.pointers = tuple(t.data_ptr() for t in (k_codes, k_scale, v_codes, v_scale))
 
     @classmethod
     def empty(cls, n_pages, heads_kv, page_size, head_dim, device=None) -> "Kv4Cache":
@@ -132,30 +131,35 @@ def _params(x, y, cache, block_table, lens, seqlens, heads_q, heads_kv, scale=0.
                       xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], scale, dtype, 1 if causal else 0)
 
 
-@contextlib.contextmanager
-def _entered(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:  # what is allocated for the call belongs to the stream that it runs on
-            with torch.cuda.stream(stream):
-                yield stream
+def _on(device, stream, call, *args):
+    """call(*args, handle) with ``device`` current and, where ``stream`` is given, that stream: what is
+    allocated for the call then belongs to the stream that it runs on, and what comes from
+    another stream is not given away before the call has run."""
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        if stream is not None:
+            for t in args:
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def kv4_write(cache: Kv4Cache, k, v, block_table, lens, *, seqlens: SeqLens | None = None, stream=None) -> Kv4Cache:
     """Quantises the newest tokens' k and v to 4 bits and stores them.  Returns the cache.
 
     Pages that a sequence shares with another must not be written to."""
-    lib = _lib.load()
     if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
         raise ValueError("v must match k in shape, dtype and device")
-    with _entered(cache.device, stream) as st:
-        k, v = _usable(k), _usable(v)
-        heads = k.shape[1] if k.dim() > 1 else 0
-        p = _params(k, v, cache, block_table, lens, seqlens, heads, heads)
-        check(lib.attn_kv4_write(p, k.data_ptr(), v.data_ptr(), cache.k_codes.data_ptr(), cache.k_scale.data_ptr(),
-                                 cache.v_codes.data_ptr(), cache.v_scale.data_ptr(), st.cuda_stream),
-              "attn_kv4_write")
+    return _on(cache.device, stream, _write, cache, k, v, block_table, lens, seqlens)
+
+
+def _write(cache, k, v, block_table, lens, seqlens, stream):
+    k, v = _usable(k), _usable(v)
+    heads = k.shape[1] if k.dim() > 1 else 0
+    p = _params(k, v, cache, block_table, lens, seqlens, heads, heads)
+    check(_lib.load().attn_kv4_write(p, k.data_ptr(), v.data_ptr(), *cache.pointers, stream), "attn_kv4_write")
     return cache
 
 
@@ -163,24 +167,25 @@ def kv4_read(cache: Kv4Cache, block_table, lens, seqlen: int | None = None, *, s
              dtype=torch.bfloat16, stream=None, out=None):
     """The newest tokens' keys and values, (k, v): ``seqlen`` of each sequence, or with
     ``seqlens`` a packed batch.  Rows of padding are 0.  out: a (k, v) pair to write to."""
-    lib = _lib.load()
     if (seqlen is None) == (seqlens is None):
         raise ValueError("give either seqlen (a fixed number of tokens) or seqlens (a packed batch)")
+    return _on(cache.device, stream, _read, cache, block_table, lens, seqlen, seqlens, dtype, out)
+
+
+def _read(cache, block_table, lens, seqlen, seqlens, dtype, out, stream):
     H, D = cache.heads_kv, cache.head_dim
     shape = (block_table.shape[0], H, int(seqlen), D) if seqlens is None else (seqlens.total, H, D)
-    with _entered(cache.device, stream) as st:
-        if out is None:
-            k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in "kv")
-        else:
-            k, v = out
-            for t in out:
-                if tuple(t.shape) != shape or t.dtype != k.dtype or t.device != cache.device or not _fits(t):
-                    raise ValueError(f"out must be two CUDA tensors of shape {shape} and one dtype, rows contiguous "
-                                     "and 16-byte aligned")
-        p = _params(k, v, cache, block_table, lens, seqlens, H, H)
-        check(lib.attn_kv4_read(p, cache.k_codes.data_ptr(), cache.k_scale.data_ptr(), cache.v_codes.data_ptr(),
-                                cache.v_scale.data_ptr(), k.data_ptr(), v.data_ptr(), st.cuda_stream),
-              "attn_kv4_read")
+    if out is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        for t in out:
+            if tuple(t.shape) != shape or t.dtype != k.dtype or t.device != cache.device or not _fits(t):
+                raise ValueError(f"out must be two CUDA tensors of shape {shape} and one dtype, rows contiguous "
+                                 "and 16-byte aligned")
+    p = _params(k, v, cache, block_table, lens, seqlens, H, H)
+    check(_lib.load().attn_kv4_read(p, *cache.pointers, k.data_ptr(), v.data_ptr(), stream), "attn_kv4_read")
     return k, v
 
 
@@ -189,27 +194,28 @@ def attn_fwd_kv4(q, cache: Kv4Cache, block_table, lens, *, causal=True, scale=No
     """O, LSE of the newest tokens' queries over all that the cache holds.  Returns (o, lse).
 
     causal: a token sees the positions up to its own; else all of its sequence's."""
+    return _on(cache.device, stream, _attend, q, cache, block_table, lens, causal, scale, seqlens, workspace, out)
+
+
+def _attend(q, cache, block_table, lens, causal, scale, seqlens, workspace, out, stream):
     lib = _lib.load()
-    with _entered(cache.device, stream) as st:
-        q = _usable(q)
-        if out is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            o = out
-            if o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or not _fits(o):
-                raise ValueError("out must match q in shape, dtype and device, rows contiguous and 16-byte aligned")
-        heads = q.shape[1] if q.dim() > 1 else 0
-        p = _params(q, o, cache, block_table, lens, seqlens, heads, cache.heads_kv,
-                    float(scale) if scale is not None else 1.0 / math.sqrt(cache.head_dim), causal)
-        lse = torch.empty(q.shape[:3] if seqlens is None else (heads, q.shape[0]), dtype=torch.float32,
-                          device=q.device)
-        need = lib.attn_kv4_workspace_size(p)
-        if need == SIZE_MAX:
-            raise _lib.AttnError(_lib.ATTN_ERR_INVALID_ARG, "workspace size", lib.attn_last_error().decode())
-        ws = workspace
-        if need and (ws is None or ws.numel() * ws.element_size() < need):
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        check(lib.attn_fwd_kv4(p, q.data_ptr(), cache.k_codes.data_ptr(), cache.k_scale.data_ptr(),
-                               cache.v_codes.data_ptr(), cache.v_scale.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                               ws.data_ptr() if need else None, need, st.cuda_stream), "attn_fwd_kv4")
+    q = _usable(q)
+    if out is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        o = out
+        if o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or not _fits(o):
+            raise ValueError("out must match q in shape, dtype and device, rows contiguous and 16-byte aligned")
+    heads = q.shape[1] if q.dim() > 1 else 0
+    p = _params(q, o, cache, block_table, lens, seqlens, heads, cache.heads_kv,
+                float(scale) if scale is not None else 1.0 / math.sqrt(cache.head_dim), causal)
+    lse = torch.empty(q.shape[:3] if seqlens is None else (heads, q.shape[0]), dtype=torch.float32, device=q.device)
+    need = lib.attn_kv4_workspace_size(p)
+    if need == SIZE_MAX:
+        raise _lib.AttnError(_lib.ATTN_ERR_INVALID_ARG, "workspace size", lib.attn_last_error().decode())
+    ws = workspace
+    if need and (ws is None or ws.numel() * ws.element_size() < need):
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    check(lib.attn_fwd_kv4(p, q.data_ptr(), *cache.pointers, o.data_ptr(), lse.data_ptr(),
+                           ws.data_ptr() if need else None, need, stream), "attn_fwd_kv4")
     return o, lse
