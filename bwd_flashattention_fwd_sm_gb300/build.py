@@ -27,7 +27,7 @@ LIB = os.path.join(BUILD, "libgbattn.so")
 LIB_CHECKED = os.path.join(BUILD, "libgbattn_checked.so")
 
 SOURCES = ["api.cu", "sched.cu", "bwd_aux.cu", "simt_attn.cu", "tma_host.cu", "tc_fwd.cu", "tc_bwd.cu", "tc_dq.cu",
-           "noalloc.cu", "ln.cu", "fp8.cu", "tc_bwd256.cu", "kv4.cu", "kv4_attn.cu"]
+           "noalloc.cu", "ln.cu", "fp8.cu", "tc_bwd256.cu", "kv4.cu", "kv4_attn.cu", "kv4_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", CSRC, "-I", INCLUDE]

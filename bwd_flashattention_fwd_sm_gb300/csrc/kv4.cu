@@ -364,6 +364,10 @@ attn_status_t check_pointers(const attn_kv4_params_t* p, const void* x, const vo
   return ATTN_OK;
 }
 
+size_t attention_workspace(const Kv4Args& a, int head_dim, bool bf16) {
+  return kv4_many_rows(a, head_dim, bf16) ? kv4_rows_workspace(a, head_dim) : kv4_attn_workspace(a, head_dim, bf16);
+}
+
 attn_status_t launch_status(cudaError_t e, const char* what) {
   return e == cudaSuccess ? ATTN_OK : kfail(ATTN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -442,7 +446,7 @@ size_t attn_kv4_workspace_size(const attn_kv4_params_t* p) {
   Kv4Args a;
   bool empty = false;
   if (resolve(p, true, &a, &empty) != ATTN_OK) return SIZE_MAX;
-  return empty ? 0 : kv4_attn_workspace(a, p->head_dim, p->dtype == ATTN_BF16);
+  return empty ? 0 : attention_workspace(a, p->head_dim, p->dtype == ATTN_BF16);
 }
 
 attn_status_t attn_fwd_kv4(const attn_kv4_params_t* p, const void* x, const void* k_codes, const void* k_scale,
@@ -456,7 +460,7 @@ attn_status_t attn_fwd_kv4(const attn_kv4_params_t* p, const void* x, const void
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return kfail(ATTN_ERR_INVALID_ARG, "lse is NULL or not 4-byte aligned");
   const bool bf16 = p->dtype == ATTN_BF16;
-  const size_t need = kv4_attn_workspace(a, p->head_dim, bf16);
+  const size_t need = attention_workspace(a, p->head_dim, bf16);
   if (need && !workspace) return kfail(ATTN_ERR_WORKSPACE, "workspace is NULL but %zu bytes are needed", need);
   if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return kfail(ATTN_ERR_WORKSPACE, "workspace is not 256-byte aligned");
@@ -472,7 +476,9 @@ attn_status_t attn_fwd_kv4(const attn_kv4_params_t* p, const void* x, const void
   a.ks = static_cast<uint32_t*>(const_cast<void*>(k_scale));
   a.vc = static_cast<uint8_t*>(const_cast<void*>(v_codes));
   a.vs = static_cast<uint32_t*>(const_cast<void*>(v_scale));
-  return launch_status(launch_kv4_attn(a, p->head_dim, bf16, workspace, static_cast<cudaStream_t>(stream)),
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(kv4_many_rows(a, p->head_dim, bf16) ? launch_kv4_rows(a, p->head_dim, workspace, wait_ns, st)
+                                                           : launch_kv4_attn(a, p->head_dim, bf16, workspace, st),
                        "cache attention launch");
 }
 

@@ -91,8 +91,16 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 cudaError_t launch_kv4_write(const Kv4Args& a, int head_dim, bool bf16, cudaStream_t st);
 cudaError_t launch_kv4_read(const Kv4Args& a, int head_dim, bool bf16, cudaStream_t st);
 
-// Attention over the cache: device scratch for these shapes, and the launch.
+// Attention over the cache: device scratch for these shapes, and the launch.  Few query
+// rows on a KV head: any type and head dim.  Many: bf16, head dim 64 or 128.
 size_t kv4_attn_workspace(const Kv4Args& a, int head_dim, bool bf16);
 cudaError_t launch_kv4_attn(const Kv4Args& a, int head_dim, bool bf16, void* workspace, cudaStream_t st);
+size_t kv4_rows_workspace(const Kv4Args& a, int head_dim);
+cudaError_t launch_kv4_rows(const Kv4Args& a, int head_dim, void* workspace, unsigned long long wait_ns, cudaStream_t st);
+
+// Which of the two: the tcgen05 kernel from 17 rows on.
+inline bool kv4_many_rows(const Kv4Args& a, int head_dim, bool bf16) {
+  return bf16 && head_dim <= 128 && (long long)a.seqlen * a.group > 16;
+}
 
 }  // namespace gbattn

@@ -31,7 +31,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "kv4.h"
+#include "kv4_line.cuh"
 #include "ptx.cuh"
 
 namespace gbattn {
@@ -39,37 +39,12 @@ namespace gbattn {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;  // each warp joins and stores a quarter of a row tile's sums
-constexpr int kSms = 152;  // a fixed count, so that the workspace size needs no device query
-
-// n / d for 0 <= n < 2^31: (n * mul) >> shift with mul = floor(2^shift / d) + 1.
-struct FastDiv {
-  uint32_t mul, shift;
-};
-FastDiv fast_div(int d) {
-  int l = 0;
-  while ((1ll << l) < d) ++l;
-  return {(uint32_t)((1ull << (31 + l)) / (uint32_t)d + 1), (uint32_t)(31 + l)};
-}
-__device__ __forceinline__ int div_by(int n, FastDiv d) {
-  return (int)(((unsigned long long)(uint32_t)n * d.mul) >> d.shift);
-}
 
 constexpr int kLeastUnit = -119;  // 2^(7 - unit) is a float32
-constexpr int kNoRow = 0x7FFFFFFF;  // the limit of a column without a query: it masks nothing
 
 // What a row tile costs beside its keys (queries into operands, the warps' results
 // joined), in tiles: the line has that many empty places before a row tile's keys.
 constexpr int kEmpty = 6;
-
-struct AttnArgs {
-  Kv4Args a;
-  FastDiv page_div;
-  float* part_o;   // [blocks][2][row tile's accumulators]
-  float* part_ml;  // [blocks][2][rows][2]: row maximum (log2 units) and sum
-  // [blocks]: the row tile whose keys begin in the block's stretch and end in block
-  // w's: (sequence, KV head, row tile, w); w = -1: there is none
-  int4* shared;
-};
 
 template <int D, int NT, bool F32>
 struct Shape {
@@ -121,14 +96,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float f16_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)w)); }
-__device__ __forceinline__ float f16_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
 __device__ __forceinline__ uint32_t add_f16(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // N values of a query row.
 template <int N>
@@ -187,133 +159,10 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A sequence's share of the line: heads_kv * row tiles * (kEmpty + key tiles).  A row
-// tile has one tile at least, so that rows that see nothing are written too.
-struct SeqWork {
-  Kv4Seq s;
-  int row_tiles, key_tiles;
-  __device__ __forceinline__ int places() const { return key_tiles + kEmpty; }  // of a row tile in the line
-};
-template <int R, int KT>
-__device__ __forceinline__ SeqWork seq_work(const Kv4Args& a, int b) {
-  SeqWork w;
-  w.s = kv4_seq(a, b);
-  w.row_tiles = (int)(((long long)w.s.n * a.group + R - 1) / R);
-  w.key_tiles = max(1, (w.s.len + (KT - 1)) / KT);
-  return w;
-}
-
-// The block whose stretch holds tile x of `total` tiles cut over n <= total blocks
-// (block i: i * total / n up to (i + 1) * total / n).
-__device__ __forceinline__ int owner(long long x, long long total, long long n) {
-  return (int)(((x + 1) * n - 1) / total);
-}
-
-// Inclusive prefix sums over the block's threads.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
-  }
-  *total = all;
-  return v + before;
-}
-
-// This block's stretch [*tile, *tile_end) of the line, the sequence that holds its
-// first tile and the first of that sequence's tiles.  The line has as many
-// stretches as there are blocks, or tiles where those are fewer: none is empty.
-// Returns the number of stretches, 0 to a block that has none; *total: the line's places.
-template <int R, int KT>
-__device__ __forceinline__ long long find_stretch(const Kv4Args& a, long long* tile, long long* tile_end, long long* total,
-                                                  int* seq, long long* first) {
-  __shared__ long long warp_sums[kWarps];
-  __shared__ long long found_first;
-  __shared__ int found_seq;
-  long long all = 0;
-  const bool one_pass = a.batch <= kThreads;
-  long long mine = 0, incl = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    mine = 0;
-    if (b < a.batch) {
-      const SeqWork w = seq_work<R, KT>(a, b);
-      mine = (long long)a.heads_kv * w.row_tiles * w.places();
-    }
-    long long sum;
-    incl = block_scan(mine, warp_sums, &sum);
-    all += sum;
-  }
-  const long long n = min(all, (long long)gridDim.x);
-  if (blockIdx.x >= n) return 0;
-  *total = all;
-  const long long want = blockIdx.x * all / n;
-  *tile = want;
-  *tile_end = (blockIdx.x + 1) * all / n;
-  long long before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    if (!one_pass) {
-      mine = 0;
-      if (b < a.batch) {
-        const SeqWork w = seq_work<R, KT>(a, b);
-        mine = (long long)a.heads_kv * w.row_tiles * w.places();
-      }
-      long long sum;
-      incl = block_scan(mine, warp_sums, &sum) + before;
-      before += sum;
-    }
-    if (b < a.batch && want < incl && want >= incl - mine) {
-      found_seq = b;
-      found_first = incl - mine;
-    }
-  }
-  __syncthreads();
-  *seq = found_seq;
-  *first = found_first;
-  return n;
-}
-
-// Where a row tile's query rows lie: row r of the tile is query row r0 + r of the
-// (sequence, KV head), token (r0 + r) / group, head h * group + (r0 + r) % group.
-struct RowPlace {
-  int token, head;
-};
-__device__ __forceinline__ RowPlace row_place(const Kv4Args& a, int h, int row) {
-  RowPlace p;
-  p.token = row / a.group;
-  p.head = h * a.group + (row - p.token * a.group);
-  return p;
-}
-__device__ __forceinline__ long long x_row(const Kv4Args& a, const Kv4Seq& s, int b, RowPlace p) {
-  return (a.cu ? (s.row0 + p.token) * a.x_ss : b * a.x_sb + p.token * a.x_ss) + p.head * a.x_sh;
-}
-__device__ __forceinline__ long long y_row(const Kv4Args& a, const Kv4Seq& s, int b, RowPlace p) {
-  return (a.cu ? (s.row0 + p.token) * a.y_ss : b * a.y_sb + p.token * a.y_ss) + p.head * a.y_sh;
-}
-__device__ __forceinline__ long long lse_row(const Kv4Args& a, const Kv4Seq& s, int b, RowPlace p) {
-  return a.cu ? (long long)p.head * a.total + s.row0 + p.token
-              : ((long long)b * a.heads_q + p.head) * a.seqlen + p.token;
-}
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
   *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y);
 }
 __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
-
-// One row's log of the sum: m in log2 units.  A row that saw nothing has l = 0.
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
 
 // Stores a 16 by 8 tile of a row tile's accumulators: accumulator e of tile j = (g, mt, nt) stands for row nt * 8 + 2 t + e % 2 and
 // value 64 g + 8 (lane / 4) + 2 mt + e / 2 of the head.
@@ -349,12 +198,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  long long tile, tile_end, total, first;
-  int b;
-  const long long n = find_stretch<R, KT>(a, &tile, &tile_end, &total, &b, &first);
+  Line<R, KT, kEmpty, kWarps> line;
+  const bool any = line.begin(a);
   if (threadIdx.x == 0) args.shared[blockIdx.x] = make_int4(0, 0, 0, -1);
-  if (n == 0) return;
-  SeqWork w = seq_work<R, KT>(a, b);
+  if (!any) return;
   const float q_sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
 
   // Copies into a warp's ring, 16 bytes a lane: codes in order, and the scales of a tile by
@@ -373,34 +220,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   const uint32_t v_lane0 = 8 * D + ((2 * t4) ^ (t4 & 1)) * (D / 2) + g8 * (4 * G);
   const uint32_t v_lane1 = 8 * D + ((2 * t4 + 1) ^ (t4 & 1)) * (D / 2) + g8 * (4 * G);
 
-  while (tile < tile_end) {
-    // skip to the sequence that holds the tile
-    while (tile - first >= (long long)a.heads_kv * w.row_tiles * w.places()) {
-      if (b + 1 >= a.batch) return;  // lengths that changed under the kernel
-      first += (long long)a.heads_kv * w.row_tiles * w.places();
-      w = seq_work<R, KT>(a, ++b);
-    }
-    const int in_seq = (int)((tile - first) / w.places());  // (head, row tile)
-    const int at = (int)(tile - first - (long long)in_seq * w.places());
-    const int t0 = max(at - kEmpty, 0), t1 = (int)min((long long)w.key_tiles, at - kEmpty + (tile_end - tile));
-    const int h = in_seq / w.row_tiles, r0 = (in_seq - h * w.row_tiles) * R;
-    const int rows = w.s.n * a.group;  // of the (sequence, KV head)
-    tile += w.places() - at;
-    if (t1 <= 0) break;  // the stretch ends before the row tile's keys
-    // keys that any of the tile's rows sees, and that all of them see
-    int klen, all_see;
-    {
-      const int low = w.s.len - w.s.n + r0 / a.group, high = w.s.len - w.s.n + (min(r0 + R, rows) - 1) / a.group;
-      klen = high < 0 ? 0 : a.causal ? high + 1 : w.s.len;
-      all_see = low < 0 ? 0 : a.causal ? low + 1 : w.s.len;
-    }
-
+  typename Line<R, KT, kEmpty, kWarps>::Piece p;
+  while (line.next(a, &p)) {
+    const int b = p.b, h = p.h, r0 = p.r0, rows = p.rows, t0 = p.t0, t1 = p.t1, klen = p.klen, all_see = p.all_see;
     // ---- keys: where they lie, and the first loads
-    // This warp's tiles end where no row sees its keys; a cache without a page shows none.
-    if (a.n_pages == 0 && klen > 0) {
-      set_status(a.status, kStatusBounds);
-      klen = 0;
-    }
+    // This warp's tiles end where no row sees its keys.
     const int te = klen > warp * CH * 16 ? min(t1, (klen - warp * CH * 16 + KT - 1) / KT) : 0;
     // Chunks of 16 keys, each in one page, in batches of 8: lane 4 x knows chunk x's row of
     // the cache.  Where the page is none, or no row sees the chunk, a row that does exist
@@ -458,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
     for (int y = 0; y < R / kWarps; ++y)
       if (r0 + y * kWarps + warp < rows)
-        load_q(q[y], static_cast<const T*>(a.x) + x_row(a, w.s, b, row_place(a, h, r0 + y * kWarps + warp)) + lane * E);
+        load_q(q[y], static_cast<const T*>(a.x) + x_row(a, p.s, b, row_place(a, h, r0 + y * kWarps + warp)) + lane * E);
 #pragma unroll
     for (int y = 0; y < R / kWarps; ++y) {
       const int r = y * kWarps + warp;
@@ -480,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         row_f[r] = a.scale_log2 != 0.f
                        ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), 24 + ex), 1.17549435e-38f), 3.40282347e38f)
                        : 1.f;
-        const int pos = w.s.len - w.s.n + (r0 + r) / a.group;
-        row_lim[r] = r0 + r >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : w.s.len;
+        const int pos = p.s.len - p.s.n + (r0 + r) / a.group;
+        row_lim[r] = r0 + r >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
       }
       // 2^-ex in two factors that are float32 numbers for every ex
       const float up = pow2(-ex / 2), up2 = pow2(-ex - -ex / 2);
@@ -628,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
               for (int e = 0; e < 2; ++e)
                 if (dead || key >= row_lim[nt * 8 + 2 * t4 + e]) x[c][nt][2 * y + e] = -INFINITY;
-            if (dead || key >= w.s.len) {  // what no position holds may be anything: not into the sums
+            if (dead || key >= p.s.len) {  // what no position holds may be anything: not into the sums
 #pragma unroll
               for (int g = 0; g < G; ++g) vsw[c][y][g] = 0;
             }
@@ -727,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
               for (int part = 0; part < PP; ++part) {
                 const uint32_t v = pack_f16(p0, p1);
                 pb[part][nt][y] = transpose8(v);
-                if (part + 1 < PP) p0 -= f16_lo(v), p1 -= f16_hi(v);
+                if (part + 1 < PP) p0 -= half_lo(v), p1 -= half_hi(v);
               }
             }
           }
@@ -820,11 +644,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
       for (int e = 0; e < 4; ++e)
         merge[(warp * S::ACC + j * 4 + e) * 32 + lane] = acc[j / NT / 4][j / NT % 4][j % NT][e];
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == w.key_tiles;
-    if (t0 == 0 && !whole && threadIdx.x == 0) {
-      const long long last = first + (long long)(in_seq + 1) * w.places() - 1;
-      args.shared[blockIdx.x] = make_int4(b, h, r0 / R, (int)owner(last, total, n));
-    }
+    const bool whole = p.whole;
+    if (t0 == 0 && !whole && threadIdx.x == 0)
+      args.shared[blockIdx.x] = make_int4(b, h, r0 / R, line.owner(p.last, line.total, line.n));
     const long long slot = blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
 #pragma unroll
     for (int jj = 0; jj < G * NT; ++jj) {
@@ -837,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int y = 0; y < kWarps; ++y) v[e] += merge[(y * S::ACC + j * 4 + e) * 32 + lane];
       }
       if (whole) {
-        store_tile<T, NT>(a, w.s, b, h, r0, rows, j, v, rl[j % NT], lane);
+        store_tile<T, NT>(a, p.s, b, h, r0, rows, j, v, rl[j % NT], lane);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) args.part_o[(slot * S::ACC + j * 4 + e) * 32 + lane] = v[e];
@@ -850,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int e = 0; e < 2; ++e) {
           const int r = nt * 8 + 2 * t4 + e;
           if (whole) {
-            if (r0 + r < rows) a.lse[lse_row(a, w.s, b, row_place(a, h, r0 + r))] = row_lse(rm[nt][e], rl[nt][e]);
+            if (r0 + r < rows) a.lse[lse_row(a, p.s, b, row_place(a, h, r0 + r))] = row_lse(rm[nt][e], rl[nt][e]);
           } else {
             args.part_ml[(slot * R + r) * 2] = rm[nt][e];
             args.part_ml[(slot * R + r) * 2 + 1] = rl[nt][e];
