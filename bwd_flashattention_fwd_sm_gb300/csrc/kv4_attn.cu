@@ -803,16 +803,16 @@ struct Launch {
   }
 };
 
-// Row tiles of 8, 16, 24 or 32 queries: the least that hold all of a KV head's, else the
+// Row tiles of 8, 16 or 24 queries: the least that hold all of a KV head's, else the
 // widest that the registers hold (accumulators: D / 16 * 4 a lane and 8 queries).
+// More bf16 rows than 24 at head dim 64 and 128 are the tcgen05 kernel's.
 template <class T, int D, class F>
 auto with_width(const Kv4Args& a, F&& f) {
-  constexpr int kMost = D == 256 || sizeof(T) == 4 ? 2 : 4;
+  constexpr bool kThree = D <= 128 && sizeof(T) == 2;
   const long long rows = (long long)a.seqlen * a.group;
   if (rows <= 8) return f(Launch<T, D, 1>());
-  if (rows <= 16 || kMost == 2) return f(Launch<T, D, 2>());
-  if (rows <= 24) return f(Launch<T, D, kMost == 2 ? 2 : 3>());
-  return f(Launch<T, D, kMost>());
+  if (rows <= 16 || !kThree) return f(Launch<T, D, 2>());
+  return f(Launch<T, D, kThree ? 3 : 2>());
 }
 template <class F>
 auto with_shape(const Kv4Args& a, int head_dim, bool bf16, F&& f) {

@@ -16,10 +16,10 @@
 // most) and multiply V group by group; the offsets' part sum(p b_g) and the row sums
 // stay in float32.
 //
-// Eight warps do the softmax, two for each 32 rows with half of the keys each; the
-// scores of tile t + 1 are computed while they work on tile t.  The running maximum is
-// raised only when a score is above it by more than 2^8; the two warps of a row agree
-// on that with one barrier a tile.  What bounds it: about 14 instructions an element
+// Sixteen warps do the softmax, four for each 32 rows with a quarter of the keys each;
+// the scores of tile t + 1 are computed while they work on tile t.  The running maximum
+// is raised only when a score is above it by more than 2^8; the four warps of a row
+// agree on that with one barrier a tile.  What bounds it: about 14 instructions an element
 // in the softmax warps, against 4 D of a product's operations.  Blocks share the work
 // by equal stretches of one line of tiles, as for few rows (kv4_attn.cu).
 #include <algorithm>
@@ -33,8 +33,13 @@ namespace gbattn {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128, kSpare = 2;  // kSpare: what a row tile costs beside its keys, in tiles
-constexpr int kSoftWarps = 8, kUnpackWarps = 4, kWarps = kSoftWarps + kUnpackWarps + 1;
+constexpr int kParts = 4, kPart = kKeys / kParts;  // warps of a row, and the keys of each
+// four warps of each 32 rows, four that unpack, and four of which one issues the products
+constexpr int kSoftWarps = 4 * kParts, kUnpackWarps = 4, kWarps = kSoftWarps + kUnpackWarps + 4;
 constexpr int kThreads = kWarps * 32;
+// Registers: 80 a thread at launch; what the issuing warps give up the softmax warps take
+// (512 * 88 + 128 * 80 + 128 * 40 <= 768 * 80).
+constexpr int kSoftRegs = 88, kIssueRegs = 56;
 
 template <int D>
 struct Smem {
@@ -42,12 +47,12 @@ struct Smem {
   uint8_t q[G][kRows * 128];  // float16, 128-byte rows, 128-byte swizzle
   uint8_t k[2][G][kKeys * 128];
   uint8_t v[2][G][kKeys * 128];
-  float2 ksz[2][G][kKeys];  // (s, b - 8 s) of a key's group
-  float2 vsb[2][G][kKeys];  // (s, b)
+  float4 ksz[2][G][kKeys / 2];  // s and b - 8 s of two neighbouring keys' groups: (s, s, z, z)
+  float4 vsb[2][G][kKeys / 2];  // (s, s, b, b)
   uint8_t dead[2][kKeys];   // the key has no page
   uint32_t bad[2];          // a byte for each unpacking warp: it has a dead key
-  float top[2][kRows];      // row maxima of the two halves of the keys
-  float sums[2][kRows][1 + G];
+  float top[kParts][kRows];  // row maxima over the parts of the keys
+  float sums[kParts][kRows][1 + G];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_free, p_full, pv_done, drain;
   ptx::Abort abort;
   uint32_t tmem;
@@ -69,21 +74,49 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {  // float16 ope
 // Tiles of a piece that any of its rows sees.
 __device__ __forceinline__ int piece_end(const TcLine::Piece& p) { return min(p.t1, (p.klen + kKeys - 1) / kKeys); }
 
-// Whether any lane of the two warps that share 32 rows says so (a barrier of both).
-__device__ __forceinline__ bool pair_any(int id, bool x) {
+// Whether any lane of the four warps that share 32 rows says so (a barrier of all four).
+__device__ __forceinline__ bool rows_any(int id, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)x), "r"(id)
       : "memory");
   return r != 0;
 }
-// A warp that gives up does not leave its partner waiting: the partner's barrier ends, and it
-// sees the flag.
-__device__ __forceinline__ void pair_leave(int id) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(id) : "memory"); }
+// A warp that gives up does not leave the others waiting: their barrier ends, and they see
+// the flag.
+__device__ __forceinline__ void rows_leave(int id) { asm volatile("barrier.cta.arrive %0, 128;" ::"r"(id) : "memory"); }
+
+// Two float32 numbers at a time.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float x, float y) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 apart(Two x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two x, Two y, Two z) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two x, Two y) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two x, Two y) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -95,6 +128,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+__device__ __forceinline__ void fetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- unpacking
 template <int D>
@@ -109,37 +144,54 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, T
     const int* table = a.table + p.b * a.table_stride;
     uint4 kw[W / 4], vw[W / 4];
     uint32_t ks[G], vs[G];
-    bool none = false, none_next = false;
     auto id_of = [&](int t) {
       const int pos = t * kKeys + key;
       return t < te && pos < p.s.len ? table[div_by(pos, args.page_div)] : -2;
     };
-    auto load = [&](int t, int id) {  // this thread's key of tile t: what is no position, or has no page, gets zeros
+    // This thread's key of a tile: its row of the cache, none for what is no position or has no page.
+    constexpr unsigned long long kNone = ~0ull;
+    auto row_of = [&](int t, int id) {
       const int pos = t * kKeys + key, pg = div_by(pos, args.page_div);
       const bool ok = (unsigned)id < (unsigned)a.n_pages;
-      none_next = !ok;
       if (!ok && id != -2) set_status(a.status, kStatusBounds);
+      return ok ? ((unsigned long long)id * a.heads_kv + p.h) * a.page + (pos - pg * a.page) : kNone;
+    };
+    auto load = [&](const uint8_t* codes, const uint32_t* scale, unsigned long long row, uint4 (&w)[W / 4], uint32_t (&sc)[G]) {
 #pragma unroll
-      for (int i = 0; i < W / 4; ++i) kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < W / 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int g = 0; g < G; ++g) ks[g] = vs[g] = 0;
-      if (ok) {
-        const unsigned long long row = ((unsigned long long)id * a.heads_kv + p.h) * a.page + (pos - pg * a.page);
-        const uint4* kp = reinterpret_cast<const uint4*>(a.kc + row * (D / 2));
-        const uint4* vp = reinterpret_cast<const uint4*>(a.vc + row * (D / 2));
+      for (int g = 0; g < G; ++g) sc[g] = 0;
+      if (row != kNone) {
+        const uint4* from = reinterpret_cast<const uint4*>(codes + row * (D / 2));
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) kw[i] = __ldg(kp + i), vw[i] = __ldg(vp + i);
+        for (int i = 0; i < W / 4; ++i) w[i] = __ldg(from + i);
 #pragma unroll
-        for (int g = 0; g < G; ++g) ks[g] = __ldg(a.ks + row * G + g), vs[g] = __ldg(a.vs + row * G + g);
+        for (int g = 0; g < G; ++g) sc[g] = __ldg(scale + row * G + g);
       }
     };
-    int id = id_of(p.t0);
-    if (p.t0 < te) load(p.t0, id);
-    id = id_of(p.t0 + 1);
+    unsigned long long row = kNone, next_row = kNone;
+    if (p.t0 < te) {
+      const int id0 = id_of(p.t0);
+      int id1 = id_of(p.t0 + 1);
+      row = row_of(p.t0, id0);
+      load(a.kc, a.ks, row, kw, ks);
+      load(a.vc, a.vs, row, vw, vs);
+      next_row = row_of(p.t0 + 1, id1);
+    }
+    int id = id_of(p.t0 + 2);
     for (int t = p.t0; t < te; ++t, ++n) {
       const uint32_t st = n & 1, ph = (n >> 1) & 1;
-      none = none_next;
+      const bool none = row == kNone;
       const uint32_t any_none = __ballot_sync(0xffffffffu, none);
+      row = next_row;  // the next tile's
+      if (t + 2 < te) {
+        next_row = row_of(t + 2, id);
+        if (next_row != kNone) {  // on its way to L2
+          fetch_l2(a.kc + next_row * (D / 2));
+          fetch_l2(a.vc + next_row * (D / 2));
+        }
+        id = id_of(t + 3);
+      }
       if (n >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait(&sm.k_empty[st], ph ^ 1, &sm.abort, a.status, args.wait_ns)))
         return false;
       const uint32_t* w = reinterpret_cast<const uint32_t*>(kw);  // word (i, g) at i * G + g
@@ -153,13 +205,15 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, T
               make_uint4(x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
         }
         const float s = bf16_lo(ks[g]);
-        sm.ksz[st][g][key] = make_float2(s, fmaf(-8.f, s, bf16_hi(ks[g])));
+        float* sz = reinterpret_cast<float*>(&sm.ksz[st][g][key >> 1]) + (key & 1);
+        sz[0] = s, sz[2] = fmaf(-8.f, s, bf16_hi(ks[g]));
       }
       sm.dead[st][key] = none ? 1 : 0;
       if (lane == 0) reinterpret_cast<uint8_t*>(&sm.bad[st])[warp] = any_none ? 1 : 0;
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.k_full[st]);
+      if (t + 1 < te) load(a.kc, a.ks, row, kw, ks);
 
       if (n >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait(&sm.v_empty[st], ph ^ 1, &sm.abort, a.status, args.wait_ns)))
         return false;
@@ -176,15 +230,13 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, T
             u[k] = add_bf16x2(((x >> (4 * k)) & 0x000F000Fu) | 0x43004300u, 0xC308C308u);
           *reinterpret_cast<uint4*>(row + ((i ^ (key & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        sm.vsb[st][g][key] = make_float2(bf16_lo(vs[g]), bf16_hi(vs[g]));
+        float* sb = reinterpret_cast<float*>(&sm.vsb[st][g][key >> 1]) + (key & 1);
+        sb[0] = bf16_lo(vs[g]), sb[2] = bf16_hi(vs[g]);
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.v_full[st]);
-      if (t + 1 < te) {
-        load(t + 1, id);
-        id = id_of(t + 2);
-      }
+      if (t + 1 < te) load(a.vc, a.vs, row, vw, vs);
     }
   }
   return true;
@@ -199,15 +251,17 @@ __device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, &sm.abort, a.status, args.wait_ns));
   };
+  const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.q[0]), 16, 1024), k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.k[0][0]), 16, 1024);
+  const uint64_t v_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.v[0][0]), 16384, 1024);
   auto scores = [&](uint32_t st) {
     ptx::tc_fence_after();
     if (ptx::elect_one()) {
+      const uint64_t kd = k_desc + st * (G * 1024);
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_ss(tmem + Tmem<D>::S + g * 128, ptx::sdesc_sw128(ptx::smem_u32(sm.q[g]) + kk * 32, 16, 1024),
-                      ptx::sdesc_sw128(ptx::smem_u32(sm.k[st][g]) + kk * 32, 16, 1024), kS, kk > 0 ? 1u : 0u);
+          ptx::mma_ss(tmem + Tmem<D>::S + g * 128, q_desc + g * 1024 + kk * 2, kd + g * 1024 + kk * 2, kS, kk > 0 ? 1u : 0u);
       ptx::mma_commit(&sm.s_full);
       ptx::mma_commit(&sm.k_empty[st]);
     }
@@ -237,7 +291,7 @@ __device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, 
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             ptx::mma_ts(tmem + Tmem<D>::O + g * 64, tmem + Tmem<D>::P + g * 64 + kk * 8,
-                        ptx::sdesc_sw128(ptx::smem_u32(sm.v[st][g]) + kk * 2048, 16384, 1024), kPV,
+                        v_desc + st * (G * 1024) + g * 1024 + kk * 128, kPV,
                         t > p.t0 || kk > 0 ? 1u : 0u);
         ptx::mma_commit(&sm.pv_done);
         ptx::mma_commit(&sm.v_empty[st]);
@@ -252,19 +306,19 @@ __device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, 
 template <int D>
 __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, TcLine line, uint32_t tmem, int warp,
                                              int lane) {
-  constexpr int G = D / kKv4Group, NV = D / 2;  // NV: a thread's values of its row, and its columns of O
+  constexpr int G = D / kKv4Group, NV = D / kParts;  // NV: a thread's values of its row, and its columns of O
   const Kv4Args& a = args.a;
-  const int half = warp >> 2, row = (warp & 3) * 32 + lane, id = 1 + (warp & 3);
+  const int part = warp >> 2, row = (warp & 3) * 32 + lane, id = 1 + (warp & 3);
   const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes of tensor memory
   const float q_sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, &sm.abort, a.status, args.wait_ns))) return true;
-    pair_leave(id);
+    rows_leave(id);
     return false;
   };
   auto gone = [&]() {
     if (!__any_sync(0xffffffffu, sm.abort.flag != 0)) return false;
-    pair_leave(id);
+    rows_leave(id);
     return true;
   };
   auto arrive = [&](uint64_t* bar) {
@@ -278,14 +332,30 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     const RowPlace pl = row_place(a, p.h, min(grow, p.rows - 1));
     const int pos = p.s.len - p.s.n + pl.token;
     const int lim = grow >= p.rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
-    float rf = 1.f, rz[G], l = 0.f, off[G], mu = 0.f, bar = -INFINITY;
+    if (p.r0 + (warp & 3) * 32 >= p.rows) {
+      // No query in this warp's rows: what stands in their lanes is never read.  It keeps
+      // step with the others: a tile's arrivals come after the end of the last one's.
+      if (p.t0 < te) arrive(&sm.q_full);
+      for (int t = p.t0; t < te; ++t, ++n) {
+        const uint32_t st = n & 1;
+        if (!wait(&sm.s_full, n & 1)) return false;
+        arrive(&sm.s_free);
+        arrive(&sm.k_empty[st]);
+        if (n > 0 && !wait(&sm.pv_done, (n - 1) & 1)) return false;
+        arrive(&sm.p_full);
+        arrive(&sm.v_empty[st]);
+      }
+      continue;
+    }
+    float rf = 1.f, rz[G], mu = 0.f, bar = -INFINITY;
+    Two l = 0, off[G];  // sums over even and odd keys
 #pragma unroll
-    for (int g = 0; g < G; ++g) rz[g] = off[g] = 0.f;
+    for (int g = 0; g < G; ++g) rz[g] = 0.f, off[g] = 0;
 
     if (p.t0 < te) {
-      // Q: half of this thread's row into its operand
+      // Q: a quarter of this thread's row into its operand
       uint4 raw[NV / 8];
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.x) + x_row(a, p.s, b, pl) + half * NV;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.x) + x_row(a, p.s, b, pl) + part * NV;
       float big = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NV / 8; ++i) {
@@ -298,20 +368,20 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
           sum += x + y;
         }
       }
-      sm.top[half][row] = big;
-      sm.sums[half][row][0] = sum;
-      pair_any(id, false);
+      sm.top[part][row] = big;
+      sm.sums[part][row][0] = sum;
+      rows_any(id, false);
       if (gone()) return false;
-      big = fmaxf(sm.top[0][row], sm.top[1][row]);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        big = fmaxf(big, sm.top[i][row]);
+        rz[i * G / kParts] += sm.sums[i][row][0];
+      }
       int ex = 0;  // |q| < 2^ex: scaled below 2^14
       if (big > 0.f && big < INFINITY) frexpf(big, &ex);
       ex -= 14;
-      if constexpr (G == 2) {
-        rz[0] = ldexpf(sm.sums[0][row][0], -(24 + ex));
-        rz[G - 1] = ldexpf(sm.sums[1][row][0], -(24 + ex));
-      } else {
-        rz[0] = ldexpf(sm.sums[0][row][0] + sm.sums[1][row][0], -(24 + ex));
-      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) rz[g] = ldexpf(rz[g], -(24 + ex));
       // at least 2^-126, at most the largest float32: scores of 0 times it stay 0
       rf = a.scale_log2 != 0.f ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), 24 + ex), 1.17549435e-38f), 3.40282347e38f) : 1.f;
       const float up = pow2(-ex / 2) * q_sign, up2 = pow2(-ex - -ex / 2);
@@ -324,7 +394,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
           v[2 * e] = bf16_lo(w[e]) * up * up2;
           v[2 * e + 1] = bf16_hi(w[e]) * up * up2 * 0.0625f;
         }
-        const int word = half * (NV / 8) + i, g = word / 8, slot = word % 8;
+        const int word = part * (NV / 8) + i, g = word / 8, slot = word % 8;
         *reinterpret_cast<uint4*>(sm.q[g] + row * 128 + ((slot ^ (row & 7)) << 4)) =
             make_uint4(pack_f16x2(v[0], v[4]), pack_f16x2(v[1], v[5]), pack_f16x2(v[2], v[6]), pack_f16x2(v[3], v[7]));
       }
@@ -337,44 +407,54 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
       const uint32_t st = n & 1, ph = (n >> 1) & 1;
       if (!wait(&sm.s_full, n & 1) || !wait(&sm.k_full[st], ph)) return false;
       ptx::tc_fence_after();
-      float x[64];
+      Two x[kPart / 2];  // of two neighbouring keys
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t s0[32], s1[G == 2 ? 32 : 1];
-        ptx::tmem_ld32(lanes + Tmem<D>::S + half * 64 + c * 32, s0);
-        if constexpr (G == 2) ptx::tmem_ld32(lanes + Tmem<D>::S + 128 + half * 64 + c * 32, s1);
+      for (int c = 0; c < kPart; c += 16) {
+        uint32_t s0[16], s1[G == 2 ? 16 : 1];
+        ptx::tmem_ld16(lanes + Tmem<D>::S + part * kPart + c, s0);
+        if constexpr (G == 2) ptx::tmem_ld16(lanes + Tmem<D>::S + 128 + part * kPart + c, s1);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float4 z = *reinterpret_cast<const float4*>(&sm.ksz[st][0][half * 64 + c * 32 + j]);
-          float x0 = fmaf(z.x, __uint_as_float(s0[j]), z.y * rz[0]), x1 = fmaf(z.z, __uint_as_float(s0[j + 1]), z.w * rz[0]);
+        for (int j = 0; j < 16; j += 2) {
+          const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(&sm.ksz[st][0][(part * kPart + c + j) / 2]);
+          Two v = fma2(z.x, two(__uint_as_float(s0[j]), __uint_as_float(s0[j + 1])), mul2(z.y, two(rz[0], rz[0])));
           if constexpr (G == 2) {
-            const float4 y = *reinterpret_cast<const float4*>(&sm.ksz[st][G - 1][half * 64 + c * 32 + j]);
-            x0 = fmaf(y.x, __uint_as_float(s1[j]), fmaf(y.y, rz[G - 1], x0));
-            x1 = fmaf(y.z, __uint_as_float(s1[j + 1]), fmaf(y.w, rz[G - 1], x1));
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&sm.ksz[st][G - 1][(part * kPart + c + j) / 2]);
+            v = fma2(y.x, two(__uint_as_float(s1[j]), __uint_as_float(s1[j + 1])), fma2(y.y, two(rz[G - 1], rz[G - 1]), v));
           }
-          x[c * 32 + j] = x0, x[c * 32 + j + 1] = x1;
+          x[(c + j) / 2] = v;
         }
       }
       ptx::tc_fence_before();
       __syncwarp();
       arrive(&sm.s_free);
-      const int k0 = t * kKeys + half * 64;
-      if (k0 + 64 > p.all_see || sm.bad[st]) {  // keys that not all rows see
+      const uint32_t dead = sm.bad[st];
+      const int k0 = t * kKeys + part * kPart;
+      if (k0 + kPart > p.all_see || dead) {  // keys that not all rows see
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (k0 + j >= lim || sm.dead[st][half * 64 + j]) x[j] = -INFINITY;
+        for (int j = 0; j < kPart; j += 2) {
+          float2 v = apart(x[j / 2]);
+          if (k0 + j >= lim || sm.dead[st][part * kPart + j]) v.x = -INFINITY;
+          if (k0 + j + 1 >= lim || sm.dead[st][part * kPart + j + 1]) v.y = -INFINITY;
+          x[j / 2] = two(v.x, v.y);
+        }
       }
+      __syncwarp();
+      arrive(&sm.k_empty[st]);
       float high = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) high = fmax3f(high, x[j], x[j + 1]);
-      const bool raise = pair_any(id, high > bar);
+      for (int j = 0; j < kPart / 2; ++j) {
+        const float2 v = apart(x[j]);
+        high = fmax3f(high, v.x, v.y);
+      }
+      const bool raise = rows_any(id, high > bar);
       if (gone()) return false;
       if (raise) {
-        sm.top[half][row] = high;
-        pair_any(id, false);
+        sm.top[part][row] = high;
+        rows_any(id, false);
         if (gone()) return false;
-        high = fmaxf(sm.top[0][row], sm.top[1][row]);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) high = fmaxf(high, sm.top[i][row]);
         float f = 1.f;
         if (high > -INFINITY) {
           high *= rf;
@@ -385,87 +465,87 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
           mu = high;
           bar = (high + 8.f) / rf;
         }
-        l *= f;
+        l = mul2(l, two(f, f));
 #pragma unroll
-        for (int g = 0; g < G; ++g) off[g] *= f;
+        for (int g = 0; g < G; ++g) off[g] = mul2(off[g], two(f, f));
         if (t > p.t0 && __any_sync(0xffffffffu, f != 1.f)) {
           if (!wait(&sm.pv_done, (n - 1) & 1)) return false;
           ptx::tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < NV / 32; ++c) {
-            uint32_t o[32];
-            ptx::tmem_ld32(lanes + Tmem<D>::O + half * NV + c * 32, o);
+          for (int c = 0; c < NV; c += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(lanes + Tmem<D>::O + part * NV + c, o);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            ptx::tmem_st32(lanes + Tmem<D>::O + half * NV + c * 32, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            ptx::tmem_st16(lanes + Tmem<D>::O + part * NV + c, o);
           }
           ptx::tmem_st_wait();
         }
       }
       if (!wait(&sm.v_full[st], ph) || (n > 0 && !wait(&sm.pv_done, (n - 1) & 1))) return false;
       ptx::tc_fence_after();
-      // weights, 32 keys at a time
+      uint32_t w[G][kPart / 2];  // weights
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[G][16];
+      for (int j = 0; j < kPart / 2; ++j) {
+        const float2 v = apart(fma2(x[j], two(rf, rf), two(-mu, -mu)));
+        const Two pr = two(fast_exp2(v.x), fast_exp2(v.y));
+        l = add2(l, pr);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float p0 = fast_exp2(fmaf(x[c * 32 + j], rf, -mu)), p1 = fast_exp2(fmaf(x[c * 32 + j + 1], rf, -mu));
-          l += p0 + p1;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const float4 z = *reinterpret_cast<const float4*>(&sm.vsb[st][g][half * 64 + c * 32 + j]);
-            w[g][j / 2] = ptx::pack_bf16x2(p0 * z.x, p1 * z.z);
-            off[g] = fmaf(p1, z.w, fmaf(p0, z.y, off[g]));
-          }
+        for (int g = 0; g < G; ++g) {
+          const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(&sm.vsb[st][g][part * kPart / 2 + j]);
+          const float2 u = apart(mul2(pr, z.x));
+          w[g][j] = ptx::pack_bf16x2(u.x, u.y);
+          off[g] = fma2(pr, z.y, off[g]);
         }
-#pragma unroll
-        for (int g = 0; g < G; ++g) ptx::tmem_st16(lanes + Tmem<D>::P + g * 64 + half * 32 + c * 16, w[g]);
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g) ptx::tmem_st16(lanes + Tmem<D>::P + g * 64 + part * (kPart / 2), w[g]);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
       arrive(&sm.p_full);
-      arrive(&sm.k_empty[st]);
       arrive(&sm.v_empty[st]);
     }
 
-    // ---- the row's sums of both halves, and its result
-    sm.sums[half][row][0] = l;
+    // ---- the row's sums over all keys, and its result
+    sm.sums[part][row][0] = apart(l).x + apart(l).y;
 #pragma unroll
-    for (int g = 0; g < G; ++g) sm.sums[half][row][1 + g] = off[g];
-    pair_any(id, false);
+    for (int g = 0; g < G; ++g) sm.sums[part][row][1 + g] = apart(off[g]).x + apart(off[g]).y;
+    rows_any(id, false);
     if (gone()) return false;
-    l = sm.sums[0][row][0] + sm.sums[1][row][0];
-    const int g = G == 2 ? half : 0;
-    const float add = sm.sums[0][row][1 + g] + sm.sums[1][row][1 + g];
+    float sum = 0.f, add = 0.f;  // of p; of p b for this thread's columns
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      sum += sm.sums[i][row][0];
+      add += sm.sums[i][row][1 + part * G / kParts];
+    }
     if (p.t0 < te) {
       if (!wait(&sm.pv_done, (n - 1) & 1)) return false;
       ptx::tc_fence_after();
     }
     const float m = bar == -INFINITY ? -INFINITY : mu;
     const long long slot = (long long)blockIdx.x * 2 + (p.t0 == 0 ? 1 : 0);
-    const float inv = p.whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+    const float inv = p.whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f;
 #pragma unroll
-    for (int c = 0; c < NV / 32; ++c) {
-      uint32_t o[32];
+    for (int c = 0; c < NV; c += 16) {
+      uint32_t o[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = 0;
+      for (int j = 0; j < 16; ++j) o[j] = 0;
       if (p.t0 < te) {
-        ptx::tmem_ld32(lanes + Tmem<D>::O + half * NV + c * 32, o);
+        ptx::tmem_ld16(lanes + Tmem<D>::O + part * NV + c, o);
         ptx::tmem_ld_wait();
       }
       if (grow < p.rows) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {  // a word's values stand as 0, 4, 1, 5, 2, 6, 3, 7
+        for (int j = 0; j < 16; j += 8) {  // a word's values stand as 0, 4, 1, 5, 2, 6, 3, 7
           float v[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             v[e] = (__uint_as_float(o[j + 2 * e]) + add) * inv;
             v[e + 4] = (__uint_as_float(o[j + 2 * e + 1]) + add) * inv;
           }
-          const int d = half * NV + c * 32 + j;
+          const int d = part * NV + c + j;
           if (p.whole) {
             __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + y_row(a, p.s, b, pl) + d;
             *reinterpret_cast<uint4*>(y) = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
@@ -479,12 +559,12 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
       }
     }
     ptx::tc_fence_before();
-    if (half == 0 && grow < p.rows) {
+    if (part == 0 && grow < p.rows) {
       if (p.whole) {
-        a.lse[lse_row(a, p.s, b, pl)] = row_lse(m, l);
+        a.lse[lse_row(a, p.s, b, pl)] = row_lse(m, sum);
       } else {
         args.part_ml[(slot * kRows + row) * 2] = m;
-        args.part_ml[(slot * kRows + row) * 2 + 1] = l;
+        args.part_ml[(slot * kRows + row) * 2 + 1] = sum;
       }
     }
     if (warp == 0 && lane == 0 && p.t0 == 0 && !p.whole)
@@ -528,10 +608,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_rows(const __grid_constant_
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem;
   if (warp < kSoftWarps) {
+    ptx::regs_increase<kSoftRegs>();
     softmax_role<D>(args, sm, line, tmem, warp, lane);
   } else if (warp < kSoftWarps + kUnpackWarps) {
+    ptx::regs_decrease<72>();
     unpack_role<D>(args, sm, line, warp - kSoftWarps, lane);
   } else {
+    ptx::regs_decrease<kIssueRegs>();
+  }
+  if (warp == kWarps - 1) {
     product_role<D>(args, sm, line, tmem);
     // every product that was issued ends before the tensor memory is given back
     if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
