@@ -66,7 +66,11 @@ struct Shape {
   static constexpr int GRID = kSms * BLOCKS;
   static constexpr size_t Q_BYTES = (size_t)G * 4 * NT * QP * 32 * 8;
   static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4, RING_BYTES = (size_t)kWarps * STAGES * STAGE_BYTES;
-  static constexpr size_t SMEM = Q_BYTES + (MERGE_BYTES > RING_BYTES ? MERGE_BYTES : RING_BYTES);
+  // The joined sums have a place of their own where two blocks of an SM have room for it, else
+  // the rings'.
+  static constexpr bool OVER = BLOCKS * (Q_BYTES + MERGE_BYTES + RING_BYTES + 4096) > 227 * 1024;
+  static constexpr size_t SMEM =
+      Q_BYTES + (!OVER ? MERGE_BYTES + RING_BYTES : MERGE_BYTES > RING_BYTES ? MERGE_BYTES : RING_BYTES);
 };
 
 __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   const Kv4Args& a = args.a;
   extern __shared__ __align__(128) uint8_t smem[];
   uint2* qfrag = reinterpret_cast<uint2*>(smem);  // [g][s][part][nt][lane] (b0, b1)
-  float* merge = reinterpret_cast<float*>(smem + S::Q_BYTES);  // over the rings, between row tiles
+  float* merge = reinterpret_cast<float*>(smem + S::Q_BYTES + (S::OVER ? 0 : S::RING_BYTES));
   __shared__ __align__(16) float row_f[R], row_z[G][R];  // read in pairs
   __shared__ int row_lim[R];
   __shared__ float warp_m[kWarps][R], warp_l[kWarps][R];
@@ -220,95 +224,106 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   const uint32_t v_lane0 = 8 * D + ((2 * t4) ^ (t4 & 1)) * (D / 2) + g8 * (4 * G);
   const uint32_t v_lane1 = 8 * D + ((2 * t4 + 1) ^ (t4 & 1)) * (D / 2) + g8 * (4 * G);
 
-  typename Line<R, KT, kEmpty, kWarps>::Piece p;
-  while (line.next(a, &p)) {
-    const int b = p.b, h = p.h, r0 = p.r0, rows = p.rows, t0 = p.t0, t1 = p.t1, klen = p.klen, all_see = p.all_see;
-    // ---- keys: where they lie, and the first loads
+  // ---- a piece's keys: where they lie, and the first copies; and its queries
+  constexpr int kBatch = 8 / CH;  // tiles
+  constexpr int E = D / 32;
+  typename Line<R, KT, kEmpty, kWarps>::Piece next;
+  bool more = line.next(a, &next);
+  int t0 = 0, te = 0, klen = 0, h = 0, ids = 0;
+  const int* table = nullptr;
+  uint32_t rows_now = 0;
+  bool bad = false;  // a chunk's page was none
+  float q[R / kWarps][E];
+  // Chunks of 16 keys, each in one page, in batches of 8: lane 4 x knows chunk x's row of
+  // the cache.  Where the page is none, or no row sees the chunk, a row that does exist
+  // is copied in its place, and masked.
+  const int my_step = (lane >> 2) / CH, my_chunk = (lane >> 2) % CH;
+  auto key_of = [&](int t) { return min((t + my_step) * KT + (warp * CH + my_chunk) * 16, (klen - 1) & ~15); };
+  auto id_of = [&](int t) { return table[div_by(key_of(t), args.page_div)]; };
+  auto rows_of = [&](int t, int id) {
+    const int k0 = key_of(t), pg = div_by(k0, args.page_div);
+    const bool ok = (unsigned)id < (unsigned)a.n_pages;
+    if (!__all_sync(0xffffffffu, ok)) {
+      bad = true;
+      set_status(a.status, kStatusBounds);
+    }
+    return ((uint32_t)(ok ? id : 0) * a.heads_kv + h) * a.page + (k0 - pg * a.page);
+  };
+  auto issue = [&](int t) {  // tile t into its stage; tiles in order
+    const int x = (t - t0) % kBatch;
+    if (x == 0) {
+      rows_now = rows_of(t, ids);
+      ids = id_of(t + kBatch);
+    }
+    const uint32_t stage = (uint32_t)((t - t0) % ST) * S::STAGE_BYTES;
+    uint32_t row[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      row[c] = __shfl_sync(0xffffffffu, rows_now, (x * CH + c) * 4);
+      const uint8_t* k = k_from + (unsigned long long)row[c] * (D / 2);
+      const uint8_t* v = v_from + (unsigned long long)row[c] * (D / 2);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        copy16(to + stage + c * S::CHUNK_BYTES + i * 512, k + i * 512);
+        copy16(to + stage + c * S::CHUNK_BYTES + 8 * D + i * 512, v + i * 512);
+      }
+    }
+    if (CH * 8 * G >= 32 || lane < CH * 8 * G)
+      copy16(s_to + stage, s_from + (unsigned long long)(CH == 2 && lane >= 8 * G ? row[CH - 1] : row[0]) * (4 * G));
+  };
+  auto begin = [&]() {
+    h = next.h, t0 = next.t0, klen = next.klen, bad = false;
     // This warp's tiles end where no row sees its keys.
-    const int te = klen > warp * CH * 16 ? min(t1, (klen - warp * CH * 16 + KT - 1) / KT) : 0;
-    // Chunks of 16 keys, each in one page, in batches of 8: lane 4 x knows chunk x's row of
-    // the cache.  Where the page is none, or no row sees the chunk, a row that does exist
-    // is copied in its place, and masked.
-    constexpr int kBatch = 8 / CH;  // tiles
-    const int* table = a.table + b * a.table_stride;
-    const int my_step = (lane >> 2) / CH, my_chunk = (lane >> 2) % CH;
-    auto key_of = [&](int t) { return min((t + my_step) * KT + (warp * CH + my_chunk) * 16, (klen - 1) & ~15); };
-    auto id_of = [&](int t) { return table[div_by(key_of(t), args.page_div)]; };
-    bool bad = false;  // a chunk's page was none
-    auto rows_of = [&](int t, int id) {
-      const int k0 = key_of(t), pg = div_by(k0, args.page_div);
-      const bool ok = (unsigned)id < (unsigned)a.n_pages;
-      if (!__all_sync(0xffffffffu, ok)) {
-        bad = true;
-        set_status(a.status, kStatusBounds);
-      }
-      return ((uint32_t)(ok ? id : 0) * a.heads_kv + h) * a.page + (k0 - pg * a.page);
-    };
-    uint32_t rows_now = 0;
-    int ids = 0;
-    auto issue = [&](int t) {  // tile t into its stage; tiles in order
-      const int x = (t - t0) % kBatch;
-      if (x == 0) {
-        rows_now = rows_of(t, ids);
-        ids = id_of(t + kBatch);
-      }
-      const uint32_t stage = (uint32_t)((t - t0) % ST) * S::STAGE_BYTES;
-      uint32_t row[CH];
+    te = klen > warp * CH * 16 ? min(next.t1, (klen - warp * CH * 16 + KT - 1) / KT) : 0;
+    table = a.table + next.b * a.table_stride;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        row[c] = __shfl_sync(0xffffffffu, rows_now, (x * CH + c) * 4);
-        const uint8_t* k = k_from + (unsigned long long)row[c] * (D / 2);
-        const uint8_t* v = v_from + (unsigned long long)row[c] * (D / 2);
+    for (int y = 0; y < R / kWarps; ++y) {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          copy16(to + stage + c * S::CHUNK_BYTES + i * 512, k + i * 512);
-          copy16(to + stage + c * S::CHUNK_BYTES + 8 * D + i * 512, v + i * 512);
-        }
-      }
-      if (CH * 8 * G >= 32 || lane < CH * 8 * G)
-        copy16(s_to + stage, s_from + (unsigned long long)(CH == 2 && lane >= 8 * G ? row[CH - 1] : row[0]) * (4 * G));
-    };
-    __syncthreads();  // nobody still reads the last row tile's operands or sums
+      for (int e = 0; e < E; ++e) q[y][e] = 0.f;
+      const int row = next.r0 + y * kWarps + warp;
+      if (row < next.rows)
+        load_q(q[y], static_cast<const T*>(a.x) + x_row(a, next.s, next.b, row_place(a, h, row)) + lane * E);
+    }
     if (t0 < te) ids = id_of(t0);
 #pragma unroll
     for (int x = 0; x < ST; ++x) {
       if (t0 + x < te) issue(t0 + x);
       copy_commit();
     }
+  };
+  if (more) begin();
+
+  while (more) {
+    const typename Line<R, KT, kEmpty, kWarps>::Piece p = next;
+    const int b = p.b, r0 = p.r0, rows = p.rows, all_see = p.all_see;
 
     // ---- Q: each row's power of two, group sums and operands
-    constexpr int E = D / 32;
-    float q[R / kWarps][E];
-#pragma unroll
-    for (int y = 0; y < R / kWarps; ++y)
-      if (r0 + y * kWarps + warp < rows)
-        load_q(q[y], static_cast<const T*>(a.x) + x_row(a, p.s, b, row_place(a, h, r0 + y * kWarps + warp)) + lane * E);
+    __syncthreads();  // nobody still reads the last row tile's
 #pragma unroll
     for (int y = 0; y < R / kWarps; ++y) {
       const int r = y * kWarps + warp;
-#pragma unroll
-      for (int e = 0; e < E; ++e) q[y][e] = r0 + r < rows ? q[y][e] * q_sign : 0.f;
       float big = 0.f, sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(q[y][e])), sum += q[y][e];
+      for (int e = 0; e < E; ++e) {
+        q[y][e] *= q_sign;
+        big = fmaxf(big, fabsf(q[y][e])), sum += q[y][e];
+      }
 #pragma unroll
       for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
 #pragma unroll
       for (int o = 32 / G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      int ex = 0;  // |q| < 2^ex: scaled below 2^14
-      if (big > 0.f && big < INFINITY) frexpf(big, &ex);
-      ex -= 14;
-      if (lane % (32 / G) == 0) row_z[lane / (32 / G)][r] = ldexpf(sum, -(24 + ex));
+      // |q| < 2^(ex + 14), by the exponent's bits: scaled below 2^14
+      const int ex = (big < INFINITY ? (int)(__float_as_uint(big) >> 23) - 126 : 0) - 14;
+      // 2^-ex in two factors that are float32 numbers for every ex
+      const float up = pow2(-ex / 2), up2 = pow2(-ex - -ex / 2);
+      if (lane % (32 / G) == 0) row_z[lane / (32 / G)][r] = sum * up * up2 * 0x1p-24f;
       if (lane == 0) {
         // at least 2^-126, at most the largest float32: scores of 0 times it stay 0
-        row_f[r] = a.scale_log2 != 0.f
-                       ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), 24 + ex), 1.17549435e-38f), 3.40282347e38f)
-                       : 1.f;
+        const float f = fabsf(a.scale_log2) * pow2(ex / 2 + 12) * pow2(ex - ex / 2 + 12);
+        row_f[r] = a.scale_log2 != 0.f ? fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f) : 1.f;
         const int pos = p.s.len - p.s.n + (r0 + r) / a.group;
         row_lim[r] = r0 + r >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
       }
-      // 2^-ex in two factors that are float32 numbers for every ex
-      const float up = pow2(-ex / 2), up2 = pow2(-ex - -ex / 2);
       __half* qh = reinterpret_cast<__half*>(qfrag);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -586,6 +601,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
       if ((t - t0) % S::FOLD == S::FOLD - 1) fold();
     }
     fold();
+    // The next piece's first copies come in while this one's sums are joined.
+    more = line.next(a, &next);
+    if (!S::OVER && more) begin();
     // to the values' own units, the offsets' part added
 #pragma unroll
     for (int g = 0; g < G; ++g)
@@ -645,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         merge[(warp * S::ACC + j * 4 + e) * 32 + lane] = acc[j / NT / 4][j / NT % 4][j % NT][e];
     __syncthreads();
     const bool whole = p.whole;
-    if (t0 == 0 && !whole && threadIdx.x == 0)
-      args.shared[blockIdx.x] = make_int4(b, h, r0 / R, line.owner(p.last, line.total, line.n));
-    const long long slot = blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
+    if (p.t0 == 0 && !whole && threadIdx.x == 0)
+      args.shared[blockIdx.x] = make_int4(b, p.h, r0 / R, line.owner(p.last, line.total, line.n));
+    const long long slot = blockIdx.x * 2 + (p.t0 == 0 ? 1 : 0);
 #pragma unroll
     for (int jj = 0; jj < G * NT; ++jj) {
       const int j = warp * G * NT + jj;
@@ -659,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int y = 0; y < kWarps; ++y) v[e] += merge[(y * S::ACC + j * 4 + e) * 32 + lane];
       }
       if (whole) {
-        store_tile<T, NT>(a, p.s, b, h, r0, rows, j, v, rl[j % NT], lane);
+        store_tile<T, NT>(a, p.s, b, p.h, r0, rows, j, v, rl[j % NT], lane);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) args.part_o[(slot * S::ACC + j * 4 + e) * 32 + lane] = v[e];
@@ -672,12 +690,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int e = 0; e < 2; ++e) {
           const int r = nt * 8 + 2 * t4 + e;
           if (whole) {
-            if (r0 + r < rows) a.lse[lse_row(a, p.s, b, row_place(a, h, r0 + r))] = row_lse(rm[nt][e], rl[nt][e]);
+            if (r0 + r < rows) a.lse[lse_row(a, p.s, b, row_place(a, p.h, r0 + r))] = row_lse(rm[nt][e], rl[nt][e]);
           } else {
             args.part_ml[(slot * R + r) * 2] = rm[nt][e];
             args.part_ml[(slot * R + r) * 2 + 1] = rl[nt][e];
           }
         }
+    }
+    if (S::OVER && more) {
+      __syncthreads();  // the joined sums are read: the rings may take their place
+      begin();
     }
   }
 }
