@@ -10,16 +10,22 @@
 //
 //   K: word & 0x000F000F is a pair of codes u 2^-24 as float16 subnormals, word &
 //      0x00F000F0 a pair u 2^-20: no conversion at all.  Q is held in float16, each
-//      row scaled by its own power of two (two parts for float32 queries), those of
+//      row scaled by its own power of two, those of
 //      the second kind of pair by 1/16 more.  With s, b a key's step and offset of a
 //      group, its part of the score is s sum(q u) + (b - 8 s) sum(q), in float32.
 //   V: the same pairs, two keys side by side.  The weights p s are float16 too, in units
 //      of a power of two that follows the largest step seen, so that the largest is below
-//      2^15: 11 bits down to 2^-29 of that, and off by at most 2^-40 of it below
-//      (float32 queries: two parts, 22 bits).  Sums of u instead of u - 8 would cancel
-//      against 8 sum(p s) over long contexts, so a ninth product counts -8 sum(p s)
-//      beside them and is folded in every 128 keys; the offsets' part sum(p b) stays in
-//      float32.
+//      2^15: 11 bits down to 2^-29 of that, and off by at most 2^-40 of it below.
+//      Sums of u instead of u - 8 would cancel against 8 sum(p s) over long contexts, so
+//      a ninth product counts -8 sum(p s) beside them and is folded in every 128 keys;
+//      the offsets' part sum(p b) stays in float32.
+//   float32: the instruction cuts its sums off where it should round them, a bias that
+//      grows with the context (3e-5 of O at 65536 keys).  So Q is three parts, multiples
+//      of 2^4, 2^-6 and 2^-16, and the weights two, of 2^5 and 2^-6, each part of at most
+//      11 bits: over 64 values or 16 keys, its products with u - 8 (exact in float16) add
+//      up to less than 2^24 of its grid, nothing is cut off, and float32 additions join
+//      the parts and the keys.  What is left of a weight, below 2^-7, is two more parts,
+//      off by 2^-25 in the end.  3e-7 of O at any length.
 //
 // Work.  A tile is the keys that a block's warps take at a time; the tiles of all
 // sequences, KV heads and row tiles stand in one line that is cut into equal
@@ -52,8 +58,8 @@ struct Shape {
   static constexpr int R = 8 * NT;                      // query rows of a row tile
   static constexpr int CH = (D == 256 || NT >= 3) ? 1 : 2;  // 16-key chunks of a warp at a time
   static constexpr int KT = kWarps * CH * 16;           // keys of a tile
-  static constexpr int QP = F32 ? 2 : 1;                // float16 parts of Q
-  static constexpr int PP = F32 ? 2 : 1;                // float16 parts of the weights
+  static constexpr int QP = F32 ? 3 : 1;                // float16 parts of Q
+  static constexpr int PP = F32 ? 4 : 1;                // float16 parts of the weights
   static constexpr int FOLD = 8 / CH;                   // tiles between two folds: 128 keys of a warp
   static constexpr int ACC = G * 4 * NT * 4;            // accumulators of a lane
   static constexpr int BLOCKS = 2;                      // of an SM
@@ -62,7 +68,7 @@ struct Shape {
   static constexpr int STAGE_BYTES = CH * CHUNK_BYTES;
   // Sums of u beside a count of -8 sum(p s): cheaper than subtracting 8 from each
   // code while there are few columns and registers for the count.
-  static constexpr bool COUNT = NT == 1;
+  static constexpr bool COUNT = NT == 1 && !F32;
   static constexpr int GRID = kSms * BLOCKS;
   static constexpr size_t Q_BYTES = (size_t)G * 4 * NT * QP * 32 * 8;
   static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4, RING_BYTES = (size_t)kWarps * STAGES * STAGE_BYTES;
@@ -99,6 +105,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// x to the nearest multiple of 2^k, for |x| < 2^(k + 22).
+template <int k>
+__device__ __forceinline__ float on_grid(float x) {
+  constexpr float kBig = k >= 0 ? 12582912.f * (1 << (k >= 0 ? k : 0)) : 12582912.f / (1 << (k < 0 ? -k : 0));
+  return __fsub_rn(__fadd_rn(x, kBig), kBig);
 }
 __device__ __forceinline__ uint32_t add_f16(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -330,11 +342,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         const int d = lane * E + e, g = d / 64, i = d % 64 / 8, n8 = d % 8;
         const int st = (i & 1) * 2 + (n8 & 3) / 2, reg = n8 & 1, half = n8 >> 2;
         float v = q[y][e] * up * up2;
-        if (reg) v *= 0.0625f;
 #pragma unroll
         for (int part = 0; part < QP; ++part) {
-          const __half hv = __float2half_rn(v);
-          v -= __half2float(hv);
+          // parts of at most 11 bits: multiples of 2^4, 2^-6 and 2^-16
+          const float t = !F32 ? v : part == 0 ? on_grid<4>(v) : part == 1 ? on_grid<-6>(v) : on_grid<-16>(v);
+          const __half hv = __float2half_rn(reg ? t * 0.0625f : t);
+          v -= t;
           qh[(((((g * 4 + st) * QP + part) * NT + r / 8) * 32 + (r & 7) * 4 + i / 2) * 2 + reg) * 2 + half] = hv;
         }
       }
@@ -345,9 +358,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     // minus[g]: -8 sum(p s) since it was last folded in
     float acc[G][4][NT][4], minus[S::COUNT ? G : 1][NT][4], accb[G][NT][2], bar[NT][2], mu[NT][2], l[NT][2];
     int unit[G];
+    float cap[G], per_unit[G];  // 2^unit, 2^(7 - unit)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       unit[g] = kLeastUnit;
+      cap[g] = pow2(kLeastUnit);
+      per_unit[g] = pow2(7 - kLeastUnit);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -397,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
           for (int y = 0; y < 2; ++y) lds_words(kw[c][y], stage + c * S::CHUNK_BYTES + k_lane + y * (4 * D));
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int g = 0; g < G; ++g) {
+          float low[F32 ? 2 : 1][F32 ? CH : 1][F32 ? NT : 1][4];  // Q's other parts: sums of their own
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
             uint2 bq[QP][NT];
@@ -410,16 +427,28 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             for (int c = 0; c < CH; ++c) {
               const uint32_t wa = kw[c][0][(st >> 1) * G + g] >> (8 * (st & 1));
               const uint32_t wb = kw[c][1][(st >> 1) * G + g] >> (8 * (st & 1));
-              const uint32_t ak[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
+              uint32_t ak[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
+              if constexpr (F32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ak[e] = add_f16(ak[e], e < 2 ? 0x80088008u : 0x80808080u);  // -8: exact
+              }
 #pragma unroll
               for (int part = 0; part < QP; ++part)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (st == 0 && part == 0) mma_f16_first(sc[g][c][nt], ak, bq[part][nt].x, bq[part][nt].y);
-                  else mma_f16(sc[g][c][nt], ak, bq[part][nt].x, bq[part][nt].y);
+                  float(&to)[4] = part == 0 ? sc[g][c][nt] : low[F32 ? part - 1 : 0][F32 ? c : 0][F32 ? nt : 0];
+                  if (st == 0) mma_f16_first(to, ak, bq[part][nt].x, bq[part][nt].y);
+                  else mma_f16(to, ak, bq[part][nt].x, bq[part][nt].y);
                 }
             }
           }
+#pragma unroll
+          for (int c = 0; c < (F32 ? CH : 0); ++c)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[g][c][nt][e] += low[0][c][nt][e] + low[F32 ? 1 : 0][c][nt][e];
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -428,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             lds_words(ksw, stage + c * S::CHUNK_BYTES + s_lane + y * (32 * G));
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              const float st = bf16_lo(ksw[g]), z = fmaf(-8.f, st, bf16_hi(ksw[g]));
+              const float st = bf16_lo(ksw[g]), z = F32 ? bf16_hi(ksw[g]) : fmaf(-8.f, st, bf16_hi(ksw[g]));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const float2 sum = *reinterpret_cast<const float2*>(&row_z[g][nt * 8 + 2 * t4]);
@@ -494,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
         for (int c = 1; c < CH; ++c) v = fmax3f(v, bf16_lo(vsw[c][0][g]), bf16_lo(vsw[c][1][g]));
         step[g] = v;
-        over |= v > pow2(unit[g]);
+        over |= v > cap[g];
       }
       if (__any_sync(0xffffffffu, over)) {
         float fg[G];
@@ -506,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           const int nu = max(unit[g], min((int)(__float_as_uint(v) >> 23) - 126, 127));  // v < 2^nu
           fg[g] = unit[g] - nu < -126 ? 0.f : pow2(unit[g] - nu);
           unit[g] = nu;
+          cap[g] = pow2(nu);
+          per_unit[g] = pow2(7 - nu);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -553,10 +584,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           uint32_t pb[PP][NT][2];
-          const float per_unit = pow2(7 - unit[g]);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float st = bf16_lo(vsw[c][y][g]) * per_unit, o = bf16_hi(vsw[c][y][g]);
+            const float st = bf16_lo(vsw[c][y][g]) * per_unit[g], o = bf16_hi(vsw[c][y][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float p0 = x[c][nt][2 * y] * st, p1 = x[c][nt][2 * y + 1] * st;
@@ -564,7 +594,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
               accb[g][nt][1] = fmaf(x[c][nt][2 * y + 1], o, accb[g][nt][1]);
 #pragma unroll
               for (int part = 0; part < PP; ++part) {
-                const uint32_t v = pack_f16(p0, p1);
+                // two parts of at most 11 bits, multiples of 2^5 and 2^-6, and what is left, twice rounded
+                float t0 = p0, t1 = p1;
+                if (F32 && part == 0) t0 = on_grid<5>(p0), t1 = on_grid<5>(p1);
+                if (F32 && part == 1) t0 = on_grid<-6>(p0), t1 = on_grid<-6>(p1);
+                const uint32_t v = pack_f16(t0, t1);
                 pb[part][nt][y] = transpose8(v);
                 if (part + 1 < PP) p0 -= half_lo(v), p1 -= half_hi(v);
               }
@@ -580,9 +614,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           if constexpr (S::COUNT) {
             const uint32_t eight[4] = {0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u};  // -8 2^-24
 #pragma unroll
-            for (int part = 0; part < PP; ++part)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(minus[g][nt], eight, pb[part][nt][0], pb[part][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(minus[g][nt], eight, pb[0][nt][0], pb[0][nt][1]);
           }
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
@@ -593,9 +625,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
               for (int e = 0; e < 4; ++e) av[e] = add_f16(av[e], (e & 1) ? 0x80808080u : 0x80088008u);  // -8: exact
             }
 #pragma unroll
-            for (int part = 0; part < PP; ++part)
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (F32) {
+                float sum[3][4];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[g][mt][nt], av, pb[part][nt][0], pb[part][nt][1]);
+                for (int part = 0; part < PP; ++part) {
+                  if (part < 3) mma_f16_first(sum[part], av, pb[part][nt][0], pb[part][nt][1]);
+                  else mma_f16(sum[2], av, pb[part][nt][0], pb[part][nt][1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[g][mt][nt][e] += sum[0][e] + (sum[1][e] + sum[2][e]);
+              } else {
+                mma_f16(acc[g][mt][nt], av, pb[0][nt][0], pb[0][nt][1]);
+              }
+            }
           }
         }
       if ((t - t0) % S::FOLD == S::FOLD - 1) fold();
@@ -789,7 +832,7 @@ struct Launch {
   static size_t ml_bytes(const Kv4Args& a) { return (size_t)grid(a) * 2 * S::R * 8; }
   static size_t workspace(const Kv4Args& a) { return o_bytes(a) + ml_bytes(a) + (size_t)grid(a) * sizeof(int4); }
   static cudaError_t run(const Kv4Args& a, void* ws, cudaStream_t st) {
-    AttnArgs args;
+    AttnArgs args = {};
     args.a = a;
     args.page_div = fast_div(a.page);
     args.part_o = static_cast<float*>(ws);
@@ -827,14 +870,17 @@ struct Launch {
 
 // Row tiles of 8, 16 or 24 queries: the least that hold all of a KV head's, else the
 // widest that the registers hold (accumulators: D / 16 * 4 a lane and 8 queries).
+// Sequences of 8192 tokens, 32 heads on 8, 4 / 16 new tokens each, us, 16 rows against 8:
+// float32 head dim 64 (8 sequences) 37 / 114 against 40 / 131, 128 71 / 219 against 66 / 217,
+// 256 151 / 486 against 130 / 459; bf16 256 81 / 232 against 78 / 261.
 // More bf16 rows than 24 at head dim 64 and 128 are the tcgen05 kernel's.
 template <class T, int D, class F>
 auto with_width(const Kv4Args& a, F&& f) {
-  constexpr bool kThree = D <= 128 && sizeof(T) == 2;
+  constexpr int kWide = sizeof(T) == 2 ? (D <= 128 ? 3 : 2) : (D == 64 ? 2 : 1);
   const long long rows = (long long)a.seqlen * a.group;
-  if (rows <= 8) return f(Launch<T, D, 1>());
-  if (rows <= 16 || !kThree) return f(Launch<T, D, 2>());
-  return f(Launch<T, D, kThree ? 3 : 2>());
+  if (rows <= 8 || kWide == 1) return f(Launch<T, D, 1>());
+  if (rows <= 16 || kWide == 2) return f(Launch<T, D, kWide < 2 ? 1 : 2>());
+  return f(Launch<T, D, kWide>());
 }
 template <class F>
 auto with_shape(const Kv4Args& a, int head_dim, bool bf16, F&& f) {
