@@ -317,6 +317,17 @@ attn_status_t resolve(const attn_kv4_params_t* p, bool attention, Kv4Args* a, bo
   if (total * heads >= (1ll << 31) || (long long)p->seqlen * heads * p->batch >= (1ll << 31))
     return kfail(ATTN_ERR_UNSUPPORTED, "%lld rows over all heads: at most 2^31 - 1 are supported",
                  std::max(total, (long long)p->seqlen * p->batch) * heads);
+  if (attention) {  // the attention counts its rows, positions and the cache's rows in 32 bits
+    if (total * heads > (1ll << 30) || (long long)p->seqlen * heads * p->batch > (1ll << 30))
+      return kfail(ATTN_ERR_UNSUPPORTED, "%lld query rows over all heads: at most 2^30 are supported",
+                   std::max(total, (long long)p->seqlen * p->batch) * heads);
+    if ((long long)p->max_pages * p->page_size > (1ll << 30))
+      return kfail(ATTN_ERR_UNSUPPORTED, "max_pages * page_size = %lld: at most 2^30 positions of a sequence are supported",
+                   (long long)p->max_pages * p->page_size);
+    if ((long long)p->n_pages * p->page_size > 0xFFFFFFFFll / p->heads_kv)
+      return kfail(ATTN_ERR_UNSUPPORTED, "n_pages=%d times heads_kv=%d times page_size=%d: fewer than 2^32 rows are supported",
+                   p->n_pages, p->heads_kv, p->page_size);
+  }
   if (!p->lens) return kfail(ATTN_ERR_INVALID_ARG, "lens is NULL");
   if (p->max_pages > 0 && !p->block_table) return kfail(ATTN_ERR_INVALID_ARG, "block_table is NULL");
   if (p->table_stride < p->max_pages && p->batch > 1)

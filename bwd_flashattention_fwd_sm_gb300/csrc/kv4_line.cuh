@@ -92,6 +92,7 @@ struct Line {
       *sum = all;
       return v + before;
     };
+    if (threadIdx.x == 0) found_seq = 0, found_first = 0;  // lengths that change under the kernel may hide the place
     total = 0;
     long long mine = 0, incl = 0, sum;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {

@@ -38,8 +38,8 @@ constexpr int kParts = 4, kPart = kKeys / kParts;  // warps of a row, and the ke
 constexpr int kSoftWarps = 4 * kParts, kUnpackWarps = 4, kWarps = kSoftWarps + kUnpackWarps + 4;
 constexpr int kThreads = kWarps * 32;
 // Registers: 80 a thread at launch; what the issuing warps give up the softmax warps take
-// (512 * 88 + 128 * 80 + 128 * 40 <= 768 * 80).
-constexpr int kSoftRegs = 88, kIssueRegs = 56;
+// (512 * 88 + 128 * 72 + 128 * 56 = 768 * 80).
+constexpr int kSoftRegs = 88, kUnpackRegs = 72, kIssueRegs = 56;
 
 template <int D>
 struct Smem {
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_rows(const __grid_constant_
     ptx::regs_increase<kSoftRegs>();
     softmax_role<D>(args, sm, line, tmem, warp, lane);
   } else if (warp < kSoftWarps + kUnpackWarps) {
-    ptx::regs_decrease<72>();
+    ptx::regs_decrease<kUnpackRegs>();
     unpack_role<D>(args, sm, line, warp - kSoftWarps, lane);
   } else {
     ptx::regs_decrease<kIssueRegs>();
@@ -682,7 +682,7 @@ struct Launch {
   static size_t ml_bytes(const Kv4Args& a) { return (size_t)grid(a) * 2 * kRows * 8; }
   static size_t workspace(const Kv4Args& a) { return o_bytes(a) + ml_bytes(a) + (size_t)grid(a) * sizeof(int4); }
   static cudaError_t run(const Kv4Args& a, void* ws, unsigned long long wait_ns, cudaStream_t st) {
-    AttnArgs args;
+    AttnArgs args = {};
     args.a = a;
     args.page_div = fast_div(a.page);
     args.part_o = static_cast<float*>(ws);

@@ -58,8 +58,13 @@ class Kv4Cache:
                 raise ValueError(f"{name}: gbattn runs on CUDA tensors of one device only")
             if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
-        self.pointers = tuple(t.data_ptr() for t in (k_codes, k_scale, v_codes, v_scale))
+        self._arrays = (k_codes, k_scale, v_codes, v_scale)
+        self._pointers = tuple(t.data_ptr() for t in self._arrays)
+
+    k_codes = property(lambda self: self._arrays[0])
+    k_scale = property(lambda self: self._arrays[1])
+    v_codes = property(lambda self: self._arrays[2])
+    v_scale = property(lambda self: self._arrays[3])
 
     @classmethod
     def empty(cls, n_pages, heads_kv, page_size, head_dim, device=None) -> "Kv4Cache":
@@ -131,19 +136,23 @@ def _params(x, y, cache, block_table, lens, seqlens, heads_q, heads_kv, scale=0.
                       xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], scale, dtype, 1 if causal else 0)
 
 
-def _on(device, stream, call, *args):
-    """call(*args, handle) with ``device`` current and, where ``stream`` is given, that stream: what is
-    allocated for the call then belongs to the stream that it runs on, and what comes from
-    another stream is not given away before the call has run."""
+def _on(cache, stream, call, *args):
+    """call(cache, *args, handle) with the cache's device current and, where ``stream`` is given, that
+    stream: what is allocated for the call then belongs to the stream that it runs on, and
+    what comes from another stream is not given away before the call has run."""
+    device = cache.device
     index = device.index
     if stream is None and index == torch.cuda.current_device():
-        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+        return call(cache, *args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(device), torch.cuda.stream(stream):
         if stream is not None:
+            given = [*cache._arrays]
             for t in args:
+                given += t if isinstance(t, (tuple, list)) else [t.device] if isinstance(t, SeqLens) else [t]
+            for t in given:
                 if isinstance(t, torch.Tensor) and t.is_cuda:
                     t.record_stream(stream)
-        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+        return call(cache, *args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def kv4_write(cache: Kv4Cache, k, v, block_table, lens, *, seqlens: SeqLens | None = None, stream=None) -> Kv4Cache:
@@ -152,14 +161,14 @@ def kv4_write(cache: Kv4Cache, k, v, block_table, lens, *, seqlens: SeqLens | No
     Pages that a sequence shares with another must not be written to."""
     if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
         raise ValueError("v must match k in shape, dtype and device")
-    return _on(cache.device, stream, _write, cache, k, v, block_table, lens, seqlens)
+    return _on(cache, stream, _write, k, v, block_table, lens, seqlens)
 
 
 def _write(cache, k, v, block_table, lens, seqlens, stream):
     k, v = _usable(k), _usable(v)
     heads = k.shape[1] if k.dim() > 1 else 0
     p = _params(k, v, cache, block_table, lens, seqlens, heads, heads)
-    check(_lib.load().attn_kv4_write(p, k.data_ptr(), v.data_ptr(), *cache.pointers, stream), "attn_kv4_write")
+    check(_lib.load().attn_kv4_write(p, k.data_ptr(), v.data_ptr(), *cache._pointers, stream), "attn_kv4_write")
     return cache
 
 
@@ -169,7 +178,7 @@ def kv4_read(cache: Kv4Cache, block_table, lens, seqlen: int | None = None, *, s
     ``seqlens`` a packed batch.  Rows of padding are 0.  out: a (k, v) pair to write to."""
     if (seqlen is None) == (seqlens is None):
         raise ValueError("give either seqlen (a fixed number of tokens) or seqlens (a packed batch)")
-    return _on(cache.device, stream, _read, cache, block_table, lens, seqlen, seqlens, dtype, out)
+    return _on(cache, stream, _read, block_table, lens, seqlen, seqlens, dtype, out)
 
 
 def _read(cache, block_table, lens, seqlen, seqlens, dtype, out, stream):
@@ -185,7 +194,7 @@ def _read(cache, block_table, lens, seqlen, seqlens, dtype, out, stream):
                 raise ValueError(f"out must be two CUDA tensors of shape {shape} and one dtype, rows contiguous "
                                  "and 16-byte aligned")
     p = _params(k, v, cache, block_table, lens, seqlens, H, H)
-    check(_lib.load().attn_kv4_read(p, *cache.pointers, k.data_ptr(), v.data_ptr(), stream), "attn_kv4_read")
+    check(_lib.load().attn_kv4_read(p, *cache._pointers, k.data_ptr(), v.data_ptr(), stream), "attn_kv4_read")
     return k, v
 
 
@@ -194,10 +203,10 @@ def attn_fwd_kv4(q, cache: Kv4Cache, block_table, lens, *, causal=True, scale=No
     """O, LSE of the newest tokens' queries over all that the cache holds.  Returns (o, lse).
 
     causal: a token sees the positions up to its own; else all of its sequence's."""
-    return _on(cache.device, stream, _attend, q, cache, block_table, lens, causal, scale, seqlens, workspace, out)
+    return _on(cache, stream, _attend, q, block_table, lens, causal, scale, seqlens, workspace, out)
 
 
-def _attend(q, cache, block_table, lens, causal, scale, seqlens, workspace, out, stream):
+def _attend(cache, q, block_table, lens, causal, scale, seqlens, workspace, out, stream):
     lib = _lib.load()
     q = _usable(q)
     if out is None:
@@ -216,6 +225,6 @@ def _attend(q, cache, block_table, lens, causal, scale, seqlens, workspace, out,
     ws = workspace
     if need and (ws is None or ws.numel() * ws.element_size() < need):
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    check(lib.attn_fwd_kv4(p, q.data_ptr(), *cache.pointers, o.data_ptr(), lse.data_ptr(),
+    check(lib.attn_fwd_kv4(p, q.data_ptr(), *cache._pointers, o.data_ptr(), lse.data_ptr(),
                            ws.data_ptr() if need else None, need, stream), "attn_fwd_kv4")
     return o, lse

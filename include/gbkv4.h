@@ -46,7 +46,9 @@
  * Constraints.  head_dim 64, 128 or 256; page_size a positive multiple of 16;
  * heads_q % heads_kv == 0; x and y and the code arrays 16-byte aligned, scale
  * arrays 16-byte aligned too; strides multiples of 16 bytes; fewer than 2^31 rows
- * over all heads in one call.  Offsets into the cache are 64-bit.
+ * over all heads in one call.  Offsets into the cache are 64-bit.  The attention
+ * takes up to 2^30 query rows over all heads, up to 2^30 positions in a page list
+ * and fewer than 2^32 rows (n_pages * heads_kv * page_size) in the cache.
  *
  * Errors and asynchrony are as for gbattn.h.  What only the device knows is
  * checked there, in every build: a page outside [0, n_pages), a length below 0 or
@@ -112,6 +114,10 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
  *     s_ij = scale <q_i, k_j> for j < lens[n] and, with causal, j <= i;
  *     LSE_i = ln sum_j exp(s_ij);   O_i = sum_j exp(s_ij - LSE_i) v_j.
  * A row that sees nothing (padding, an empty sequence) gets O = 0 and LSE = -inf.
+ * Sums are float32.  Roundings to fewer bits, beside that of O: float32 rows none;
+ * bf16 rows the weights exp(s_ij - max) times a group's step, to 11 bits for up to
+ * 24 query rows of a KV head (seqlen * heads_q / heads_kv) or head_dim 256, else to
+ * 8 bits.  Cached values beyond 2^96 in size may overflow the sums.
  * y: O; lse: contiguous float32 [batch, heads_q, seqlen], packed [heads_q,
  * total_tokens].  The result is bit-identical from run to run.  workspace: device
  * scratch, 256-byte aligned, >= attn_kv4_workspace_size(p) bytes (SIZE_MAX if the

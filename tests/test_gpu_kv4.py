@@ -339,6 +339,52 @@ def test_strided_views_and_unaligned_tensors():
                  "bf16", "views")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale, spread", [(3.0, 1.0), (-0.2, 1.0), (0.0, 1.0), (0.1, 1e-20), (0.1, 1e18)])
+def test_many_rows_extreme_scores(scale, spread, D):
+    """The same with more than 24 rows on a KV head, padding among them."""
+    c = Paged([200, 17], 2, D, 16, seed=18)
+    q = (torch.randn(2, 8, 20, D, generator=torch.Generator().manual_seed(2)) * spread).to(torch.bfloat16)
+    o, lse = attn_fwd_kv4(q.to(DEV), c.cache, c.table_dev, c.lens_dev, scale=scale / spread)
+    torch.cuda.synchronize()
+    check_attend(c, q.double().numpy(), o.double().cpu().numpy(), lse.double().cpu().numpy(), scale / spread, True,
+                 "bf16", f"rows scale {scale} {spread}")
+
+
+def test_many_rows_long_split_and_bit_identical():
+    c = Paged([20000, 130], 1, 128, 64, seed=19)
+    q, o, lse = attend_fixed(c, 8, 5, "bf16", seed=1, scale=0.1)
+    q, o2, lse2 = attend_fixed(c, 8, 5, "bf16", seed=1, scale=0.1)
+    assert np.array_equal(o, o2) and np.array_equal(lse, lse2)
+    check_attend(c, q, o, lse, 0.1, True, "bf16", "rows long")
+
+
+def test_many_rows_broken_queries_and_pages():
+    """Infinities and NaN stay in their rows; a page that is none is left out and recorded."""
+    c = Paged([150, 70], 2, 128, 16, seed=62)
+    q = torch.randn(2, 8, 40, 128, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(DEV)
+    o, lse = attn_fwd_kv4(q, c.cache, c.table_dev, c.lens_dev)
+    broken = q.clone()
+    broken[0, 1, 3, 5], broken[1, 6, 39, 0] = float("nan"), float("inf")
+    o2, lse2 = attn_fwd_kv4(broken, c.cache, c.table_dev, c.lens_dev)
+    hit = torch.zeros(2, 8, 40, dtype=torch.bool, device=DEV)
+    hit[0, 1, 3] = hit[1, 6, 39] = True
+    assert torch.equal(o[~hit], o2[~hit]) and torch.equal(lse[~hit], lse2[~hit])
+    assert not torch.isfinite(o2[0, 1, 3]).any()
+    bad = c.table_dev.clone()
+    bad[0, 1], bad[1] = c.n_pages, -1
+    o, lse = attn_fwd_kv4(q, c.cache, bad, c.lens_dev, causal=False)
+    assert get_status() == _lib.ATTN_ERR_DEVICE_BOUNDS and get_status() == 0
+    assert torch.all(o[1] == 0) and torch.all(torch.isneginf(lse[1]))
+    keep = Paged([134, 0], 2, 128, 16, seed=62)  # the first sequence without its second page
+    for which in range(2):
+        for dst, src in ((keep.codes, c.codes), (keep.scale, c.scale)):
+            for i, j in enumerate(j for j in range(10) if j != 1):
+                dst[which][keep.table[0, i]] = src[which][c.table[0, j]]
+    check_attend(keep, q.double().cpu().numpy(), o.double().cpu().numpy(), lse.double().cpu().numpy(), 128 ** -0.5,
+                 False, "bf16", "rows bad pages")
+
+
 # ---------------------------------------------------------------- as they are used
 
 
@@ -448,6 +494,41 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_many_rows_captured_and_on_two_streams():
+    """Prompt chunks: a captured call follows new lengths, two graphs and two streams share nothing."""
+    a, b = Paged([700, 90], 2, 128, 64, seed=43), Paged([260, 1000, 7], 1, 64, 16, seed=44)
+    qa = torch.randn(2, 8, 30, 128, device=DEV).to(torch.bfloat16)
+    qb = torch.randn(3, 4, 40, 64, device=DEV).to(torch.bfloat16)
+    runs = [(qa, a), (qb, b)]
+    call = lambda q, c, **kw: attn_fwd_kv4(q, c.cache, c.table_dev, c.lens_dev, **kw)  # noqa: E731
+    want = [call(q, c) for q, c in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [call(q, c, stream=s) for (q, c), s in zip(runs, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    graphs, outs = [], []
+    for q, c in runs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call(q, c))
+    for less in (0, 3):
+        for _, c in runs:
+            c.lens_dev -= less
+        for g, s in zip(graphs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (q, c), g in zip(runs, outs):
+            w = call(q, c)
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    torch.cuda.synchronize()
+    assert get_status() == 0
 
 
 # ---------------------------------------------------------------- large caches, refusals

@@ -79,6 +79,21 @@ def test_refusals_of_the_attention(lib):
                             None) == _lib.ATTN_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("change", [
+    {"n_pages": 1 << 27},                                              # 2^32 rows
+    {"n_pages": (1 << 31) - 1, "page_size": 1 << 30, "max_pages": 1},  # and far more
+    {"max_pages": (1 << 26) + 1, "table_stride": 1 << 27},             # 2^30 + 16 positions of a sequence
+    {"max_pages": (1 << 31) - 1, "table_stride": 1 << 31, "page_size": 1 << 30},
+    {"seqlen": 1 << 27, "batch": 1, "heads_q": 10},                    # more than 2^30 query rows
+])
+def test_sizes_that_the_attention_refuses(lib, change):
+    p = params(**change)
+    assert calls(lib, p) == (_lib.ATTN_ERR_CUDA, _lib.ATTN_ERR_CUDA, _lib.ATTN_ERR_UNSUPPORTED)
+    assert lib.attn_kv4_workspace_size(p) == _lib.SIZE_MAX
+    near = params(n_pages=(1 << 27) - 1, max_pages=1 << 26, table_stride=1 << 27)
+    assert calls(lib, near)[2] == _lib.ATTN_ERR_CUDA
+
+
 def test_pointers(lib):
     assert calls(lib, params(), ptr=None) == (_lib.ATTN_ERR_INVALID_ARG,) * 3
     assert calls(lib, params(), ptr=FAKE + 8) == (_lib.ATTN_ERR_INVALID_ARG,) * 3
