@@ -351,6 +351,7 @@ attn_status_t resolve(const attn_kv4_params_t* p, bool attention, Kv4Args* a, bo
   a->heads_q = p->heads_q;
   a->heads_kv = p->heads_kv;
   a->group = attention ? p->heads_q / p->heads_kv : 1;
+  a->by_group = fast_div(a->group);
   a->seqlen = p->seqlen;
   a->page = p->page_size;
   a->n_pages = p->n_pages;

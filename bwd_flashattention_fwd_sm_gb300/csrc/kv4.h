@@ -12,6 +12,19 @@ namespace gbattn {
 
 constexpr int kKv4Group = 64;  // values that share one (s, b) pair
 
+// n / d for 0 <= n < 2^31: (n * mul) >> shift with mul = floor(2^shift / d) + 1.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+inline FastDiv fast_div(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  return {(uint32_t)((1ull << (31 + l)) / (uint32_t)d + 1), (uint32_t)(31 + l)};
+}
+__device__ __forceinline__ int div_by(int n, FastDiv d) {
+  return (int)(((unsigned long long)(uint32_t)n * d.mul) >> d.shift);
+}
+
 // Everything a kernel needs, resolved on the host.  Strides in elements.
 struct Kv4Args {
   uint8_t* kc;   // codes [n_pages, heads_kv, page, D / 2]
@@ -24,6 +37,7 @@ struct Kv4Args {
   const int* cu;         // NULL: fixed length
   long long total;       // packed rows
   int batch, heads_q, heads_kv, group, seqlen, page, n_pages, max_pages;
+  FastDiv by_group;  // group, as a divisor
   void* x;
   void* y;
   float* lse;

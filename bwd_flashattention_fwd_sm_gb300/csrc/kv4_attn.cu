@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         // at least 2^-126, at most the largest float32: scores of 0 times it stay 0
         const float f = fabsf(a.scale_log2) * pow2(ex / 2 + 12) * pow2(ex - ex / 2 + 12);
         row_f[r] = a.scale_log2 != 0.f ? fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f) : 1.f;
-        const int pos = p.s.len - p.s.n + (r0 + r) / a.group;
+        const int pos = p.s.len - p.s.n + div_by(r0 + r, a.by_group);
         row_lim[r] = r0 + r >= rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
       }
       __half* qh = reinterpret_cast<__half*>(qfrag);

@@ -12,19 +12,6 @@ namespace {
 
 constexpr int kSms = 152;  // a fixed count, so that the workspace size needs no device query
 
-// n / d for 0 <= n < 2^31: (n * mul) >> shift with mul = floor(2^shift / d) + 1.
-struct FastDiv {
-  uint32_t mul, shift;
-};
-FastDiv fast_div(int d) {
-  int l = 0;
-  while ((1ll << l) < d) ++l;
-  return {(uint32_t)((1ull << (31 + l)) / (uint32_t)d + 1), (uint32_t)(31 + l)};
-}
-__device__ __forceinline__ int div_by(int n, FastDiv d) {
-  return (int)(((unsigned long long)(uint32_t)n * d.mul) >> d.shift);
-}
-
 // The line of a kernel whose row tiles are kRows queries high, whose tiles are kKeys
 // keys long and whose blocks have kWarps warps.  A row tile has kEmpty places before
 // its keys' tiles: what it costs beside them (queries into operands, results joined),
@@ -102,8 +89,10 @@ struct Line {
     }
     n = min(total, (long long)gridDim.x);
     if (blockIdx.x >= n) return false;
-    tile = blockIdx.x * total / n;
-    tile_end = (blockIdx.x + 1) * total / n;
+    // 64-bit divisions only where the numbers need them: they take longer than the rest here
+    const bool small = total < (1 << 22);  // kSms * 2 blocks at most
+    tile = small ? (uint32_t)blockIdx.x * (uint32_t)total / (uint32_t)n : blockIdx.x * total / n;
+    tile_end = small ? (uint32_t)(blockIdx.x + 1) * (uint32_t)total / (uint32_t)n : (blockIdx.x + 1) * total / n;
     long long before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
       const int x = b0 + threadIdx.x;
@@ -132,7 +121,8 @@ struct Line {
       first += (long long)a.heads_kv * w.row_tiles * w.places();
       w = seq_work(a, ++b);
     }
-    const int in_seq = (int)((tile - first) / w.places());  // (head, row tile)
+    const long long in = tile - first;
+    const int in_seq = in < 0x7FFFFFFF ? (int)in / w.places() : (int)(in / w.places());  // (head, row tile)
     const int at = (int)(tile - first - (long long)in_seq * w.places());
     p->b = b;
     p->s = w.s;
@@ -145,8 +135,8 @@ struct Line {
     p->last = first + (long long)(in_seq + 1) * w.places() - 1;
     tile += w.places() - at;
     if (p->t1 <= 0) return false;  // the stretch ends before the row tile's keys
-    const int low = w.s.len - w.s.n + p->r0 / a.group;
-    const int high = w.s.len - w.s.n + (min(p->r0 + kRows, p->rows) - 1) / a.group;
+    const int low = w.s.len - w.s.n + div_by(p->r0, a.by_group);
+    const int high = w.s.len - w.s.n + div_by(min(p->r0 + kRows, p->rows) - 1, a.by_group);
     p->klen = high < 0 ? 0 : a.causal ? high + 1 : w.s.len;
     p->all_see = low < 0 ? 0 : a.causal ? low + 1 : w.s.len;
     if (a.n_pages == 0 && p->klen > 0) {  // a cache without a page
@@ -164,7 +154,7 @@ struct RowPlace {
 };
 __device__ __forceinline__ RowPlace row_place(const Kv4Args& a, int h, int row) {
   RowPlace p;
-  p.token = row / a.group;
+  p.token = div_by(row, a.by_group);
   p.head = h * a.group + (row - p.token * a.group);
   return p;
 }

@@ -1,27 +1,28 @@
 // Attention over the 4-bit key/value cache for many query rows: a prompt's chunk, or
 // a few proposed tokens of a large group of heads.
 //
-// Here the products bound, not the cache's bytes, and unpacking a key must not be
-// repeated for every few queries: 128 query rows of a KV head meet 128 keys on tcgen05
-// instructions, with the row sums in tensor memory.  Four warps unpack each tile once
-// into shared memory (128-byte rows of 64 values, swizzled, one box for each group
-// of 64):
-//   K: pairs of codes as float16 subnormals, u 2^-24 from a word's even values and
-//      u 2^-20 from the odd ones, five operations for eight codes.  Q is float16 in
-//      each row's own power of two, in the same order, its odd values scaled by 1/16.
-//   V: codes as bfloat16 integers -8 .. 7.
-// Each group has its own score product, so that a key's step and offset are applied to
-// float32 sums: x = sum_g s_g C_g + (b_g - 8 s_g) sum(q_g), exact but for float32
-// roundings.  The weights p s_g are rounded once to bfloat16 (2^-8 of themselves at
-// most) and multiply V group by group; the offsets' part sum(p b_g) and the row sums
-// stay in float32.
+// Here the work per score bounds, not the cache's bytes: 128 query rows of a KV head meet
+// 128 keys on tcgen05 instructions, with scores, weights and sums in tensor memory, and
+// what an unpacked key costs is shared by the rows.  So everything that belongs to a key
+// goes into its operands, and a score needs no more than a masked maximum, one
+// multiplication and addition, exp2 and a rounding:
+//   - A step has 8 significant bits and u - 8 three, so s (u - 8) is a float16 number,
+//     exactly, once the tile's largest step is brought below 2^12 (steps 2^-25 of that
+//     and less lose bits).  Four warps write these, K's and V's, into 128-byte rows of 64
+//     values, swizzled, one box for each group of 64.
+//   - The offsets are operands too: sum_g b_g sum(q_g) is one more step of 16 of Q K^T
+//     (sum(q_g) in three float16 parts), and sum(p b_g) one more product of 16 columns.
+//   - K's power of two, a tile's, goes into the factor that takes scores to log2 units; V's
+//     is the largest since the first tile, and where it grows the sums are scaled.
+// Q is float16 in each row's own power of two.  The weights p are rounded once to
+// float16, with 2^7 at the running maximum and at most 2^15 (it is raised only when a score
+// is above it by more than 2^8): 11 bits, 2^-32 of the maximum at least.
 //
 // Sixteen warps do the softmax, four for each 32 rows with a quarter of the keys each;
-// the scores of tile t + 1 are computed while they work on tile t.  The running maximum
-// is raised only when a score is above it by more than 2^8; the four warps of a row
-// agree on that with one barrier a tile.  What bounds it: about 14 instructions an element
-// in the softmax warps, against 4 D of a product's operations.  Blocks share the work
-// by equal stretches of one line of tiles, as for few rows (kv4_attn.cu).
+// they agree on the maximum with one barrier a tile.  Scores have two places, so that the
+// next tile's are computed meanwhile.
+// Blocks share the work by equal stretches of one line of tiles, as for few rows
+// (kv4_attn.cu).
 #include <algorithm>
 #include <atomic>
 
@@ -37,44 +38,67 @@ constexpr int kParts = 4, kPart = kKeys / kParts;  // warps of a row, and the ke
 // four warps of each 32 rows, four that unpack, and four of which one issues the products
 constexpr int kSoftWarps = 4 * kParts, kUnpackWarps = 4, kWarps = kSoftWarps + kUnpackWarps + 4;
 constexpr int kThreads = kWarps * 32;
-// Registers: 80 a thread at launch; what the issuing warps give up the softmax warps take
-// (512 * 88 + 128 * 72 + 128 * 56 = 768 * 80).
-constexpr int kSoftRegs = 88, kUnpackRegs = 72, kIssueRegs = 56;
+// Registers: 80 a thread at launch; what the issuing warps give up the others take
+// ((512 + 128) * 88 + 128 * 40 = 768 * 80).
+constexpr int kSoftRegs = 88, kUnpackRegs = 88, kIssueRegs = 40;
+
+using TcLine = Line<kRows, kKeys, kSpare, kWarps>;
+
+// A warp's place in the block's stretch.  In shared memory: the registers are needed for a
+// tile's data.
+struct Walk {
+  TcLine line;
+  TcLine::Piece p;
+};
 
 template <int D>
 struct Smem {
   static constexpr int G = D / kKv4Group;
   uint8_t q[G][kRows * 128];  // float16, 128-byte rows, 128-byte swizzle
+  uint8_t qx[kRows * 128];    // three parts of each group's sum(q), in the first 16 columns
   uint8_t k[2][G][kKeys * 128];
+  uint8_t kx[2][kKeys * 128];  // offsets, to qx's columns
   uint8_t v[2][G][kKeys * 128];
-  float4 ksz[2][G][kKeys / 2];  // s and b - 8 s of two neighbouring keys' groups: (s, s, z, z)
-  float4 vsb[2][G][kKeys / 2];  // (s, s, b, b)
-  uint8_t dead[2][kKeys];   // the key has no page
-  uint32_t bad[2];          // a byte for each unpacking warp: it has a dead key
+  uint8_t vx[2][2][16 * 128];  // V's offsets: a group a row, 64 keys a box
+  uint8_t dead[2][kKeys];      // the key has no page
+  uint32_t bad[2];             // a byte for each unpacking warp: it has a dead key
+  int2 exps[2][kUnpackWarps];  // the unpacking warps' powers of two (K's, V's)
+  int2 unit[2];                // and the tile's
   float top[kParts][kRows];  // row maxima over the parts of the keys
-  float sums[kParts][kRows][1 + G];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_free, p_full, pv_done, drain;
+  float sums[kParts][kRows];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
+  Walk walk[kSoftWarps + kUnpackWarps + 1];
   ptx::Abort abort;
   uint32_t tmem;
 };
 
-// Tensor memory, in 32-bit columns: the groups' scores, the weights, O.
+// Tensor memory, in 32-bit columns: two tiles' scores, the weights, O and the offsets' sums.
 template <int D>
 struct Tmem {
-  static constexpr int G = D / kKv4Group;
-  static constexpr uint32_t S = 0, P = G * 128, O = P + G * 64, N = O + D;
-  static constexpr uint32_t kCols = N <= 256 ? 256 : 512;
+  static constexpr uint32_t S = 0, P = 256, O = 320, X = O + D, kCols = 512;
 };
 
-using TcLine = Line<kRows, kKeys, kSpare, kWarps>;
 
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {  // float16 operands, K-major, float32 sums
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// float16 operands, float32 sums; A K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Tiles of a piece that any of its rows sees.
 __device__ __forceinline__ int piece_end(const TcLine::Piece& p) { return min(p.t1, (p.klen + kKeys - 1) / kKeys); }
 
-// Whether any lane of the four warps that share 32 rows says so (a barrier of all four).
+// The warp's next piece into its place; false at the stretch's end.
+__device__ __forceinline__ bool advance(const Kv4Args& a, Walk& walk, int lane) {
+  TcLine line = walk.line;
+  TcLine::Piece p;
+  const bool more = line.next(a, &p);
+  __syncwarp();
+  if (lane == 0) walk.line = line, walk.p = p;
+  __syncwarp();
+  return more;
+}
+
+// Whether any lane of four warps says so (a barrier of all four: those that share 32 rows,
+// or those that unpack).
 __device__ __forceinline__ bool rows_any(int id, bool x) {
   uint32_t r;
   asm volatile(
@@ -118,9 +142,14 @@ __device__ __forceinline__ Two add2(Two x, Two y) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t x, uint32_t y) {
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -132,111 +161,145 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ void fetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- unpacking
+// |x| < 2^exp_of(x); what is not finite counts for nothing.
+__device__ __forceinline__ int exp_of(float x) {
+  const int e = (__float_as_uint(x) >> 23) & 255;
+  return e == 255 ? -126 : e - 126;
+}
+// s (u - 8) of a code word's values (0, 4), (1, 5), (2, 6), (3, 7); step: s twice, step16: s / 16.
+// 1024 + u and 1024 + 16 u by bit operations; minus 1032 or 1152, exact.
+__device__ __forceinline__ uint4 eight_values(uint32_t x, uint32_t step, uint32_t step16) {
+  const uint32_t y = x >> 8;
+  return make_uint4(mul_f16x2(add_f16x2((x & 0x000F000Fu) | 0x64006400u, 0xE408E408u), step),
+                    mul_f16x2(add_f16x2((x & 0x00F000F0u) | 0x64006400u, 0xE480E480u), step16),
+                    mul_f16x2(add_f16x2((y & 0x000F000Fu) | 0x64006400u, 0xE408E408u), step),
+                    mul_f16x2(add_f16x2((y & 0x00F000F0u) | 0x64006400u, 0xE480E480u), step16));
+}
+
 template <int D>
-__device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, TcLine line, int warp, int lane) {
+__device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, Walk& walk, int warp, int lane) {
   constexpr int G = D / kKv4Group, W = 8 * G;  // code words of a row
   const Kv4Args& a = args.a;
-  const int key = warp * 32 + lane;
-  uint32_t n = 0;
-  TcLine::Piece p;
-  while (line.next(a, &p)) {
-    const int te = piece_end(p);
-    const int* table = a.table + p.b * a.table_stride;
-    uint4 kw[W / 4], vw[W / 4];
-    uint32_t ks[G], vs[G];
-    auto id_of = [&](int t) {
-      const int pos = t * kKeys + key;
-      return t < te && pos < p.s.len ? table[div_by(pos, args.page_div)] : -2;
-    };
-    // This thread's key of a tile: its row of the cache, none for what is no position or has no page.
-    constexpr unsigned long long kNone = ~0ull;
-    auto row_of = [&](int t, int id) {
-      const int pos = t * kKeys + key, pg = div_by(pos, args.page_div);
-      const bool ok = (unsigned)id < (unsigned)a.n_pages;
-      if (!ok && id != -2) set_status(a.status, kStatusBounds);
-      return ok ? ((unsigned long long)id * a.heads_kv + p.h) * a.page + (pos - pg * a.page) : kNone;
-    };
-    auto load = [&](const uint8_t* codes, const uint32_t* scale, unsigned long long row, uint4 (&w)[W / 4], uint32_t (&sc)[G]) {
+  const int key = warp * 32 + lane, id = 1 + kSoftWarps / kParts;  // id: their barrier
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, &sm.abort, a.status, args.wait_ns))) return true;
+    rows_leave(id);
+    return false;
+  };
+  // A group's values into a box's row.
+  auto unpack = [&](uint8_t* box, const uint32_t (&w)[W], int g, float s) {
+    const uint32_t step = pack_f16x2(s, s), step16 = pack_f16x2(s * 0.0625f, s * 0.0625f);
 #pragma unroll
-      for (int i = 0; i < W / 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(box + key * 128 + ((i ^ (key & 7)) << 4)) = eight_values(w[i * G + g], step, step16);
+  };
+  uint32_t n = 0;
+  const TcLine::Piece& p = walk.p;
+  while (advance(a, walk, lane)) {
+    const int t0 = p.t0, te = piece_end(p), len = p.s.len, h = p.h;
+    const int* table = a.table + p.b * a.table_stride;
+    // This thread's key of a tile: its row of the cache, none for what is no position or has no page.
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
+    auto page_of = [&](int t) {
+      const int pos = t * kKeys + key;
+      return t < te && pos < len ? table[div_by(pos, args.page_div)] : -2;
+    };
+    auto row_of = [&](int t, int page) {
+      const int pos = t * kKeys + key, pg = div_by(pos, args.page_div);
+      const bool ok = (unsigned)page < (unsigned)a.n_pages;
+      if (!ok && page != -2) set_status(a.status, kStatusBounds);
+      return ok ? ((uint32_t)page * a.heads_kv + h) * a.page + (pos - pg * a.page) : kNone;
+    };
+    uint32_t kw[W], vw[W], ks[G], vs[G];
+    auto load = [&](const uint8_t* codes, const uint32_t* scale, uint32_t row, uint32_t (&w)[W], uint32_t (&sc)[G]) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = 0;
 #pragma unroll
       for (int g = 0; g < G; ++g) sc[g] = 0;
       if (row != kNone) {
-        const uint4* from = reinterpret_cast<const uint4*>(codes + row * (D / 2));
+        const uint4* from = reinterpret_cast<const uint4*>(codes + (unsigned long long)row * (D / 2));
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) w[i] = __ldg(from + i);
+        for (int i = 0; i < W / 4; ++i) {
+          const uint4 v = __ldg(from + i);
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
 #pragma unroll
-        for (int g = 0; g < G; ++g) sc[g] = __ldg(scale + row * G + g);
+        for (int g = 0; g < G; ++g) sc[g] = __ldg(scale + (unsigned long long)row * G + g);
       }
     };
-    unsigned long long row = kNone, next_row = kNone;
-    if (p.t0 < te) {
-      const int id0 = id_of(p.t0);
-      int id1 = id_of(p.t0 + 1);
-      row = row_of(p.t0, id0);
+    uint32_t row = kNone, next_row = kNone;
+    int page = -2, unit_v = -119;
+    if (t0 < te) {
+      const int page0 = page_of(t0), page1 = page_of(t0 + 1);
+      page = page_of(t0 + 2);
+      row = row_of(t0, page0);
       load(a.kc, a.ks, row, kw, ks);
       load(a.vc, a.vs, row, vw, vs);
-      next_row = row_of(p.t0 + 1, id1);
+      next_row = row_of(t0 + 1, page1);
     }
-    int id = id_of(p.t0 + 2);
-    for (int t = p.t0; t < te; ++t, ++n) {
+    for (int t = t0; t < te; ++t, ++n) {
       const uint32_t st = n & 1, ph = (n >> 1) & 1;
       const bool none = row == kNone;
-      const uint32_t any_none = __ballot_sync(0xffffffffu, none);
       row = next_row;  // the next tile's
       if (t + 2 < te) {
-        next_row = row_of(t + 2, id);
+        next_row = row_of(t + 2, page);
         if (next_row != kNone) {  // on its way to L2
-          fetch_l2(a.kc + next_row * (D / 2));
-          fetch_l2(a.vc + next_row * (D / 2));
+          fetch_l2(a.kc + (unsigned long long)next_row * (D / 2));
+          fetch_l2(a.vc + (unsigned long long)next_row * (D / 2));
         }
-        id = id_of(t + 3);
+        page = page_of(t + 3);
       }
-      if (n >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait(&sm.k_empty[st], ph ^ 1, &sm.abort, a.status, args.wait_ns)))
-        return false;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(kw);  // word (i, g) at i * G + g
+      // The tile's powers of two: steps below 2^12, offsets below 2^9 (V's 2^15).
+      int ek = -119, ev = unit_v;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        uint8_t* row = sm.k[st][g] + key * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t x = w[i * G + g], y = x >> 8;
-          *reinterpret_cast<uint4*>(row + ((i ^ (key & 7)) << 4)) =
-              make_uint4(x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
-        }
-        const float s = bf16_lo(ks[g]);
-        float* sz = reinterpret_cast<float*>(&sm.ksz[st][g][key >> 1]) + (key & 1);
-        sz[0] = s, sz[2] = fmaf(-8.f, s, bf16_hi(ks[g]));
+        ek = max(ek, max(exp_of(bf16_lo(ks[g])) - 12, exp_of(bf16_hi(ks[g])) - 9));
+        ev = max(ev, max(exp_of(bf16_lo(vs[g])) - 12, exp_of(bf16_hi(vs[g])) - 15));
       }
+      ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
+      if (lane == 0) sm.exps[st][warp] = make_int2(ek, ev);
+      rows_any(id, false);
+      if (__any_sync(0xffffffffu, sm.abort.flag != 0)) {
+        rows_leave(id);
+        return false;
+      }
+#pragma unroll
+      for (int i = 0; i < kUnpackWarps; ++i) {
+        const int2 e = sm.exps[st][i];
+        ek = max(ek, e.x), ev = max(ev, e.y);
+      }
+      unit_v = ev;
+      if (n >= 2 && !wait(&sm.k_empty[st], ph ^ 1)) return false;
+      const float up_k = pow2(-ek), up_v = pow2(-ev);
+      uint32_t o[2];  // offsets of the groups, float16
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        unpack(sm.k[st][g], kw, g, bf16_lo(ks[g]) * up_k);
+        const float x = bf16_hi(ks[g]) * up_k * 64.f;  // sum(q) in qx is divided by that
+        o[g] = pack_f16x2(x, x);
+      }
+      *reinterpret_cast<uint4*>(sm.kx[st] + key * 128 + ((key & 7) << 4)) =
+          G == 2 ? make_uint4(o[0], __byte_perm(o[0], o[G - 1], 0x5410), o[G - 1], 0) : make_uint4(o[0], o[0] & 0xFFFFu, 0, 0);
       sm.dead[st][key] = none ? 1 : 0;
+      const bool any_none = __any_sync(0xffffffffu, none);
       if (lane == 0) reinterpret_cast<uint8_t*>(&sm.bad[st])[warp] = any_none ? 1 : 0;
+      if (key == 0) sm.unit[st] = make_int2(ek, ev);
+      if (t + 1 < te) load(a.kc, a.ks, row, kw, ks);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.k_full[st]);
-      if (t + 1 < te) load(a.kc, a.ks, row, kw, ks);
 
-      if (n >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait(&sm.v_empty[st], ph ^ 1, &sm.abort, a.status, args.wait_ns)))
-        return false;
-      w = reinterpret_cast<const uint32_t*>(vw);
+      if (n >= 2 && !wait(&sm.v_empty[st], ph ^ 1)) return false;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        uint8_t* row = sm.v[st][g] + key * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t x = w[i * G + g];
-          uint32_t u[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // 128 + u by bit operations, minus 136: exact
-            u[k] = add_bf16x2(((x >> (4 * k)) & 0x000F000Fu) | 0x43004300u, 0xC308C308u);
-          *reinterpret_cast<uint4*>(row + ((i ^ (key & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-        float* sb = reinterpret_cast<float*>(&sm.vsb[st][g][key >> 1]) + (key & 1);
-        sb[0] = bf16_lo(vs[g]), sb[2] = bf16_hi(vs[g]);
+        unpack(sm.v[st][g], vw, g, bf16_lo(vs[g]) * up_v);
+        *reinterpret_cast<__half*>(sm.vx[st][key / 64] + g * 128 + (((key % 64 / 8) ^ g) << 4) + key % 8 * 2) =
+            __float2half_rn(bf16_hi(vs[g]) * up_v);
       }
+      if (t + 1 < te) load(a.vc, a.vs, row, vw, vs);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.v_full[st]);
-      if (t + 1 < te) load(a.vc, a.vs, row, vw, vs);
     }
   }
   return true;
@@ -244,56 +307,59 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, T
 
 // ---------------------------------------------------------------- products
 template <int D>
-__device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, TcLine line, uint32_t tmem) {
+__device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, Walk& walk, uint32_t tmem, int lane) {
   constexpr int G = D / kKv4Group;
   const Kv4Args& a = args.a;
-  constexpr uint32_t kS = idesc_f16(kRows, kKeys), kPV = ptx::idesc_bf16(kRows, kKv4Group, false, true);
+  constexpr uint32_t kS = idesc_f16(kRows, kKeys, false), kPV = idesc_f16(kRows, D, true), kPX = idesc_f16(kRows, 16, false);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, &sm.abort, a.status, args.wait_ns));
   };
   const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.q[0]), 16, 1024), k_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.k[0][0]), 16, 1024);
-  const uint64_t v_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.v[0][0]), 16384, 1024);
+  const uint64_t qx_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.qx), 16, 1024), kx_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.kx[0]), 16, 1024);
+  const uint64_t v_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.v[0][0]), 16384, 1024), vx_desc = ptx::sdesc_sw128(ptx::smem_u32(sm.vx[0][0]), 16, 1024);
   auto scores = [&](uint32_t st) {
     ptx::tc_fence_after();
     if (ptx::elect_one()) {
       const uint64_t kd = k_desc + st * (G * 1024);
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_ss(tmem + Tmem<D>::S + g * 128, q_desc + g * 1024 + kk * 2, kd + g * 1024 + kk * 2, kS, kk > 0 ? 1u : 0u);
-      ptx::mma_commit(&sm.s_full);
+      for (int kk = 0; kk < 4 * G; ++kk)
+        ptx::mma_ss(tmem + Tmem<D>::S + st * 128, q_desc + (kk >> 2) * 1024 + (kk & 3) * 2,
+                    kd + (kk >> 2) * 1024 + (kk & 3) * 2, kS, kk > 0 ? 1u : 0u);
+      ptx::mma_ss(tmem + Tmem<D>::S + st * 128, qx_desc, kx_desc + st * 1024, kS, 1u);
+      ptx::mma_commit(&sm.s_full[st]);
       ptx::mma_commit(&sm.k_empty[st]);
     }
     __syncwarp();
   };
+  // A tile's scores take the place of those two tiles before.  A row tile's first ones
+  // follow Q, which is written when the last row tile's products are done.
   uint32_t n = 0, pieces = 0;
-  TcLine::Piece p;
-  while (line.next(a, &p)) {
-    const int te = piece_end(p);
-    if (p.t0 >= te) continue;
+  const TcLine::Piece& p = walk.p;
+  while (advance(a, walk, lane)) {
+    const int t0 = p.t0, te = piece_end(p);
+    if (t0 >= te) continue;
     if (!wait(&sm.q_full, pieces & 1)) return false;
     ++pieces;
     if (!wait(&sm.k_full[n & 1], (n >> 1) & 1)) return false;
-    if (n > 0 && !wait(&sm.s_free, (n - 1) & 1)) return false;
     scores(n & 1);
-    for (int t = p.t0; t < te; ++t, ++n) {
-      const uint32_t st = n & 1;
+    for (int t = t0; t < te; ++t, ++n) {
+      const uint32_t st = n & 1, ph = (n >> 1) & 1;
       if (t + 1 < te) {
-        if (!wait(&sm.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1) || !wait(&sm.s_free, n & 1)) return false;
-        scores((n + 1) & 1);
+        if (!wait(&sm.k_full[st ^ 1], ((n + 1) >> 1) & 1)) return false;
+        if (n > 0 && !wait(&sm.s_free[st ^ 1], ((n - 1) >> 1) & 1)) return false;
+        scores(st ^ 1);
       }
-      if (!wait(&sm.v_full[st], (n >> 1) & 1) || !wait(&sm.p_full, n & 1)) return false;
+      if (!wait(&sm.v_full[st], ph) || !wait(&sm.p_full[st], ph)) return false;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            ptx::mma_ts(tmem + Tmem<D>::O + g * 64, tmem + Tmem<D>::P + g * 64 + kk * 8,
-                        v_desc + st * (G * 1024) + g * 1024 + kk * 128, kPV,
-                        t > p.t0 || kk > 0 ? 1u : 0u);
-        ptx::mma_commit(&sm.pv_done);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t from = tmem + Tmem<D>::P + kk * 8;
+          const uint32_t acc = t > t0 || kk > 0 ? 1u : 0u;
+          ptx::mma_ts(tmem + Tmem<D>::O, from, v_desc + st * (G * 1024) + kk * 128, kPV, acc);
+          ptx::mma_ts(tmem + Tmem<D>::X, from, vx_desc + st * 256 + (kk >> 2) * 128 + (kk & 3) * 2, kPX, acc);
+        }
+        ptx::mma_commit(&sm.pv_done[st]);
         ptx::mma_commit(&sm.v_empty[st]);
       }
       __syncwarp();
@@ -304,7 +370,7 @@ __device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, 
 
 // ---------------------------------------------------------------- softmax
 template <int D>
-__device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, TcLine line, uint32_t tmem, int warp,
+__device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, Walk& walk, uint32_t tmem, int warp,
                                              int lane) {
   constexpr int G = D / kKv4Group, NV = D / kParts;  // NV: a thread's values of its row, and its columns of O
   const Kv4Args& a = args.a;
@@ -325,37 +391,36 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     if (lane == 0) ptx::mbar_arrive(bar);
   };
   uint32_t n = 0;
-  TcLine::Piece p;
-  while (line.next(a, &p)) {
-    const int te = piece_end(p), b = p.b;
+  const TcLine::Piece& p = walk.p;
+  while (advance(a, walk, lane)) {
+    const int t0 = p.t0, te = piece_end(p), all_see = p.all_see;
     const int grow = p.r0 + row;  // of the (sequence, KV head)
-    const RowPlace pl = row_place(a, p.h, min(grow, p.rows - 1));
-    const int pos = p.s.len - p.s.n + pl.token;
-    const int lim = grow >= p.rows ? kNoRow : pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
+    int lim = kNoRow;
+    if (grow < p.rows) {
+      const int pos = p.s.len - p.s.n + div_by(grow, a.by_group);
+      lim = pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
+    }
     if (p.r0 + (warp & 3) * 32 >= p.rows) {
       // No query in this warp's rows: what stands in their lanes is never read.  It keeps
-      // step with the others: a tile's arrivals come after the end of the last one's.
-      if (p.t0 < te) arrive(&sm.q_full);
-      for (int t = p.t0; t < te; ++t, ++n) {
+      // step with the others: a tile's scores come after the arrivals of two tiles before.
+      if (t0 < te) arrive(&sm.q_full);
+      for (int t = t0; t < te; ++t, ++n) {
         const uint32_t st = n & 1;
-        if (!wait(&sm.s_full, n & 1)) return false;
-        arrive(&sm.s_free);
+        if (!wait(&sm.s_full[st], (n >> 1) & 1)) return false;
+        arrive(&sm.s_free[st]);
         arrive(&sm.k_empty[st]);
-        if (n > 0 && !wait(&sm.pv_done, (n - 1) & 1)) return false;
-        arrive(&sm.p_full);
-        arrive(&sm.v_empty[st]);
+        arrive(&sm.p_full[st]);
       }
       continue;
     }
-    float rf = 1.f, rz[G], mu = 0.f, bar = -INFINITY;
-    Two l = 0, off[G];  // sums over even and odd keys
-#pragma unroll
-    for (int g = 0; g < G; ++g) rz[g] = 0.f, off[g] = 0;
+    float rf = 1.f, top = 0.f, bar = -INFINITY;
+    int unit_v = 0;
+    Two l = 0;  // sums over even and odd keys
 
-    if (p.t0 < te) {
+    if (t0 < te) {
       // Q: a quarter of this thread's row into its operand
       uint4 raw[NV / 8];
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.x) + x_row(a, p.s, b, pl) + part * NV;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.x) + x_row(a, p.s, p.b, row_place(a, p.h, min(grow, p.rows - 1))) + part * NV;
       float big = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NV / 8; ++i) {
@@ -369,21 +434,20 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
         }
       }
       sm.top[part][row] = big;
-      sm.sums[part][row][0] = sum;
+      sm.sums[part][row] = sum;
       rows_any(id, false);
       if (gone()) return false;
+      float rz[G] = {};
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         big = fmaxf(big, sm.top[i][row]);
-        rz[i * G / kParts] += sm.sums[i][row][0];
+        rz[i * G / kParts] += sm.sums[i][row];
       }
       int ex = 0;  // |q| < 2^ex: scaled below 2^14
       if (big > 0.f && big < INFINITY) frexpf(big, &ex);
       ex -= 14;
-#pragma unroll
-      for (int g = 0; g < G; ++g) rz[g] = ldexpf(rz[g], -(24 + ex));
       // at least 2^-126, at most the largest float32: scores of 0 times it stay 0
-      rf = a.scale_log2 != 0.f ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), 24 + ex), 1.17549435e-38f), 3.40282347e38f) : 1.f;
+      rf = a.scale_log2 != 0.f ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), ex), 1.17549435e-38f), 3.40282347e38f) : 1.f;
       const float up = pow2(-ex / 2) * q_sign, up2 = pow2(-ex - -ex / 2);
 #pragma unroll
       for (int i = 0; i < NV / 8; ++i) {
@@ -392,147 +456,140 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[2 * e] = bf16_lo(w[e]) * up * up2;
-          v[2 * e + 1] = bf16_hi(w[e]) * up * up2 * 0.0625f;
+          v[2 * e + 1] = bf16_hi(w[e]) * up * up2;
         }
         const int word = part * (NV / 8) + i, g = word / 8, slot = word % 8;
         *reinterpret_cast<uint4*>(sm.q[g] + row * 128 + ((slot ^ (row & 7)) << 4)) =
             make_uint4(pack_f16x2(v[0], v[4]), pack_f16x2(v[1], v[5]), pack_f16x2(v[2], v[6]), pack_f16x2(v[3], v[7]));
+      }
+      if (part == 0) {  // the groups' sums in units of 2^(ex + 6), below 2^14
+        uint32_t x[2] = {0, 0}, y[2] = {0, 0};  // a group's first two parts; its third
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float z = ldexpf(rz[g], -(ex + 6));
+          const float h = __half2float(__float2half_rn(z));
+          z -= h;
+          const float m = __half2float(__float2half_rn(z));
+          x[g] = pack_f16x2(h, m), y[g] = pack_f16x2(z - m, 0.f);
+        }
+        *reinterpret_cast<uint4*>(sm.qx + row * 128 + ((row & 7) << 4)) =
+            make_uint4(x[0], (y[0] & 0xFFFFu) | (x[1] << 16), (x[1] >> 16) | (y[1] << 16), 0);
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       arrive(&sm.q_full);
     }
 
-    for (int t = p.t0; t < te; ++t, ++n) {
+    for (int t = t0; t < te; ++t, ++n) {
       const uint32_t st = n & 1, ph = (n >> 1) & 1;
-      if (!wait(&sm.s_full, n & 1) || !wait(&sm.k_full[st], ph)) return false;
+      if (!wait(&sm.s_full[st], ph) || !wait(&sm.k_full[st], ph)) return false;
       ptx::tc_fence_after();
-      Two x[kPart / 2];  // of two neighbouring keys
-#pragma unroll
-      for (int c = 0; c < kPart; c += 16) {
-        uint32_t s0[16], s1[G == 2 ? 16 : 1];
-        ptx::tmem_ld16(lanes + Tmem<D>::S + part * kPart + c, s0);
-        if constexpr (G == 2) ptx::tmem_ld16(lanes + Tmem<D>::S + 128 + part * kPart + c, s1);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(&sm.ksz[st][0][(part * kPart + c + j) / 2]);
-          Two v = fma2(z.x, two(__uint_as_float(s0[j]), __uint_as_float(s0[j + 1])), mul2(z.y, two(rz[0], rz[0])));
-          if constexpr (G == 2) {
-            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&sm.ksz[st][G - 1][(part * kPart + c + j) / 2]);
-            v = fma2(y.x, two(__uint_as_float(s1[j]), __uint_as_float(s1[j + 1])), fma2(y.y, two(rz[G - 1], rz[G - 1]), v));
-          }
-          x[(c + j) / 2] = v;
-        }
-      }
+      uint32_t x[kPart];
+      ptx::tmem_ld32(lanes + Tmem<D>::S + st * 128 + part * kPart, x);
+      ptx::tmem_ld_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      arrive(&sm.s_free);
+      arrive(&sm.s_free[st]);
+      const int2 unit = sm.unit[st];
       const uint32_t dead = sm.bad[st];
       const int k0 = t * kKeys + part * kPart;
-      if (k0 + kPart > p.all_see || dead) {  // keys that not all rows see
+      if (k0 + kPart > all_see || dead) {  // keys that not all rows see
 #pragma unroll
-        for (int j = 0; j < kPart; j += 2) {
-          float2 v = apart(x[j / 2]);
-          if (k0 + j >= lim || sm.dead[st][part * kPart + j]) v.x = -INFINITY;
-          if (k0 + j + 1 >= lim || sm.dead[st][part * kPart + j + 1]) v.y = -INFINITY;
-          x[j / 2] = two(v.x, v.y);
-        }
+        for (int j = 0; j < kPart; ++j)
+          if (k0 + j >= lim || sm.dead[st][part * kPart + j]) x[j] = 0xFF800000u;  // minus infinity
       }
       __syncwarp();
       arrive(&sm.k_empty[st]);
       float high = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < kPart / 2; ++j) {
-        const float2 v = apart(x[j]);
-        high = fmax3f(high, v.x, v.y);
-      }
+      for (int j = 0; j < kPart; j += 2) high = fmax3f(high, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+      const float of_tile = pow2(unit.x);
+      high *= of_tile;
       const bool raise = rows_any(id, high > bar);
       if (gone()) return false;
+      float f = 1.f;
       if (raise) {
         sm.top[part][row] = high;
         rows_any(id, false);
         if (gone()) return false;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) high = fmaxf(high, sm.top[i][row]);
-        float f = 1.f;
         if (high > -INFINITY) {
           high *= rf;
           if (bar > -INFINITY) {
-            high = fmaxf(high, mu);
-            f = fast_exp2(mu - high);
+            high = fmaxf(high, top);
+            f = fast_exp2(top - high);
           }
-          mu = high;
+          top = high;
           bar = (high + 8.f) / rf;
         }
         l = mul2(l, two(f, f));
-#pragma unroll
-        for (int g = 0; g < G; ++g) off[g] = mul2(off[g], two(f, f));
-        if (t > p.t0 && __any_sync(0xffffffffu, f != 1.f)) {
-          if (!wait(&sm.pv_done, (n - 1) & 1)) return false;
+      }
+      if (t > t0) {
+        if (unit.y != unit_v) f *= unit_v - unit.y < -126 ? 0.f : pow2(unit_v - unit.y);
+        if ((raise || unit.y != unit_v) && __any_sync(0xffffffffu, f != 1.f)) {
+          if (!wait(&sm.pv_done[st ^ 1], ((n - 1) >> 1) & 1)) return false;  // (and once more below)
           ptx::tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < NV; c += 16) {
+          auto scale = [&](uint32_t at) {
             uint32_t o[16];
-            ptx::tmem_ld16(lanes + Tmem<D>::O + part * NV + c, o);
+            ptx::tmem_ld16(lanes + at, o);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            ptx::tmem_st16(lanes + Tmem<D>::O + part * NV + c, o);
-          }
+            ptx::tmem_st16(lanes + at, o);
+          };
+#pragma unroll
+          for (int c = 0; c < NV; c += 16) scale(Tmem<D>::O + part * NV + c);
+          if (part == 0) scale(Tmem<D>::X);
           ptx::tmem_st_wait();
         }
       }
-      if (!wait(&sm.v_full[st], ph) || (n > 0 && !wait(&sm.pv_done, (n - 1) & 1))) return false;
-      ptx::tc_fence_after();
-      uint32_t w[G][kPart / 2];  // weights
+      unit_v = unit.y;
+      // rf as for rf itself
+      const float r = fminf(fmaxf(rf * of_tile, 1.17549435e-38f), 3.40282347e38f), shift = 7.f - top;
+      uint32_t w[kPart / 2];  // weights
 #pragma unroll
-      for (int j = 0; j < kPart / 2; ++j) {
-        const float2 v = apart(fma2(x[j], two(rf, rf), two(-mu, -mu)));
-        const Two pr = two(fast_exp2(v.x), fast_exp2(v.y));
-        l = add2(l, pr);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(&sm.vsb[st][g][part * kPart / 2 + j]);
-          const float2 u = apart(mul2(pr, z.x));
-          w[g][j] = ptx::pack_bf16x2(u.x, u.y);
-          off[g] = fma2(pr, z.y, off[g]);
-        }
+      for (int j = 0; j < kPart; j += 2) {
+        const float2 v = apart(fma2(two(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), two(r, r), two(shift, shift)));
+        const float p0 = fast_exp2(v.x), p1 = fast_exp2(v.y);
+        l = add2(l, two(p0, p1));
+        w[j / 2] = pack_f16x2(p0, p1);
       }
-#pragma unroll
-      for (int g = 0; g < G; ++g) ptx::tmem_st16(lanes + Tmem<D>::P + g * 64 + part * (kPart / 2), w[g]);
+      if (n > 0 && !wait(&sm.pv_done[st ^ 1], ((n - 1) >> 1) & 1)) return false;
+      ptx::tc_fence_after();
+      ptx::tmem_st16(lanes + Tmem<D>::P + part * (kPart / 2), w);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      arrive(&sm.p_full);
-      arrive(&sm.v_empty[st]);
+      arrive(&sm.p_full[st]);
     }
 
     // ---- the row's sums over all keys, and its result
-    sm.sums[part][row][0] = apart(l).x + apart(l).y;
-#pragma unroll
-    for (int g = 0; g < G; ++g) sm.sums[part][row][1 + g] = apart(off[g]).x + apart(off[g]).y;
+    sm.sums[part][row] = apart(l).x + apart(l).y;
     rows_any(id, false);
     if (gone()) return false;
     float sum = 0.f, add = 0.f;  // of p; of p b for this thread's columns
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-      sum += sm.sums[i][row][0];
-      add += sm.sums[i][row][1 + part * G / kParts];
-    }
-    if (p.t0 < te) {
-      if (!wait(&sm.pv_done, (n - 1) & 1)) return false;
+    for (int i = 0; i < kParts; ++i) sum += sm.sums[i][row];
+    if (t0 < te) {
+      if (!wait(&sm.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) return false;
       ptx::tc_fence_after();
+      uint32_t o[16];
+      ptx::tmem_ld16(lanes + Tmem<D>::X, o);
+      ptx::tmem_ld_wait();
+      add = __uint_as_float(G == 2 && part >= kParts / 2 ? o[1] : o[0]);
     }
-    const float m = bar == -INFINITY ? -INFINITY : mu;
+    const RowPlace pl = row_place(a, p.h, min(grow, p.rows - 1));
+    const int b = p.b;
+    const float m = bar == -INFINITY ? -INFINITY : top - 7.f;
     const long long slot = (long long)blockIdx.x * 2 + (p.t0 == 0 ? 1 : 0);
-    const float inv = p.whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f;
+    const float inv = pow2(unit_v) * (p.whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f);
 #pragma unroll
     for (int c = 0; c < NV; c += 16) {
       uint32_t o[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j] = 0;
-      if (p.t0 < te) {
+      if (t0 < te) {
         ptx::tmem_ld16(lanes + Tmem<D>::O + part * NV + c, o);
         ptx::tmem_ld_wait();
       }
@@ -568,7 +625,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
       }
     }
     if (warp == 0 && lane == 0 && p.t0 == 0 && !p.whole)
-      args.shared[blockIdx.x] = make_int4(b, p.h, p.r0 / kRows, line.owner(p.last, line.total, line.n));
+      args.shared[blockIdx.x] = make_int4(b, p.h, p.r0 / kRows, TcLine::owner(p.last, walk.line.total, walk.line.n));
   }
   return true;
 }
@@ -587,18 +644,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_rows(const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.k_full[i], kUnpackWarps);
       ptx::mbar_init(&sm.v_full[i], kUnpackWarps);
-      ptx::mbar_init(&sm.k_empty[i], kSoftWarps + 1);  // the scales are read, the score product is done
-      ptx::mbar_init(&sm.v_empty[i], kSoftWarps + 1);
+      ptx::mbar_init(&sm.k_empty[i], kSoftWarps + 1);  // the units and dead keys are read, the score product is done
+      ptx::mbar_init(&sm.v_empty[i], 1);
+      ptx::mbar_init(&sm.s_full[i], 1);
+      ptx::mbar_init(&sm.s_free[i], kSoftWarps);
+      ptx::mbar_init(&sm.p_full[i], kSoftWarps);
+      ptx::mbar_init(&sm.pv_done[i], 1);
     }
     ptx::mbar_init(&sm.q_full, kSoftWarps);
-    ptx::mbar_init(&sm.s_full, 1);
-    ptx::mbar_init(&sm.s_free, kSoftWarps);
-    ptx::mbar_init(&sm.p_full, kSoftWarps);
-    ptx::mbar_init(&sm.pv_done, 1);
     ptx::mbar_init(&sm.drain, 1);
     sm.abort.flag = 0;
     ptx::fence_mbar_init();
   }
+  // columns and rows that no group fills
+  for (int i = threadIdx.x * 16; i < (int)sizeof(sm.qx); i += kThreads * 16) *reinterpret_cast<uint4*>(sm.qx + i) = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x * 16; i < (int)sizeof(sm.kx); i += kThreads * 16) *reinterpret_cast<uint4*>(sm.kx[0] + i) = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x * 16; i < (int)sizeof(sm.vx); i += kThreads * 16) *reinterpret_cast<uint4*>(sm.vx[0][0] + i) = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
   if (warp == kWarps - 1) {
     ptx::tmem_alloc(&sm.tmem, Tmem<D>::kCols);
     ptx::tmem_relinquish();
@@ -607,17 +669,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_rows(const __grid_constant_
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  Walk& walk = sm.walk[min(warp, kSoftWarps + kUnpackWarps)];
+  if (lane == 0 && (warp < kSoftWarps + kUnpackWarps || warp == kWarps - 1)) walk.line = line;
+  __syncwarp();
   if (warp < kSoftWarps) {
     ptx::regs_increase<kSoftRegs>();
-    softmax_role<D>(args, sm, line, tmem, warp, lane);
+    softmax_role<D>(args, sm, walk, tmem, warp, lane);
   } else if (warp < kSoftWarps + kUnpackWarps) {
-    ptx::regs_decrease<kUnpackRegs>();
-    unpack_role<D>(args, sm, line, warp - kSoftWarps, lane);
+    ptx::regs_increase<kUnpackRegs>();
+    unpack_role<D>(args, sm, walk, warp - kSoftWarps, lane);
   } else {
     ptx::regs_decrease<kIssueRegs>();
   }
   if (warp == kWarps - 1) {
-    product_role<D>(args, sm, line, tmem);
+    product_role<D>(args, sm, walk, tmem, lane);
     // every product that was issued ends before the tensor memory is given back
     if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
     __syncwarp();

@@ -115,9 +115,8 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
  *     LSE_i = ln sum_j exp(s_ij);   O_i = sum_j exp(s_ij - LSE_i) v_j.
  * A row that sees nothing (padding, an empty sequence) gets O = 0 and LSE = -inf.
  * Sums are float32.  Roundings to fewer bits, beside that of O: float32 rows none;
- * bf16 rows the weights exp(s_ij - max) times a group's step, to 11 bits for up to
- * 24 query rows of a KV head (seqlen * heads_q / heads_kv) or head_dim 256, else to
- * 8 bits.  Cached values beyond 2^96 in size may overflow the sums.
+ * bf16 rows the weights exp(s_ij - max), to 11 bits.  Cached values beyond 2^96 in
+ * size may overflow the sums.
  * y: O; lse: contiguous float32 [batch, heads_q, seqlen], packed [heads_q,
  * total_tokens].  The result is bit-identical from run to run.  workspace: device
  * scratch, 256-byte aligned, >= attn_kv4_workspace_size(p) bytes (SIZE_MAX if the

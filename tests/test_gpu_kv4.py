@@ -14,8 +14,12 @@ and sums over n positions n eps.  So each p is off by d = (D + 16) eps W + n eps
 and below float16's normal range by half its least step, 2^-25 units <= 2^-31 of the
 largest s.  With |u - 8| <= 8 and sum p >= 1 in the units that the maximum sets: 2^-11
 R (2^-23 R), R = sum p |s (u - 8)|, and n 2^-28 max s.  With more than 24 bfloat16 query
-rows on a KV head (head dim 64 or 128) the weights are bfloat16: 2^-8 R and no least
-step.  O is rounded once: 2^-8 |O| for bfloat16, eps |O| for float32.
+rows on a KV head (head dim 64 or 128) the rounded weights are p alone, in units in which 1
+is 2^7, and offsets are multiplied by them too: p' = p (1 + e), |e| <= 2^-11, or off by
+2^-25 = 2^-32 of 1 below the normal range, so that sum p' (s (u - 8) + b) is off by 2^-11 A
+and n 2^-32 (8 max s + max |b|); s (u - 8) itself is float16 in units in which the largest s
+is at least 2^11, off by 2^-36 of that (n 2^-28 max s has room for both).  O is rounded
+once: 2^-8 |O| for bfloat16, eps |O| for float32.
 """
 
 import numpy as np
@@ -87,10 +91,11 @@ def check_attend(c, q, o, lse, scale, causal, dtype, name):
         assert np.all(go[empty] == 0)
         tol = 2 * d[..., None] * A
         many = dtype == "bf16" and c.D <= 128 and max(x.shape[1] for x in q) * (q[n].shape[0] // c.Hkv) > 24
-        weights = 2.0 ** -8 if many else 2.0 ** -11
-        tol += weights * R + 2.0 ** -8 * np.abs(ro) * (1 + 2.0 ** -8) if dtype == "bf16" else 2 * EPS * (R + np.abs(ro))
+        tol += 2.0 ** -11 * (A if many else R) + 2.0 ** -8 * np.abs(ro) * (1 + 2.0 ** -8) if dtype == "bf16" else 2 * EPS * (R + np.abs(ro))
         if c.lens[n]:
             tol += c.lens[n] * 2.0 ** -28 * np.repeat(vu[1].max((1, 2)), go.shape[0] // c.Hkv)[:, None, None]
+            if many:
+                tol += c.lens[n] * 2.0 ** -32 * np.repeat(np.abs(vu[2]).max((1, 2)), go.shape[0] // c.Hkv)[:, None, None]
         err = np.abs(go - ro)
         lerr = np.abs(np.where(empty, 0, gl) - np.where(empty, 0, rl))[~empty]
         ltol = (d + 4 * EPS * np.abs(np.where(empty, 0, rl)))[~empty]
