@@ -35,7 +35,8 @@ namespace {
 
 constexpr int kRows = 128, kKeys = 128, kSpare = 2;  // kSpare: what a row tile costs beside its keys, in tiles
 constexpr int kParts = 4, kPart = kKeys / kParts;  // warps of a row, and the keys of each
-// four warps of each 32 rows, four that unpack, and four of which one issues the products
+// four warps of each 32 rows, four that unpack, and four of which one issues the products and one
+// finds the pieces of work
 constexpr int kSoftWarps = 4 * kParts, kUnpackWarps = 4, kWarps = kSoftWarps + kUnpackWarps + 4;
 constexpr int kThreads = kWarps * 32;
 // Registers: 80 a thread at launch; what the issuing warps give up the others take
@@ -44,11 +45,11 @@ constexpr int kSoftRegs = 88, kUnpackRegs = 88, kIssueRegs = 40;
 
 using TcLine = Line<kRows, kKeys, kSpare, kWarps>;
 
-// A warp's place in the block's stretch.  In shared memory: the registers are needed for a
-// tile's data.
-struct Walk {
-  TcLine line;
+// A piece of the block's stretch as one warp finds it, ahead of the others.
+struct Work {
   TcLine::Piece p;
+  int owner;  // the block whose stretch has the row tile's last keys
+  bool any;   // false: the stretch's end
 };
 
 template <int D>
@@ -66,8 +67,8 @@ struct Smem {
   int2 unit[2];                // and the tile's
   float top[kParts][kRows];  // row maxima over the parts of the keys
   float sums[kParts][kRows];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
-  Walk walk[kSoftWarps + kUnpackWarps + 1];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], work_full[2], work_free[2], q_full, drain;
+  Work work[2];
   ptx::Abort abort;
   uint32_t tmem;
 };
@@ -85,17 +86,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 }
 // Tiles of a piece that any of its rows sees.
 __device__ __forceinline__ int piece_end(const TcLine::Piece& p) { return min(p.t1, (p.klen + kKeys - 1) / kKeys); }
-
-// The warp's next piece into its place; false at the stretch's end.
-__device__ __forceinline__ bool advance(const Kv4Args& a, Walk& walk, int lane) {
-  TcLine line = walk.line;
-  TcLine::Piece p;
-  const bool more = line.next(a, &p);
-  __syncwarp();
-  if (lane == 0) walk.line = line, walk.p = p;
-  __syncwarp();
-  return more;
-}
 
 // Whether any lane of four warps says so (a barrier of all four: those that share 32 rows,
 // or those that unpack).
@@ -177,7 +167,7 @@ __device__ __forceinline__ uint4 eight_values(uint32_t x, uint32_t step, uint32_
 }
 
 template <int D>
-__device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, Walk& walk, int warp, int lane) {
+__device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, int warp, int lane) {
   constexpr int G = D / kKv4Group, W = 8 * G;  // code words of a row
   const Kv4Args& a = args.a;
   const int key = warp * 32 + lane, id = 1 + kSoftWarps / kParts;  // id: their barrier
@@ -194,8 +184,10 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, W
       *reinterpret_cast<uint4*>(box + key * 128 + ((i ^ (key & 7)) << 4)) = eight_values(w[i * G + g], step, step16);
   };
   uint32_t n = 0;
-  const TcLine::Piece& p = walk.p;
-  while (advance(a, walk, lane)) {
+  for (uint32_t m = 0;; ++m) {
+    if (!wait(&sm.work_full[m & 1], (m >> 1) & 1)) return false;
+    if (!sm.work[m & 1].any) return true;
+    const TcLine::Piece& p = sm.work[m & 1].p;
     const int t0 = p.t0, te = piece_end(p), len = p.s.len, h = p.h;
     const int* table = a.table + p.b * a.table_stride;
     // This thread's key of a tile: its row of the cache, none for what is no position or has no page.
@@ -301,13 +293,33 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, W
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.v_full[st]);
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sm.work_free[m & 1]);
   }
-  return true;
+}
+
+// ---------------------------------------------------------------- pieces
+template <int D>
+__device__ __forceinline__ bool work_role(const AttnArgs& args, Smem<D>& sm, TcLine line, int lane) {
+  for (uint32_t m = 0;; ++m) {
+    TcLine::Piece p = {};
+    const bool any = line.next(args.a, &p);
+    if (m >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait(&sm.work_free[m & 1], (m >> 1 & 1) ^ 1, &sm.abort, args.a.status, args.wait_ns)))
+      return false;
+    if (lane == 0) {
+      sm.work[m & 1].p = p;
+      sm.work[m & 1].owner = any ? TcLine::owner(p.last, line.total, line.n) : 0;
+      sm.work[m & 1].any = any;
+      ptx::mbar_arrive(&sm.work_full[m & 1]);
+    }
+    __syncwarp();
+    if (!any) return true;
+  }
 }
 
 // ---------------------------------------------------------------- products
 template <int D>
-__device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, Walk& walk, uint32_t tmem, int lane) {
+__device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, uint32_t tmem, int lane) {
   constexpr int G = D / kKv4Group;
   const Kv4Args& a = args.a;
   constexpr uint32_t kS = idesc_f16(kRows, kKeys, false), kPV = idesc_f16(kRows, D, true), kPX = idesc_f16(kRows, 16, false);
@@ -334,9 +346,12 @@ __device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, 
   // A tile's scores take the place of those two tiles before.  A row tile's first ones
   // follow Q, which is written when the last row tile's products are done.
   uint32_t n = 0, pieces = 0;
-  const TcLine::Piece& p = walk.p;
-  while (advance(a, walk, lane)) {
-    const int t0 = p.t0, te = piece_end(p);
+  for (uint32_t m = 0;; ++m) {
+    if (!wait(&sm.work_full[m & 1], (m >> 1) & 1)) return false;
+    if (!sm.work[m & 1].any) return true;
+    const int t0 = sm.work[m & 1].p.t0, te = piece_end(sm.work[m & 1].p);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sm.work_free[m & 1]);
     if (t0 >= te) continue;
     if (!wait(&sm.q_full, pieces & 1)) return false;
     ++pieces;
@@ -365,13 +380,11 @@ __device__ __forceinline__ bool product_role(const AttnArgs& args, Smem<D>& sm, 
       __syncwarp();
     }
   }
-  return true;
 }
 
 // ---------------------------------------------------------------- softmax
 template <int D>
-__device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, Walk& walk, uint32_t tmem, int warp,
-                                             int lane) {
+__device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, uint32_t tmem, int warp, int lane) {
   constexpr int G = D / kKv4Group, NV = D / kParts;  // NV: a thread's values of its row, and its columns of O
   const Kv4Args& a = args.a;
   const int part = warp >> 2, row = (warp & 3) * 32 + lane, id = 1 + (warp & 3);
@@ -391,8 +404,10 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     if (lane == 0) ptx::mbar_arrive(bar);
   };
   uint32_t n = 0;
-  const TcLine::Piece& p = walk.p;
-  while (advance(a, walk, lane)) {
+  for (uint32_t m = 0;; ++m) {
+    if (!wait(&sm.work_full[m & 1], (m >> 1) & 1)) return false;
+    if (!sm.work[m & 1].any) return true;
+    const TcLine::Piece& p = sm.work[m & 1].p;
     const int t0 = p.t0, te = piece_end(p), all_see = p.all_see;
     const int grow = p.r0 + row;  // of the (sequence, KV head)
     int lim = kNoRow;
@@ -411,6 +426,8 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
         arrive(&sm.k_empty[st]);
         arrive(&sm.p_full[st]);
       }
+      __syncwarp();
+      arrive(&sm.work_free[m & 1]);
       continue;
     }
     float rf = 1.f, top = 0.f, bar = -INFINITY;
@@ -581,7 +598,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     }
     const RowPlace pl = row_place(a, p.h, min(grow, p.rows - 1));
     const int b = p.b;
-    const float m = bar == -INFINITY ? -INFINITY : top - 7.f;
+    const float high = bar == -INFINITY ? -INFINITY : top - 7.f;
     const long long slot = (long long)blockIdx.x * 2 + (p.t0 == 0 ? 1 : 0);
     const float inv = pow2(unit_v) * (p.whole ? (sum != 0.f ? 1.f / sum : 0.f) : 1.f);
 #pragma unroll
@@ -607,10 +624,10 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
             __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + y_row(a, p.s, b, pl) + d;
             *reinterpret_cast<uint4*>(y) = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
                                                       ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
-          } else {
-            float* y = args.part_o + (slot * kRows + row) * D + d;
-            *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(y + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          } else {  // four values of all rows side by side
+            float4* y = reinterpret_cast<float4*>(args.part_o) + (slot * (D / 4) + d / 4) * kRows + row;
+            y[0] = make_float4(v[0], v[1], v[2], v[3]);
+            y[kRows] = make_float4(v[4], v[5], v[6], v[7]);
           }
         }
       }
@@ -618,16 +635,17 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     ptx::tc_fence_before();
     if (part == 0 && grow < p.rows) {
       if (p.whole) {
-        a.lse[lse_row(a, p.s, b, pl)] = row_lse(m, sum);
+        a.lse[lse_row(a, p.s, b, pl)] = row_lse(high, sum);
       } else {
-        args.part_ml[(slot * kRows + row) * 2] = m;
+        args.part_ml[(slot * kRows + row) * 2] = high;
         args.part_ml[(slot * kRows + row) * 2 + 1] = sum;
       }
     }
     if (warp == 0 && lane == 0 && p.t0 == 0 && !p.whole)
-      args.shared[blockIdx.x] = make_int4(b, p.h, p.r0 / kRows, TcLine::owner(p.last, walk.line.total, walk.line.n));
+      args.shared[blockIdx.x] = make_int4(b, p.h, p.r0 / kRows, sm.work[m & 1].owner);
+    __syncwarp();
+    arrive(&sm.work_free[m & 1]);
   }
-  return true;
 }
 
 template <int D>
@@ -636,10 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_rows(const __grid_constant_
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  TcLine line;
-  const bool any = line.begin(args.a);
-  if (threadIdx.x == 0) args.shared[blockIdx.x] = make_int4(0, 0, 0, -1);
-  if (!any) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.k_full[i], kUnpackWarps);
@@ -650,39 +664,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_rows(const __grid_constant_
       ptx::mbar_init(&sm.s_free[i], kSoftWarps);
       ptx::mbar_init(&sm.p_full[i], kSoftWarps);
       ptx::mbar_init(&sm.pv_done[i], 1);
+      ptx::mbar_init(&sm.work_full[i], 1);
+      ptx::mbar_init(&sm.work_free[i], kSoftWarps + kUnpackWarps + 1);
     }
     ptx::mbar_init(&sm.q_full, kSoftWarps);
     ptx::mbar_init(&sm.drain, 1);
     sm.abort.flag = 0;
     ptx::fence_mbar_init();
+    args.shared[blockIdx.x] = make_int4(0, 0, 0, -1);
   }
   // columns and rows that no group fills
-  for (int i = threadIdx.x * 16; i < (int)sizeof(sm.qx); i += kThreads * 16) *reinterpret_cast<uint4*>(sm.qx + i) = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x * 16; i < (int)sizeof(sm.kx); i += kThreads * 16) *reinterpret_cast<uint4*>(sm.kx[0] + i) = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x * 16; i < (int)sizeof(sm.vx); i += kThreads * 16) *reinterpret_cast<uint4*>(sm.vx[0][0] + i) = make_uint4(0, 0, 0, 0);
+  auto clear = [&](uint8_t* to, int bytes) {
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) *reinterpret_cast<uint4*>(to + i) = make_uint4(0, 0, 0, 0);
+  };
+  clear(sm.qx, sizeof(sm.qx));
+  clear(sm.kx[0], sizeof(sm.kx));
+  clear(sm.vx[0][0], sizeof(sm.vx));
   ptx::fence_proxy_async_smem();
   if (warp == kWarps - 1) {
     ptx::tmem_alloc(&sm.tmem, Tmem<D>::kCols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
+  TcLine line;
+  const bool any = line.begin(args.a);  // with barriers of the block
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  Walk& walk = sm.walk[min(warp, kSoftWarps + kUnpackWarps)];
-  if (lane == 0 && (warp < kSoftWarps + kUnpackWarps || warp == kWarps - 1)) walk.line = line;
-  __syncwarp();
+  if (!any) {
+    if (warp == kWarps - 1) ptx::tmem_dealloc(tmem, Tmem<D>::kCols);
+    return;
+  }
   if (warp < kSoftWarps) {
     ptx::regs_increase<kSoftRegs>();
-    softmax_role<D>(args, sm, walk, tmem, warp, lane);
+    softmax_role<D>(args, sm, tmem, warp, lane);
   } else if (warp < kSoftWarps + kUnpackWarps) {
     ptx::regs_increase<kUnpackRegs>();
-    unpack_role<D>(args, sm, walk, warp - kSoftWarps, lane);
+    unpack_role<D>(args, sm, warp - kSoftWarps, lane);
   } else {
     ptx::regs_decrease<kIssueRegs>();
   }
+  if (warp == kWarps - 2) work_role<D>(args, sm, line, lane);
   if (warp == kWarps - 1) {
-    product_role<D>(args, sm, walk, tmem, lane);
+    product_role<D>(args, sm, tmem, lane);
     // every product that was issued ends before the tensor memory is given back
     if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
     __syncwarp();
@@ -709,14 +733,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv4_rows_join(const __grid_con
   const int b = tile.x, h = tile.y, i0 = blockIdx.x, i1 = tile.w;
   if (i1 < 0) return;
   const Kv4Seq s = kv4_seq(a, b);
-  const int row = blockIdx.y * (kJoinThreads * 8 / D) + threadIdx.x / (D / 8), d = threadIdx.x % (D / 8) * 8;
+  const int row = threadIdx.x % kRows, d = (blockIdx.y * (kJoinThreads / kRows) + threadIdx.x / kRows) * 8;
   const int grow = tile.z * kRows + row;
   if (grow >= s.n * a.group) return;
   float o[8] = {}, m = -INFINITY, l = 0.f;
   for (int i = i0; i <= i1; ++i) {
     const long long slot = (long long)i * 2 + (i == i0 ? 1 : 0);
-    const float4* from = reinterpret_cast<const float4*>(args.part_o + (slot * kRows + row) * D + d);
-    const float4 x = __ldcg(from), y = __ldcg(from + 1);
+    const float4* from = reinterpret_cast<const float4*>(args.part_o) + (slot * (D / 4) + d / 4) * kRows + row;
+    const float4 x = __ldcg(from), y = __ldcg(from + kRows);
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.part_ml + (slot * kRows + row) * 2));
     const float top = fmaxf(m, ml.x), u = top == -INFINITY ? 0.f : top;
     const float f = m == -INFINITY ? 1.f : fast_exp2(m - u), fp = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - u);
