@@ -116,7 +116,9 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
  * A row that sees nothing (padding, an empty sequence) gets O = 0 and LSE = -inf.
  * Sums are float32.  Roundings to fewer bits, beside that of O: float32 rows none;
  * bf16 rows the weights exp(s_ij - max), to 11 bits.  Cached values beyond 2^96 in
- * size may overflow the sums.
+ * size may overflow the sums.  bf16 calls with head_dim 64 or 128 and more than 24
+ * query rows on a KV head (seqlen * heads_q / heads_kv) hold the values of one KV
+ * head in units of its largest step and offset: what is 2^25 times smaller loses bits.
  * y: O; lse: contiguous float32 [batch, heads_q, seqlen], packed [heads_q,
  * total_tokens].  The result is bit-identical from run to run.  workspace: device
  * scratch, 256-byte aligned, >= attn_kv4_workspace_size(p) bytes (SIZE_MAX if the
