@@ -103,11 +103,15 @@ struct Eight<float> {
 template <bool kClamp, class T>
 __device__ __forceinline__ uint32_t code_word(const Eight<T>& x, float b, float inv) {
   uint32_t w = 0;
+  const Two minus_b = two(-b, -b), last = two(12582920.f, 12582920.f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float m = __fmul_rn(__fsub_rn(x[k], b), inv);
-    if (kClamp) m = fminf(fmaxf(m, -8.f), 7.f);
-    w += __float_as_uint(__fadd_rn(m, 12582920.f)) << (4 * k);
+  for (int k = 0; k < 8; k += 2) {
+    // the products one by one: packed ones would be joined with the sums that follow
+    const float2 v = apart(add2(two(x[k], x[k + 1]), minus_b));
+    float m0 = __fmul_rn(v.x, inv), m1 = __fmul_rn(v.y, inv);
+    if (kClamp) m0 = fminf(fmaxf(m0, -8.f), 7.f), m1 = fminf(fmaxf(m1, -8.f), 7.f);
+    const float2 u = apart(add2(two(m0, m1), last));
+    w += (__float_as_uint(u.x) << (4 * k)) + (__float_as_uint(u.y) << (4 * k + 4));
   }
   return w - (0x4B400000u + (0x4B400000u << 4) + (0x4B400000u << 8));
 }

@@ -112,34 +112,6 @@ __device__ __forceinline__ bool rows_any(int id, bool x) {
 // the flag.
 __device__ __forceinline__ void rows_leave(int id) { asm volatile("barrier.cta.arrive %0, 128;" ::"r"(id) : "memory"); }
 
-// Two float32 numbers at a time.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float x, float y) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 apart(Two x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two x, Two y, Two z) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ Two mul2(Two x, Two y) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ Two add2(Two x, Two y) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t add_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
