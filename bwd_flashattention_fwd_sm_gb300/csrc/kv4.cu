@@ -6,8 +6,9 @@
 // position's page is looked up once, and neighbouring positions' (s, b) pairs fill
 // their 32-byte sectors.  They are bound by device memory: 2 D bytes in and D / 2 + D / 16
 // out for a bf16 row of D values, or the other way round.  Measured: 16 packed prompts of up
-// to 8192, 32 heads of 128, written and read back 483 us (5.8 TB/s; the write alone 272, issue slots 75%
-// busy, its arithmetic is next); 131072 tokens of 8 heads read 104 us (6.6 TB/s).
+// to 8192, 32 heads of 128, written and read back 473 us (5.9 TB/s); 16 of 4096 written 217 us (6.3
+// TB/s; with single sums 224: issue slots 75% busy, the arithmetic is next); 131072 tokens of 8 heads
+// read 104 us (6.6 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
