@@ -74,7 +74,11 @@ struct Smem {
   int2 exps[2][kUnpackWarps];  // the unpacking warps' powers of two (K's, V's)
   int2 unit[2];                // and the tile's
   float top[kParts][kRows];  // row maxima over the parts of the keys
-  float sums[kParts][kRows];
+  float sums[kParts][kRows];  // of Q's groups
+  // of the weights, at a piece's end, by the piece's parity: a warp that is ahead writes the next
+  // piece's while others still read this one's, and the barrier of that piece's end lies
+  // before this place is written again
+  float last[2][kParts][kRows];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], work_full[2], work_free[2], q_full, drain;
   Work work[2];
   ptx::Abort abort;
@@ -562,12 +566,12 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     }
 
     // ---- the row's sums over all keys, and its result
-    sm.sums[part][row] = apart(l).x + apart(l).y;
+    sm.last[m & 1][part][row] = apart(l).x + apart(l).y;
     rows_any(id, false);
     if (gone()) return false;
     float sum = 0.f, add = 0.f;  // of p; of p b for this thread's columns
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) sum += sm.sums[i][row];
+    for (int i = 0; i < kParts; ++i) sum += sm.last[m & 1][i][row];
     if (t0 < te) {
       if (!wait(&sm.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) return false;
       ptx::tc_fence_after();
