@@ -127,6 +127,9 @@ def make_params(q, k, *, causal=False, block_mask: BlockMask | None = None, scal
 
 
 def _workspace(nbytes: int, device, workspace=None):
+    """Device scratch of at least nbytes: the caller's tensor if it is large enough, else a new one."""
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if nbytes == SIZE_MAX:
         raise _lib.AttnError(_lib.ATTN_ERR_INVALID_ARG, "workspace size", _lib.load().attn_last_error().decode())
     if nbytes == 0:

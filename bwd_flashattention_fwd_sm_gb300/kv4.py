@@ -27,8 +27,8 @@ import math
 import torch
 
 from . import _lib
-from ._lib import ATTN_BF16, ATTN_F32, SIZE_MAX, Kv4ParamsC, check
-from .attention import SeqLens
+from ._lib import ATTN_BF16, ATTN_F32, Kv4ParamsC, check
+from .attention import SeqLens, _workspace
 
 GROUP = 64  # values that share one (s, b) pair
 
@@ -220,11 +220,7 @@ def _attend(cache, q, block_table, lens, causal, scale, seqlens, workspace, out,
                 float(scale) if scale is not None else 1.0 / math.sqrt(cache.head_dim), causal)
     lse = torch.empty(q.shape[:3] if seqlens is None else (heads, q.shape[0]), dtype=torch.float32, device=q.device)
     need = lib.attn_kv4_workspace_size(p)
-    if need == SIZE_MAX:
-        raise _lib.AttnError(_lib.ATTN_ERR_INVALID_ARG, "workspace size", lib.attn_last_error().decode())
-    ws = workspace
-    if need and (ws is None or ws.numel() * ws.element_size() < need):
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws = _workspace(need, q.device, workspace)
     check(lib.attn_fwd_kv4(p, q.data_ptr(), *cache._pointers, o.data_ptr(), lse.data_ptr(),
-                           ws.data_ptr() if need else None, need, stream), "attn_fwd_kv4")
+                           None if ws is None else ws.data_ptr(), need, stream), "attn_fwd_kv4")
     return o, lse
