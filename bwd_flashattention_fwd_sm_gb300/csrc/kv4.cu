@@ -285,9 +285,12 @@ attn_status_t kfail(attn_status_t s, const char* fmt, ...) {
   return s;
 }
 
+enum class Op { kWrite, kRead, kAttend };
+
 // Checks everything about the parameters that no data pointer is needed for and
 // fills the kernels' arguments; *empty: there is no row to deal with.
-attn_status_t resolve(const attn_kv4_params_t* p, bool attention, Kv4Args* a, bool* empty) {
+attn_status_t resolve(const attn_kv4_params_t* p, Op op, Kv4Args* a, bool* empty) {
+  const bool attention = op == Op::kAttend;
   std::memset(a, 0, sizeof(*a));
   set_last_error_text("");
   if (!p) return kfail(ATTN_ERR_INVALID_ARG, "params is NULL");
@@ -348,6 +351,11 @@ attn_status_t resolve(const attn_kv4_params_t* p, bool attention, Kv4Args* a, bo
     if (strides[i] < 0 || strides[i] % align)
       return kfail(ATTN_ERR_INVALID_ARG, "%s=%lld must be a non-negative multiple of %d elements", names[i], strides[i],
                    align);
+    const long long entries = i % 3 == 0 ? p->batch : i % 3 == 1 ? heads : p->cu_seqlens ? total : p->seqlen;
+    const bool output = op == Op::kRead || (op == Op::kAttend && i >= 3);
+    if (output && entries > 1 && strides[i] < p->head_dim)
+      return kfail(ATTN_ERR_INVALID_ARG, "%s=%lld over %lld entries: rows of an output must not overlap", names[i],
+                   strides[i], entries);
   }
   a->table = p->block_table;
   a->table_stride = p->table_stride;
@@ -425,7 +433,7 @@ attn_status_t attn_kv4_write(const attn_kv4_params_t* p, const void* x, const vo
                              void* v_codes, void* v_scale, void* stream) {
   Kv4Args a;
   bool empty = false;
-  attn_status_t s = resolve(p, false, &a, &empty);
+  attn_status_t s = resolve(p, Op::kWrite, &a, &empty);
   if (s != ATTN_OK || empty) return s;
   if ((s = check_pointers(p, x, y, k_codes, k_scale, v_codes, v_scale))) return s;
   int sms = 0;
@@ -445,7 +453,7 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
                             const void* v_scale, void* x, void* y, void* stream) {
   Kv4Args a;
   bool empty = false;
-  attn_status_t s = resolve(p, false, &a, &empty);
+  attn_status_t s = resolve(p, Op::kRead, &a, &empty);
   if (s != ATTN_OK || empty) return s;
   if ((s = check_pointers(p, x, y, k_codes, k_scale, v_codes, v_scale))) return s;
   int sms = 0;
@@ -464,7 +472,7 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
 size_t attn_kv4_workspace_size(const attn_kv4_params_t* p) {
   Kv4Args a;
   bool empty = false;
-  if (resolve(p, true, &a, &empty) != ATTN_OK) return SIZE_MAX;
+  if (resolve(p, Op::kAttend, &a, &empty) != ATTN_OK) return SIZE_MAX;
   return empty ? 0 : attention_workspace(a, p->head_dim, p->dtype == ATTN_BF16);
 }
 
@@ -473,7 +481,7 @@ attn_status_t attn_fwd_kv4(const attn_kv4_params_t* p, const void* x, const void
                            size_t workspace_bytes, void* stream) {
   Kv4Args a;
   bool empty = false;
-  attn_status_t s = resolve(p, true, &a, &empty);
+  attn_status_t s = resolve(p, Op::kAttend, &a, &empty);
   if (s != ATTN_OK || empty) return s;
   if ((s = check_pointers(p, x, y, k_codes, k_scale, v_codes, v_scale))) return s;
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))

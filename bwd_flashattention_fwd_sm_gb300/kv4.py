@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import math
 
+import numpy as np
 import torch
 
 from . import _lib
@@ -87,10 +88,35 @@ def _usable(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _rows_overlap(shape, strides):
+    """Whether two rows (the last axis, of stride 1) of such a tensor share an element."""
+    axes = sorted((s, n) for s, n in zip(strides[:-1], shape[:-1]) if n > 1)
+    span, apart = shape[-1], True  # each axis steps over all that the ones before it span: the usual layouts
+    for s, n in axes:
+        if s < shape[-1]:
+            return True
+        apart = apart and s >= span
+        span += (n - 1) * s
+    if apart:
+        return False
+    # all steps along the shorter axes: is there one along the longest that leads back?
+    (far, most), *rest = sorted(axes, key=lambda a: -a[1])
+    d = np.zeros(1, np.int64)
+    for s, n in rest:
+        d = (d[:, None] + np.arange(1 - n, n, dtype=np.int64) * s).ravel()
+    for k in range(-1, 2):
+        to = -(d // far) + k
+        hit = (np.abs(d + to * far) < shape[-1]) & (np.abs(to) < most)
+        hit[len(d) // 2] &= to[len(d) // 2] != 0  # a row and itself
+        if hit.any():
+            return True
+    return False
+
+
 def _fits(t):
     """Whether an output tensor can be written in place."""
     return t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(
-        s % (16 // t.element_size()) == 0 for s in t.stride()[:-1])
+        s % (16 // t.element_size()) == 0 for s in t.stride()[:-1]) and not _rows_overlap(t.shape, t.stride())
 
 
 def _params(x, y, cache, block_table, lens, seqlens, heads_q, heads_kv, scale=0.0, causal=True):
@@ -191,8 +217,10 @@ def _read(cache, block_table, lens, seqlen, seqlens, dtype, out, stream):
         k, v = out
         for t in out:
             if tuple(t.shape) != shape or t.dtype != k.dtype or t.device != cache.device or not _fits(t):
-                raise ValueError(f"out must be two CUDA tensors of shape {shape} and one dtype, rows contiguous "
-                                 "and 16-byte aligned")
+                raise ValueError(f"out must be two CUDA tensors of shape {shape} and one dtype, rows contiguous, "
+                                 "16-byte aligned and apart")
+        if k.numel() and k.data_ptr() == v.data_ptr():
+            raise ValueError("out: k and v are the same memory")
     p = _params(k, v, cache, block_table, lens, seqlens, H, H)
     check(_lib.load().attn_kv4_read(p, *cache._pointers, k.data_ptr(), v.data_ptr(), stream), "attn_kv4_read")
     return k, v
@@ -214,7 +242,7 @@ def _attend(cache, q, block_table, lens, causal, scale, seqlens, workspace, out,
     else:
         o = out
         if o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or not _fits(o):
-            raise ValueError("out must match q in shape, dtype and device, rows contiguous and 16-byte aligned")
+            raise ValueError("out must match q in shape, dtype and device, rows contiguous, 16-byte aligned and apart")
     heads = q.shape[1] if q.dim() > 1 else 0
     p = _params(q, o, cache, block_table, lens, seqlens, heads, cache.heads_kv,
                 float(scale) if scale is not None else 1.0 / math.sqrt(cache.head_dim), causal)

@@ -45,8 +45,9 @@
  *
  * Constraints.  head_dim 64, 128 or 256; page_size a positive multiple of 16;
  * heads_q % heads_kv == 0; x and y and the code arrays 16-byte aligned, scale
- * arrays 16-byte aligned too; strides multiples of 16 bytes; fewer than 2^31 rows
- * over all heads in one call.  Offsets into the cache are 64-bit.  The attention
+ * arrays 16-byte aligned too; strides multiples of 16 bytes, not negative; rows of an
+ * output must not overlap (refused where one stride alone makes them: one below head_dim over
+ * more than one entry); fewer than 2^31 rows over all heads in one call.  Offsets into the cache are 64-bit.  The attention
  * takes up to 2^30 query rows over all heads, up to 2^30 positions in a page list
  * and fewer than 2^32 rows (n_pages * heads_kv * page_size) in the cache.
  *
