@@ -176,14 +176,12 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, i
     const int* table = a.table + p.b * a.table_stride;
     // This thread's key of a tile: its row of the cache, none for what is no position or has no page.
     constexpr uint32_t kNone = 0xFFFFFFFFu;
-    auto page_of = [&](int t) {
-      const int pos = t * kKeys + key;
-      return t < te && pos < len ? table[div_by(pos, args.page_div)] : -2;
-    };
+    auto held = [&](int t) { return t < te && t * kKeys + key < len; };
+    auto page_of = [&](int t) { return held(t) ? table[div_by(t * kKeys + key, args.page_div)] : -1; };
     auto row_of = [&](int t, int page) {
       const int pos = t * kKeys + key, pg = div_by(pos, args.page_div);
       const bool ok = (unsigned)page < (unsigned)a.n_pages;
-      if (!ok && page != -2) set_status(a.status, kStatusBounds);
+      if (!ok && held(t)) set_status(a.status, kStatusBounds);
       return ok ? ((uint32_t)page * a.heads_kv + h) * a.page + (pos - pg * a.page) : kNone;
     };
     uint32_t kw[W], vw[W], ks[G], vs[G];
@@ -204,7 +202,7 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, i
       }
     };
     uint32_t row = kNone, next_row = kNone;
-    int page = -2, unit_v = -119;
+    int page = -1, unit_v = -119;
     if (t0 < te) {
       const int page0 = page_of(t0), page1 = page_of(t0 + 1);
       page = page_of(t0 + 2);
