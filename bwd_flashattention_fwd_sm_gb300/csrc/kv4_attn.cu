@@ -13,9 +13,11 @@
 //      row scaled by its own power of two, those of
 //      the second kind of pair by 1/16 more.  With s, b a key's step and offset of a
 //      group, its part of the score is s sum(q u) + (b - 8 s) sum(q), in float32.
-//   V: the same pairs, two keys side by side.  The weights p s are float16 too, in units
-//      of a power of two that follows the largest step seen, so that the largest is below
-//      2^15: 11 bits down to 2^-29 of that, and off by at most 2^-40 of it below.
+//   V: the same pairs, two keys side by side.  The weights p s are float16 too, each row's and
+//      group's in units of a power of two of its own that follows the largest p s it has met, so
+//      that this is 2^4 at least and 2^15 at most: 11 bits down to 2^-18 of it, off by at most
+//      2^-29 of it below.  Units of the largest step would lose the sums of a row whose weight
+//      lies on a position with small steps, such as a first token that all look at.
 //      Sums of u instead of u - 8 would cancel against 8 sum(p s) over long contexts, so
 //      a ninth product counts -8 sum(p s) beside them and is folded in every 128 keys;
 //      the offsets' part sum(p b) stays in float32.
@@ -24,8 +26,8 @@
 //      of 2^4, 2^-6 and 2^-16, and the weights two, of 2^5 and 2^-6, each part of at most
 //      11 bits: over 64 values or 16 keys, its products with u - 8 (exact in float16) add
 //      up to less than 2^24 of its grid, nothing is cut off, and float32 additions join
-//      the parts and the keys.  What is left of a weight, below 2^-7, is two more parts,
-//      off by 2^-25 in the end.  3e-7 of O at any length.
+//      the parts and the keys.  What is left of a weight, below 2^-7, is two more parts
+//      in units of 2^-12, off by 2^-37 in the end, 2^-41 of the row's largest p s.
 //
 // Work.  A tile is the keys that a block's warps take at a time; the tiles of all
 // sequences, KV heads and row tiles stand in one line that is cut into equal
@@ -34,7 +36,7 @@
 // result, which a second kernel joins in order, so results do not vary.
 //
 // Measured (bf16, 32 heads on 8 of 128): 64 sequences of up to 8192, one token each, 76 us, 60% of
-// the rate of a copy; a sequence of 131072 39 us, 57%; one of 777 9.1 us with both kernels. The
+// the rate of a copy; a sequence of 131072 38 us, 58%; one of 777 9.2 us with both kernels. The
 // instructions bound it: ALU 46% and tensor pipe 26% busy, hardly a warp waits for memory, and
 // without the arithmetic the same copies run at the rate of memory.  4 products and 16 bit operations
 // take 51 to 60 cycles of a sub-core where the longer of the two alone takes 32.
@@ -52,7 +54,11 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;  // each warp joins and stores a quarter of a row tile's sums
 
-constexpr int kLeastUnit = -119;  // 2^(7 - unit) is a float32
+// Scores may be 2^kSlack above the running maximum, steps 2^kRoom in the weights' units; together
+// they stay at 2^15.  A weight that is found too large is brought below 2^kSet, so that steps
+// of four times its size still have room.
+constexpr int kSlack = 8, kRoom = 15 - kSlack, kSet = kRoom - 2;
+constexpr int kFinest = 126;  // the weights' largest power of two: it and its reciprocal are normal numbers
 
 // What a row tile costs beside its keys (queries into operands, the warps' results
 // joined), in tiles: the line has that many empty places before a row tile's keys.  2, 6 and
@@ -79,6 +85,9 @@ struct Shape {
   // Sums of u beside a count of -8 sum(p s): cheaper than subtracting 8 from each
   // code while there are few columns and registers for the count.
   static constexpr bool COUNT = NT == 1 && !F32;
+  // The weights' units: a lane's own, or a warp's in shared memory where registers are short (16
+  // sequences of up to 4100, bf16: head dim 256, 16 rows 41.3 and 40.3 us, 128, 20 rows 47.5 and 47.0).
+  static constexpr bool UP_SMEM = G * NT > 4;
   static constexpr int GRID = kSms * BLOCKS;
   static constexpr size_t Q_BYTES = (size_t)G * 4 * NT * QP * 32 * 8;
   static constexpr size_t MERGE_BYTES = (size_t)kWarps * ACC * 32 * 4, RING_BYTES = (size_t)kWarps * STAGES * STAGE_BYTES;
@@ -121,6 +130,12 @@ template <int k>
 __device__ __forceinline__ float on_grid(float x) {
   constexpr float kBig = k >= 0 ? 12582912.f * (1 << (k >= 0 ? k : 0)) : 12582912.f / (1 << (k < 0 ? -k : 0));
   return __fsub_rn(__fadd_rn(x, kBig), kBig);
+}
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }  // x > 0, normal
+__device__ __forceinline__ uint32_t max_u16(uint32_t x, uint32_t y) {  // of both halves
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
 }
 __device__ __forceinline__ uint32_t add_f16(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -221,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
   __shared__ __align__(16) float row_f[R], row_z[G][R];  // read in pairs
   __shared__ int row_lim[R];
   __shared__ float warp_m[kWarps][R], warp_l[kWarps][R];
+  __shared__ __align__(16) float warp_up[S::UP_SMEM ? kWarps : 1][S::UP_SMEM ? G : 1][R];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -364,18 +380,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     }
     __syncthreads();
 
-    // sums in units of 2^(unit[g] - 7 - 24) (values 0, 2, 4, 6 of a word) and 2^4 of it (1, 3, 5, 7);
-    // minus[g]: -8 sum(p s) since it was last folded in
+    // up: the power of two that two rows' weights of a group are multiplied by; cap: steps that it leaves room
+    // for.  acc: sums of those weights and u, in units of 2^-24 (values 0, 2, 4, 6 of a word) and
+    // 2^-20 (1, 3, 5, 7).  minus: -8 sum(p s) since it was last folded in.
     float acc[G][4][NT][4], minus[S::COUNT ? G : 1][NT][4], accb[G][NT][2], bar[NT][2], mu[NT][2], l[NT][2];
-    int unit[G];
-    float cap[G], per_unit[G];  // 2^unit, 2^(7 - unit)
+    float cap[G];
+    float2 own_up[S::UP_SMEM ? 1 : G][S::UP_SMEM ? 1 : NT];
+    auto up = [&](int g, int nt) -> float2& {
+      return S::UP_SMEM ? *reinterpret_cast<float2*>(&warp_up[S::UP_SMEM ? warp : 0][S::UP_SMEM ? g : 0][nt * 8 + 2 * t4])
+                        : own_up[S::UP_SMEM ? 0 : g][S::UP_SMEM ? 0 : nt];
+    };
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      unit[g] = kLeastUnit;
-      cap[g] = pow2(kLeastUnit);
-      per_unit[g] = pow2(7 - kLeastUnit);
+      cap[g] = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        up(g, nt) = make_float2(pow2(kFinest), pow2(kFinest));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (S::COUNT) minus[g][nt][e] = 0.f;
@@ -389,6 +409,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) bar[nt][e] = -INFINITY, mu[nt][e] = l[nt][e] = 0.f;
+    // A row's sums of a group times f.
+    auto rescale = [&](int g, int nt, int e, float f) {
+      if constexpr (S::COUNT) minus[g][nt][e] *= f;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] *= f, acc[g][mt][nt][2 + e] *= f;
+    };
     auto fold = [&]() {
       if constexpr (S::COUNT) {
 #pragma unroll
@@ -513,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           }
         }
       }
-      // The running maximum is raised only when a score is above it by more than 2^8,
-      // the unit only when a step is above it.
+      // The running maximum is raised only when a score is above it by more than 2^kSlack, the
+      // weights are looked at only then or when a step is above what their units have room for.
       float high[NT][2], step[G];
       bool over = false;
 #pragma unroll
@@ -535,19 +561,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         step[g] = v;
         over |= v > cap[g];
       }
-      if (__any_sync(0xffffffffu, over)) {
-        float fg[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float v = step[g];
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          const int nu = max(unit[g], min((int)(__float_as_uint(v) >> 23) - 126, 127));  // v < 2^nu
-          fg[g] = unit[g] - nu < -126 ? 0.f : pow2(unit[g] - nu);
-          unit[g] = nu;
-          cap[g] = pow2(nu);
-          per_unit[g] = pow2(7 - nu);
-        }
+      over = __any_sync(0xffffffffu, over);
+      float fall[NT][2];  // what the weights so far are multiplied by, if over
+      if (over) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -564,16 +580,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
                 f = fast_exp2(mu[nt][e] - v);
               }
               mu[nt][e] = v;
-              bar[nt][e] = (v + 8.f) / r;
+              bar[nt][e] = (v + (float)kSlack) / r;
             }
             l[nt][e] *= f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              accb[g][nt][e] *= f;
-              if constexpr (S::COUNT) minus[g][nt][e] *= f * fg[g];
-#pragma unroll
-              for (int mt = 0; mt < 4; ++mt) acc[g][mt][nt][e] *= f * fg[g], acc[g][mt][nt][2 + e] *= f * fg[g];
-            }
+            for (int g = 0; g < G; ++g) accb[g][nt][e] *= f;
+            fall[nt][e] = f;
           }
       }
 #pragma unroll
@@ -587,6 +599,42 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
             l[nt][e & 1] += x[c][nt][e];
           }
       }
+      if (over) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          int most = -kFinest;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float v[2] = {0.f, 0.f};  // the rows' largest weights here
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                v[e] = fmax3f(v[e], x[c][nt][e] * bf16_lo(vsw[c][0][g]), x[c][nt][2 + e] * bf16_lo(vsw[c][1][g]));
+            uint32_t both = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x7632);  // their first 16 bits
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) both = max_u16(both, __shfl_xor_sync(0xffffffffu, both, o));
+            const float2 u = up(g, nt);
+            if constexpr (S::UP_SMEM) __syncwarp();  // read by all lanes
+            float to[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int size = (int)(both >> (e ? 23 : 7) & 255u) - 127;  // 2^size <= v < 2^(size + 1)
+              // the sums' factor f: its power of two goes into the units, what is left of it is 1 to 2
+              const float f = fall[nt][e];
+              const int was = exponent(e ? u.y : u.x), less = f > 0.f ? -exponent(f) : 2 * kFinest;
+              int now = min(was + less, kFinest);
+              if (size + now >= kSet) now = kSet - 1 - size;
+              const int by = now - was - less;
+              rescale(g, nt, e, f > 0.f && by >= -126 ? f * pow2(less) * pow2(by) : 0.f);
+              most = max(most, now);
+              to[e] = pow2(now);
+            }
+            up(g, nt) = make_float2(to[0], to[1]);
+          }
+          cap[g] = pow2(min(kRoom - most, 127));
+        }
+      }
 
       // O^T += V^T (p s), and the offsets' sums
 #pragma unroll
@@ -596,10 +644,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           uint32_t pb[PP][NT][2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float st = bf16_lo(vsw[c][y][g]) * per_unit[g], o = bf16_hi(vsw[c][y][g]);
+            const float st = bf16_lo(vsw[c][y][g]), o = bf16_hi(vsw[c][y][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float p0 = x[c][nt][2 * y] * st, p1 = x[c][nt][2 * y + 1] * st;
+              // p s first: it is finite where s times the units may not be
+              const float2 u = up(g, nt);
+              const Two ps = mul2(two(x[c][nt][2 * y], x[c][nt][2 * y + 1]), two(st, st));
+              float p0 = apart(mul2(ps, two(u.x, u.y))).x, p1 = apart(mul2(ps, two(u.x, u.y))).y;
               accb[g][nt][0] = fmaf(x[c][nt][2 * y], o, accb[g][nt][0]);
               accb[g][nt][1] = fmaf(x[c][nt][2 * y + 1], o, accb[g][nt][1]);
 #pragma unroll
@@ -611,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
                 const uint32_t v = pack_f16(t0, t1);
                 pb[part][nt][y] = transpose8(v);
                 if (part + 1 < PP) p0 -= half_lo(v), p1 -= half_hi(v);
+                if (F32 && part == 1) p0 *= 0x1p12f, p1 *= 0x1p12f;
               }
             }
           }
@@ -644,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
                   else mma_f16(sum[2], av, pb[part][nt][0], pb[part][nt][1]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[g][mt][nt][e] += sum[0][e] + (sum[1][e] + sum[2][e]);
+                for (int e = 0; e < 4; ++e) acc[g][mt][nt][e] += sum[0][e] + fmaf(sum[2][e], 0x1p-12f, sum[1][e]);
               } else {
                 mma_f16(acc[g][mt][nt], av, pb[0][nt][0], pb[0][nt][1]);
               }
@@ -666,10 +718,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) accb[g][nt][e] += __shfl_xor_sync(0xffffffffu, accb[g][nt][e], o);
+          const float down = pow2(-exponent(e ? up(g, nt).y : up(g, nt).x));
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p17f, pow2(unit[g]), accb[g][nt][e]);
-            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p13f, pow2(unit[g]), accb[g][nt][e]);
+            acc[g][mt][nt][e] = fmaf(acc[g][mt][nt][e] * 0x1p24f, down, accb[g][nt][e]);
+            acc[g][mt][nt][2 + e] = fmaf(acc[g][mt][nt][2 + e] * 0x1p20f, down, accb[g][nt][e]);
           }
         }
 

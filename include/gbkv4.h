@@ -115,11 +115,17 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
  *     s_ij = scale <q_i, k_j> for j < lens[n] and, with causal, j <= i;
  *     LSE_i = ln sum_j exp(s_ij);   O_i = sum_j exp(s_ij - LSE_i) v_j.
  * A row that sees nothing (padding, an empty sequence) gets O = 0 and LSE = -inf.
- * Sums are float32.  Roundings to fewer bits, beside that of O: float32 rows none;
- * bf16 rows the weights exp(s_ij - max), to 11 bits.  Cached values beyond 2^96 in
- * size may overflow the sums.  bf16 calls with head_dim 64 or 128 and more than 24
- * query rows on a KV head (seqlen * heads_q / heads_kv) hold the values of one KV
- * head in units of its largest step and offset: what is 2^25 times smaller loses bits.
+ * Sums are float32.  Roundings to fewer bits, beside that of O:
+ *   float32 rows  none but at the far end: queries to 2^-30 of a row's largest element, the weights
+ *     p_j s_j (p_j = exp(s_ij - LSE_i), s_j a group's step) to 2^-41 of the row's largest;
+ *   bf16 rows     the weights p_j s_j, to 11 bits, or to 2^-29 of the row's largest where that is
+ *     more; query elements 2^26 times smaller than a row's largest lose bits.
+ * bf16 calls with head_dim 64 or 128 and more than 24 query rows on a KV head (seqlen * heads_q /
+ * heads_kv) round the weights p_j instead, to 11 bits, or to 2^-32 of the row's largest, and hold the
+ * cache's values of 128 keys (V: of all keys so far) in units of the largest step and offset among
+ * them: steps that are 2^25 times smaller than the largest step, or than the largest offset 2^22 (keys)
+ * or 2^28 (values) times, lose bits.
+ * Cached values beyond 2^96 in size may overflow the sums.
  * y: O; lse: contiguous float32 [batch, heads_q, seqlen], packed [heads_q,
  * total_tokens].  The result is bit-identical from run to run.  workspace: device
  * scratch, 256-byte aligned, >= attn_kv4_workspace_size(p) bytes (SIZE_MAX if the
