@@ -102,6 +102,11 @@ __device__ __forceinline__ long long kv4_row(const Kv4Args& a, int b, int h, int
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Whether both bf16 numbers of a pair are finite.
+__device__ __forceinline__ bool finite2(uint32_t w) {
+  return (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) == 0;  // an exponent of ones carries
+}
+
 // Two float32 numbers at a time.
 using Two = unsigned long long;
 __device__ __forceinline__ Two two(float x, float y) {

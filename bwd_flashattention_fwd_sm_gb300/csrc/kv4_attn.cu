@@ -536,6 +536,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
               for (int g = 0; g < G; ++g) vsw[c][y][g] = 0;
             }
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              if (!finite2(vsw[c][y][g])) {  // to the rows that see it alone: 0 times it is not 0
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (key < row_lim[nt * 8 + 2 * t4 + e]) accb[g][nt][e] = NAN;
+                vsw[c][y][g] = 0;
+              }
           }
         }
       }

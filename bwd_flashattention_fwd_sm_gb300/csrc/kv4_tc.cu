@@ -58,6 +58,7 @@ struct Work {
   TcLine::Piece p;
   int owner;  // the block whose stretch has the row tile's last keys
   bool any;   // false: the stretch's end
+  int odd[2];  // the first position of the piece's keys whose value is not finite, by groups
 };
 
 template <int D>
@@ -135,10 +136,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ void fetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- unpacking
-// |x| < 2^exp_of(x); what is not finite counts for nothing.
+// |x| < 2^size_of(x), kNotFinite for what is not finite; that counts for nothing in exp_of.
+constexpr int kNotFinite = 129;
+__device__ __forceinline__ int size_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255) - 126; }
 __device__ __forceinline__ int exp_of(float x) {
-  const int e = (__float_as_uint(x) >> 23) & 255;
-  return e == 255 ? -126 : e - 126;
+  const int e = size_of(x);
+  return e == kNotFinite ? -126 : e;
 }
 // s (u - 8) of a code word's values (0, 4), (1, 5), (2, 6), (3, 7); step: s twice, step16: s / 16.
 // 1024 + u and 1024 + 16 u by bit operations; minus 1032 or 1152, exact.
@@ -157,6 +160,12 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, i
   const int key = warp * 32 + lane, id = 1 + kSoftWarps / kParts;  // id: their barrier
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, &sm.abort, a.status, args.wait_ns))) return true;
+    rows_leave(id);
+    return false;
+  };
+  auto meet = [&]() {  // the barrier of these warps; false: one of them has given up
+    rows_any(id, false);
+    if (!__any_sync(0xffffffffu, sm.abort.flag != 0)) return true;
     rows_leave(id);
     return false;
   };
@@ -225,22 +234,34 @@ __device__ __forceinline__ bool unpack_role(const AttnArgs& args, Smem<D>& sm, i
       }
       // The tile's powers of two: steps below 2^12, offsets below 2^9 (V's 2^15).
       int ek = -119, ev = unit_v;
+      auto powers = [&]() {
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        ek = max(ek, max(exp_of(bf16_lo(ks[g])) - 12, exp_of(bf16_hi(ks[g])) - 9));
-        ev = max(ev, max(exp_of(bf16_lo(vs[g])) - 12, exp_of(bf16_hi(vs[g])) - 15));
-      }
-      ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
-      if (lane == 0) sm.exps[st][warp] = make_int2(ek, ev);
-      rows_any(id, false);
-      if (__any_sync(0xffffffffu, sm.abort.flag != 0)) {
-        rows_leave(id);
-        return false;
-      }
+        for (int g = 0; g < G; ++g) {
+          ek = max(ek, max(exp_of(bf16_lo(ks[g])) - 12, exp_of(bf16_hi(ks[g])) - 9));
+          ev = max(ev, max(size_of(bf16_lo(vs[g])) - 12, size_of(bf16_hi(vs[g])) - 15));
+        }
+        ek = __reduce_max_sync(0xffffffffu, ek), ev = __reduce_max_sync(0xffffffffu, ev);
+        if (lane == 0) sm.exps[st][warp] = make_int2(ek, ev);
+        if (!meet()) return false;
 #pragma unroll
-      for (int i = 0; i < kUnpackWarps; ++i) {
-        const int2 e = sm.exps[st][i];
-        ek = max(ek, e.x), ev = max(ev, e.y);
+        for (int i = 0; i < kUnpackWarps; ++i) {
+          const int2 e = sm.exps[st][i];
+          ek = max(ek, e.x), ev = max(ev, e.y);
+        }
+        return true;
+      };
+      if (!powers()) return false;
+      if (ev >= kNotFinite - 15) {
+        // There may be a value that is not finite: it stays out of the product (0 times it is not 0),
+        // the rows that see it learn of it beside the product.
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if (!finite2(vs[g])) {
+            atomicMin(&sm.work[m & 1].odd[g], t * kKeys + key);
+            vs[g] = 0;
+          }
+        ev = unit_v;
+        if (!meet() || !powers()) return false;  // the others have read
       }
       unit_v = ev;
       if (n >= 2 && !wait(&sm.k_empty[st], ph ^ 1)) return false;
@@ -292,6 +313,7 @@ __device__ __forceinline__ bool work_role(const AttnArgs& args, Smem<D>& sm, TcL
       sm.work[m & 1].p = p;
       sm.work[m & 1].owner = any ? TcLine::owner(p.last, line.total, line.n) : 0;
       sm.work[m & 1].any = any;
+      sm.work[m & 1].odd[0] = sm.work[m & 1].odd[1] = kNoRow;
       ptx::mbar_arrive(&sm.work_full[m & 1]);
     }
     __syncwarp();
@@ -385,6 +407,11 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
   auto arrive = [&](uint64_t* bar) {
     if (lane == 0) ptx::mbar_arrive(bar);
   };
+  auto limit = [&](const TcLine::Piece& p, int row) {  // the keys that a row sees
+    if (p.r0 + row >= p.rows) return kNoRow;
+    const int pos = p.s.len - p.s.n + div_by(p.r0 + row, a.by_group);
+    return pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
+  };
   uint32_t n = 0;
   for (uint32_t m = 0;; ++m) {
     if (!wait(&sm.work_full[m & 1], (m >> 1) & 1)) return false;
@@ -392,11 +419,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
     const TcLine::Piece& p = sm.work[m & 1].p;
     const int t0 = p.t0, te = piece_end(p), all_see = p.all_see;
     const int grow = p.r0 + row;  // of the (sequence, KV head)
-    int lim = kNoRow;
-    if (grow < p.rows) {
-      const int pos = p.s.len - p.s.n + div_by(grow, a.by_group);
-      lim = pos < 0 ? 0 : a.causal ? pos + 1 : p.s.len;
-    }
+    const int lim = limit(p, row);
     if (p.r0 + (warp & 3) * 32 >= p.rows) {
       // No query in this warp's rows: what stands in their lanes is never read.  It keeps
       // step with the others: a tile's scores come after the arrivals of two tiles before.
@@ -576,7 +599,8 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& args, Smem<D>& sm, 
       uint32_t o[16];
       ptx::tmem_ld16(lanes + Tmem<D>::X, o);
       ptx::tmem_ld_wait();
-      add = __uint_as_float(G == 2 && part >= kParts / 2 ? o[1] : o[0]);
+      const int g = G == 2 && part >= kParts / 2 ? 1 : 0;  // of this thread's columns
+      add = limit(p, row) > sm.work[m & 1].odd[g] ? NAN : __uint_as_float(g ? o[1] : o[0]);
     }
     const RowPlace pl = row_place(a, p.h, min(grow, p.rows - 1));
     const int b = p.b;

@@ -114,7 +114,8 @@ attn_status_t attn_kv4_read(const attn_kv4_params_t* p, const void* k_codes, con
  * and the row of position i of sequence n,
  *     s_ij = scale <q_i, k_j> for j < lens[n] and, with causal, j <= i;
  *     LSE_i = ln sum_j exp(s_ij);   O_i = sum_j exp(s_ij - LSE_i) v_j.
- * A row that sees nothing (padding, an empty sequence) gets O = 0 and LSE = -inf.
+ * A row that sees nothing (padding, an empty sequence) gets O = 0 and LSE = -inf.  A cached group
+ * that is not finite reaches the rows that see its position and no other.
  * Sums are float32.  Roundings to fewer bits, beside that of O:
  *   float32 rows  none but at the far end: queries to 2^-30 of a row's largest element, the weights
  *     p_j s_j (p_j = exp(s_ij - LSE_i), s_j a group's step) to 2^-41 of the row's largest;
