@@ -264,13 +264,15 @@ __global__ void __launch_bounds__(kThreads) k_kv4_read(const __grid_constant__ K
     if (k / G < p.heads) store_values(dst + k / G * sh + k % G * kKv4Group, w[k], sb[k]);
 }
 
+long long blocks_per_seq(int seqlen, int heads_kv, int head_dim) {
+  const int heads = kWords / (head_dim / kKv4Group);
+  return ((long long)seqlen + kSlots - 1) / kSlots * (((long long)heads_kv + heads - 1) / heads);
+}
+
 template <class F>
 cudaError_t launch_rows(const Kv4Args& a, int head_dim, F&& kernel, cudaStream_t st) {
-  const int heads = kWords / (head_dim / kKv4Group);
-  const long long per_seq = ((long long)a.seqlen + kSlots - 1) / kSlots * ((a.heads_kv + heads - 1) / heads);
-  const long long blocks = per_seq * a.batch;
-  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  kernel<<<dim3((unsigned)blocks, 2), kThreads, 0, st>>>(a, (int)per_seq);
+  const long long per_seq = blocks_per_seq(a.seqlen, a.heads_kv, head_dim);
+  kernel<<<dim3((unsigned)(per_seq * a.batch), 2), kThreads, 0, st>>>(a, (int)per_seq);
   return cudaGetLastError();
 }
 
@@ -324,13 +326,16 @@ attn_status_t resolve(const attn_kv4_params_t* p, Op op, Kv4Args* a, bool* empty
   *empty = total == 0;
   if (*empty) return ATTN_OK;  // nothing is read or written
   const int heads = attention ? p->heads_q : p->heads_kv;
-  if (total * heads >= (1ll << 31) || (long long)p->seqlen * heads * p->batch >= (1ll << 31))
-    return kfail(ATTN_ERR_UNSUPPORTED, "%lld rows over all heads: at most 2^31 - 1 are supported",
-                 std::max(total, (long long)p->seqlen * p->batch) * heads);
+  // Quotients: a product of three counts may not fit 64 bits.
+  if (total > 0x7FFFFFFFll / heads)
+    return kfail(ATTN_ERR_UNSUPPORTED, "%lld rows of %d heads: at most 2^31 - 1 over all heads are supported", total, heads);
+  const int seqlen = (int)std::min<long long>(p->seqlen, total);  // a packed sequence has no more rows than all
+  if (!attention && p->batch > 0x7FFFFFFFll / blocks_per_seq(seqlen, heads, p->head_dim))
+    return kfail(ATTN_ERR_UNSUPPORTED, "%d packed sequences of up to %d rows: too many blocks of 16 rows", p->batch, seqlen);
   if (attention) {  // the attention counts its rows, positions and the cache's rows in 32 bits
-    if (total * heads > (1ll << 30) || (long long)p->seqlen * heads * p->batch > (1ll << 30))
-      return kfail(ATTN_ERR_UNSUPPORTED, "%lld query rows over all heads: at most 2^30 are supported",
-                   std::max(total, (long long)p->seqlen * p->batch) * heads);
+    if (total > (1ll << 30) / heads)
+      return kfail(ATTN_ERR_UNSUPPORTED, "%lld query rows of %d heads: at most 2^30 over all heads are supported", total,
+                   heads);
     if ((long long)p->max_pages * p->page_size > (1ll << 30))
       return kfail(ATTN_ERR_UNSUPPORTED, "max_pages * page_size = %lld: at most 2^30 positions of a sequence are supported",
                    (long long)p->max_pages * p->page_size);
@@ -367,7 +372,7 @@ attn_status_t resolve(const attn_kv4_params_t* p, Op op, Kv4Args* a, bool* empty
   a->heads_kv = p->heads_kv;
   a->group = attention ? p->heads_q / p->heads_kv : 1;
   a->by_group = fast_div(a->group);
-  a->seqlen = p->seqlen;
+  a->seqlen = seqlen;
   a->page = p->page_size;
   a->n_pages = p->n_pages;
   a->max_pages = p->max_pages;

@@ -47,8 +47,10 @@
  * heads_q % heads_kv == 0; x and y and the code arrays 16-byte aligned, scale
  * arrays 16-byte aligned too; strides multiples of 16 bytes, not negative; rows of an
  * output must not overlap (refused where one stride alone makes them: one below head_dim over
- * more than one entry); fewer than 2^31 rows over all heads in one call.  Offsets into the cache are 64-bit.  The attention
- * takes up to 2^30 query rows over all heads, up to 2^30 positions in a page list
+ * more than one entry); fewer than 2^31 rows over all heads in one call, packed ones counted
+ * as they are (a packed write or read: and batch * ceil(seqlen / 16) * heads_kv below 2^31).
+ * Offsets into the cache are 64-bit.  The attention takes up to 2^30 query rows over all heads,
+ * up to 2^30 positions in a page list
  * and fewer than 2^32 rows (n_pages * heads_kv * page_size) in the cache.
  *
  * Errors and asynchrony are as for gbattn.h.  What only the device knows is
