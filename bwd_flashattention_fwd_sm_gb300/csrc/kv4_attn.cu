@@ -36,10 +36,10 @@
 // result, which a second kernel joins in order, so results do not vary.
 //
 // Measured (bf16, 32 heads on 8 of 128): 64 sequences of up to 8192, one token each, 76 us, 60% of
-// the rate of a copy; a sequence of 131072 38 us, 58%; one of 777 9.2 us with both kernels. The
-// instructions bound it: ALU 46% and tensor pipe 26% busy, hardly a warp waits for memory, and
-// without the arithmetic the same copies run at the rate of memory.  4 products and 16 bit operations
-// take 51 to 60 cycles of a sub-core where the longer of the two alone takes 32.
+// the rate of a copy; a sequence of 131072 38 us, 58%; one of 777 9.5 us with both kernels.  No pipe
+// bounds it (issue slots 50% busy, ALU 46%, tensor pipe 25%, DRAM 57%), and hardly a warp waits for memory:
+// two warps a scheduler, each with one chain of products, exp2 and products again, wait for their own
+// results.  Without the arithmetic the same copies run at the rate of memory.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -62,7 +62,7 @@ constexpr int kFinest = 126;  // the weights' largest power of two: it and its r
 
 // What a row tile costs beside its keys (queries into operands, the warps' results
 // joined), in tiles: the line has that many empty places before a row tile's keys.  2, 6 and
-// 12 with 64 sequences of up to 8192: 88, 77, 80 us; 16 of up to 4100 at head dim 256: 60, 53, 58.
+// 12 with 64 sequences of up to 8192: 88, 76, 78 us; 16 of up to 4100 at head dim 256: 61, 52, 58.
 constexpr int kEmpty = 6;
 
 template <int D, int NT, bool F32>
@@ -75,9 +75,9 @@ struct Shape {
   static constexpr int PP = F32 ? 4 : 1;                // float16 parts of the weights
   static constexpr int FOLD = 8 / CH;                   // tiles between two folds: 128 keys of a warp
   static constexpr int ACC = G * 4 * NT * 4;            // accumulators of a lane
-  // Blocks of an SM: 1, 2 and 3 (fewer registers) with 64 sequences of up to 8192 102, 77, 80 us, a
-  // sequence of 131072 48, 39, 41.  Tiles in a warp's ring: 2, 3 and 4 76.1, 77.0 and 77.0 us, 38.9,
-  // 39.4 and 39.3: the next block's warps cover what one waits for.
+  // Blocks of an SM: 1, 2 and 3 (fewer registers) with 64 sequences of up to 8192 103, 76, 82 us, a
+  // sequence of 131072 48, 38, 42.  Tiles in a warp's ring: 2, 3 and 4 75.8, 76.2 and 75.4 us, 37.8,
+  // 38.3 and 37.8: the next block's warps cover what one waits for.
   static constexpr int BLOCKS = 2;
   static constexpr int STAGES = 2;
   static constexpr int CHUNK_BYTES = 16 * (D + 8 * G);  // K codes, V codes, K scales, V scales of 16 keys
@@ -944,8 +944,8 @@ struct Launch {
 // Row tiles of 8, 16 or 24 queries: the least that hold all of a KV head's, else the
 // widest that the registers hold (accumulators: D / 16 * 4 a lane and 8 queries).
 // Sequences of 8192 tokens, 32 heads on 8, 4 / 16 new tokens each, us, 16 rows against 8:
-// float32 head dim 64 (8 sequences) 37 / 114 against 40 / 131, 128 71 / 219 against 66 / 217,
-// 256 151 / 486 against 130 / 459; bf16 256 81 / 232 against 78 / 261.
+// float32 head dim 64 (8 sequences) 39 / 125 against 42 / 139, 128 72 / 238 against 71 / 241,
+// 256 160 / 531 against 139 / 498; bf16 256 84 / 235 against 78 / 262.
 // More bf16 rows than 24 at head dim 64 and 128 are the tcgen05 kernel's.
 template <class T, int D, class F>
 auto with_width(const Kv4Args& a, F&& f) {

@@ -16,6 +16,9 @@ constexpr int kSms = 152;  // a fixed count, so that the workspace size needs no
 // keys long and whose blocks have kWarps warps.  A row tile has kEmpty places before
 // its keys' tiles: what it costs beside them (queries into operands, results joined),
 // in tiles.  It has one tile at least, so that rows that see nothing are written too.
+// With `causal` too all of a sequence's tiles are counted, seen or not: even shares while the new tokens
+// are few beside the context (one of 512 in 8192 is 1.03 of the mean), up to twice the mean where they
+// are all of it (a prompt of 4096 over itself 465 us, 459 without `causal`).
 template <int kRows, int kKeys, int kEmpty, int kWarps>
 struct Line {
   struct SeqWork {

@@ -24,11 +24,12 @@
 // Blocks share the work by equal stretches of one line of tiles, as for few rows
 // (kv4_attn.cu).
 //
-// Measured: 2 sequences of up to 8192, 512 new tokens, 32 heads on 8 of 128: 118 us, 470 TFLOP/s
+// Measured: 2 sequences of up to 8192, 512 new tokens, 32 heads on 8 of 128: 119 us, 467 TFLOP/s
 // of products; issue slots 48% busy, tensor pipe 24%, memory 2%.  What bounds it is the length of a
 // tile's chain (unpack, scores, softmax, weights), about 4500 cycles between two tiles: with
 // an eighth of the unpacking 40 us less, without exp2 or most of the products nothing.
-// Two quarters of the keys a warp instead of one: 132 us; warps of their own for K and V: 123.
+// Two quarters of the keys a warp instead of one: 132 us; warps of their own for K and V: 123
+// (118 then).  80 registers a thread leave 344 bytes of spills at head dim 128.
 #include <algorithm>
 #include <atomic>
 
@@ -39,8 +40,8 @@ namespace gbattn {
 
 namespace {
 
-// kSpare: what a row tile costs beside its keys, in tiles (1, 2, 3, 5: 62, 56, 57, 60 us with 16
-// sequences of 4096 and 32 tokens each).
+// kSpare: what a row tile costs beside its keys, in tiles (1, 2, 3, 5: 60, 55, 52, 53 us with 16
+// sequences of up to 4096 and 32 tokens each, 80, 81, 81, 85 us with 16 of 4096).
 constexpr int kRows = 128, kKeys = 128, kSpare = 2;
 constexpr int kParts = 4, kPart = kKeys / kParts;  // warps of a row, and the keys of each
 // four warps of each 32 rows, four that unpack, and four of which one issues the products and one

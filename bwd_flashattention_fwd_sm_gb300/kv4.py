@@ -201,7 +201,8 @@ def _write(cache, k, v, block_table, lens, seqlens, stream):
 def kv4_read(cache: Kv4Cache, block_table, lens, seqlen: int | None = None, *, seqlens: SeqLens | None = None,
              dtype=torch.bfloat16, stream=None, out=None):
     """The newest tokens' keys and values, (k, v): ``seqlen`` of each sequence, or with
-    ``seqlens`` a packed batch.  Rows of padding are 0.  out: a (k, v) pair to write to."""
+    ``seqlens`` a packed batch.  Rows of padding are 0.  out: a (k, v) pair to write to,
+    two tensors apart."""
     if (seqlen is None) == (seqlens is None):
         raise ValueError("give either seqlen (a fixed number of tokens) or seqlens (a packed batch)")
     return _on(cache, stream, _read, block_table, lens, seqlen, seqlens, dtype, out)
@@ -230,7 +231,8 @@ def attn_fwd_kv4(q, cache: Kv4Cache, block_table, lens, *, causal=True, scale=No
                  stream=None, workspace=None, out=None):
     """O, LSE of the newest tokens' queries over all that the cache holds.  Returns (o, lse).
 
-    causal: a token sees the positions up to its own; else all of its sequence's."""
+    causal: a token sees the positions up to its own; else all of its sequence's.  workspace: a contiguous
+    tensor on the cache's device, taken if it is large enough.  out: O's tensor, which may be q itself."""
     return _on(cache, stream, _attend, q, block_table, lens, causal, scale, seqlens, workspace, out)
 
 
