@@ -146,7 +146,7 @@ size_t kv4_rows_workspace(const Kv4Args& a, int head_dim);
 cudaError_t launch_kv4_rows(const Kv4Args& a, int head_dim, void* workspace, unsigned long long wait_ns, cudaStream_t st);
 
 // Which of the two: the tcgen05 kernel from 25 rows on.  Measured with 16 sequences of up to
-// 4096 positions (32 query heads on 8, head dim 128; us): 24 rows 48 against 48, 32 rows
+// 4096 positions (32 query heads on 8, head dim 128; us): 24 rows 49 against 48, 32 rows
 // 77 against 47, 128 rows 172 against 55.
 inline bool kv4_many_rows(const Kv4Args& a, int head_dim, bool bf16) {
   return bf16 && head_dim <= 128 && (long long)a.seqlen * a.group > 24;

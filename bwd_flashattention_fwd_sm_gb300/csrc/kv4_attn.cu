@@ -35,8 +35,8 @@
 // themselves.  A stretch that ends inside a row tile's keys leaves its partial
 // result, which a second kernel joins in order, so results do not vary.
 //
-// Measured (bf16, 32 heads on 8 of 128): 64 sequences of up to 8192, one token each, 76 us, 60% of
-// the rate of a copy; a sequence of 131072 38 us, 58%; one of 777 9.5 us with both kernels.  No pipe
+// Measured (bf16, 32 heads on 8 of 128): 64 sequences of up to 8192, one token each, 77 us, 60% of
+// the rate of a copy; a sequence of 131072 38 us, 58%; one of 777 9.4 us with both kernels.  No pipe
 // bounds it (issue slots 50% busy, ALU 46%, tensor pipe 25%, DRAM 57%), and hardly a warp waits for memory:
 // two warps a scheduler, each with one chain of products, exp2 and products again, wait for their own
 // results.  Without the arithmetic the same copies run at the rate of memory.
@@ -549,10 +549,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
           }
         }
       }
-      // The running maximum is raised only when a score is above it by more than 2^kSlack, the
-      // weights are looked at only then or when a step is above what their units have room for.
+      // The running maximum is raised only when a score is above it by more than 2^kSlack, the weights
+      // are looked at only then or when a step is above what their units have room for and may have
+      // the weight to need it (where a position with small steps holds a row's weight, most steps are:
+      // 64 sequences of up to 8192 76 us, so 80, and 97 if all of those were looked at).
       float high[NT][2], step[G];
-      bool over = false;
+      bool over = false, wide = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -569,9 +571,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(T) == 4>::BLOCK
 #pragma unroll
         for (int c = 1; c < CH; ++c) v = fmax3f(v, bf16_lo(vsw[c][0][g]), bf16_lo(vsw[c][1][g]));
         step[g] = v;
-        over |= v > cap[g];
+        wide |= v > cap[g];
       }
-      over = __any_sync(0xffffffffu, over);
+      if (__any_sync(0xffffffffu, over || wide)) {
+        over = __any_sync(0xffffffffu, over);
+        if (!over) {
+          // a lane's largest step with its largest weight
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 rf = *reinterpret_cast<const float2*>(&row_f[nt * 8 + 2 * t4]);
+            const float p0 = fast_exp2(fmaf(high[nt][0], rf.x, -mu[nt][0]));
+            const float p1 = fast_exp2(fmaf(high[nt][1], rf.y, -mu[nt][1]));
+#pragma unroll
+            for (int g = 0; g < G; ++g) over |= fmaxf(p0 * step[g] * up(g, nt).x, p1 * step[g] * up(g, nt).y) > 0x1p15f;
+          }
+          over = __any_sync(0xffffffffu, over);
+        }
+      }
       float fall[NT][2];  // what the weights so far are multiplied by, if over
       if (over) {
 #pragma unroll
