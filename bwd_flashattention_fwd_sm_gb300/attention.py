@@ -126,10 +126,20 @@ def make_params(q, k, *, causal=False, block_mask: BlockMask | None = None, scal
     return p
 
 
+def _dense(t) -> bool:
+    """Whether a tensor's elements fill the memory behind its address, in any order of its axes."""
+    step = 1
+    for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if s != step:
+            return t.numel() == 0
+        step *= n
+    return True
+
+
 def _workspace(nbytes: int, device, workspace=None):
     """Device scratch of at least nbytes: the caller's tensor if it is large enough, else a new one."""
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if workspace is not None and (workspace.device != device or not _dense(workspace)):
+        raise ValueError(f"workspace must be a tensor on {device} without gaps or repeats")
     if nbytes == SIZE_MAX:
         raise _lib.AttnError(_lib.ATTN_ERR_INVALID_ARG, "workspace size", _lib.load().attn_last_error().decode())
     if nbytes == 0:

@@ -17,13 +17,16 @@ def test_of_the_device_and_large_enough_is_taken():
     more = _workspace(257, CPU, ws)  # too small: a new one
     assert more is not ws and more.numel() * more.element_size() >= 257
     assert _workspace(16, CPU).device == CPU
+    for t in (torch.empty(64, 64).t(), torch.empty(4, 1, 8, 16).permute(2, 0, 3, 1), torch.empty(2, 64, 64)[1]):
+        assert _workspace(4 * t.numel(), CPU, t) is t  # any order of the axes
 
 
 @pytest.mark.parametrize("ws, device", [
     (torch.empty(1 << 12, dtype=torch.uint8), torch.device("cuda", 0)),  # host memory
     (torch.empty(1, dtype=torch.uint8).expand(1 << 12), CPU),           # one byte that counts as many
     (torch.empty(1 << 13, dtype=torch.uint8)[::2], CPU),                # with bytes of others between
-    (torch.empty(64, 64).t(), CPU),
+    (torch.empty(64, 64)[:, :63], CPU),
+    (torch.empty(64, 64).as_strided((32, 64), (32, 1)), CPU),           # rows that overlap
 ])
 def test_refused(ws, device):
     with pytest.raises(ValueError, match="workspace"):
