@@ -113,6 +113,14 @@ def _rows_overlap(shape, strides):
     return False
 
 
+def _share(a, b):
+    """Whether two tensors of one shape have rows that share an element (unequal strides: whether they begin together)."""
+    if a.numel() == 0 or a.data_ptr() == b.data_ptr():
+        return a.numel() > 0
+    apart = abs(a.data_ptr() - b.data_ptr()) // a.element_size()
+    return a.stride() == b.stride() and _rows_overlap((2, *a.shape), (apart, *a.stride()))
+
+
 def _fits(t):
     """Whether an output tensor can be written in place."""
     return t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(
@@ -220,8 +228,8 @@ def _read(cache, block_table, lens, seqlen, seqlens, dtype, out, stream):
             if tuple(t.shape) != shape or t.dtype != k.dtype or t.device != cache.device or not _fits(t):
                 raise ValueError(f"out must be two CUDA tensors of shape {shape} and one dtype, rows contiguous, "
                                  "16-byte aligned and apart")
-        if k.numel() and k.data_ptr() == v.data_ptr():
-            raise ValueError("out: k and v are the same memory")
+        if _share(k, v):
+            raise ValueError("out: k and v share memory")
     p = _params(k, v, cache, block_table, lens, seqlens, H, H)
     check(_lib.load().attn_kv4_read(p, *cache._pointers, k.data_ptr(), v.data_ptr(), stream), "attn_kv4_read")
     return k, v
@@ -231,8 +239,8 @@ def attn_fwd_kv4(q, cache: Kv4Cache, block_table, lens, *, causal=True, scale=No
                  stream=None, workspace=None, out=None):
     """O, LSE of the newest tokens' queries over all that the cache holds.  Returns (o, lse).
 
-    causal: a token sees the positions up to its own; else all of its sequence's.  workspace: a contiguous
-    tensor on the cache's device, taken if it is large enough.  out: O's tensor, which may be q itself."""
+    causal: a token sees the positions up to its own; else all of its sequence's.  workspace: a tensor
+    without gaps on the cache's device, taken if it is large enough.  out: O's tensor, which may be q itself."""
     return _on(cache, stream, _attend, q, block_table, lens, causal, scale, seqlens, workspace, out)
 
 

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from bwd_flashattention_fwd_sm_gb300 import Kv4Cache, _lib, attn_fwd_kv4, get_status, kv4_read
-from bwd_flashattention_fwd_sm_gb300.kv4 import _fits, _rows_overlap
+from bwd_flashattention_fwd_sm_gb300.kv4 import _fits, _rows_overlap, _share
 
 from test_kv4_abi import FAKE, params
 
@@ -77,6 +77,16 @@ def test_usual_views_fit():
     assert not _fits(flat.as_strided((2, 4, 6, 64), (4 * 64, 64, 64, 1)))
 
 
+def test_two_outputs_that_share_memory():
+    both = torch.zeros(2, 5, 2, 3, 64)  # [batch, tokens, keys or values, heads, head_dim]
+    k, v = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    assert not _share(k, v) and not _share(v, k) and not _share(k[:0], k[:0])
+    assert _share(k, k) and _share(k[:, :, :4], k[:, :, 1:]) and _share(k[:, :, 1:], k[:, :, :4])
+    assert not _share(k[:, :2], v[:, :2]) and not _share(torch.zeros(2, 64), torch.zeros(2, 64))
+    rows = torch.zeros(8, 64)
+    assert _share(rows[:4], rows[3:7]) and not _share(rows[:4], rows[4:]) and not _share(rows[::2], rows[1::2])
+
+
 @pytest.mark.gpu
 def test_refused_by_the_calls():
     dev = torch.device("cuda", 0)
@@ -88,10 +98,12 @@ def test_refused_by_the_calls():
     for wrong in (q[:1].expand(2, 4, 3, 64), q[:, :1].expand(2, 4, 3, 64), q[:, :, :1].expand(2, 4, 3, 64)):
         with pytest.raises(ValueError, match="apart"):
             attn_fwd_kv4(q, cache, table, lens, out=wrong)
-    for wrong in ((k, k), (k, k[:1].expand(2, 2, 3, 64)), (k[:, :1].expand(2, 2, 3, 64), k)):
+    long = torch.zeros(2, 2, 7, 64, dtype=torch.bfloat16, device=dev)
+    for wrong in ((k, k), (long[:, :, :3], long[:, :, 2:5]), (k, k[:1].expand(2, 2, 3, 64)), (k[:, :1].expand(2, 2, 3, 64), k)):
         with pytest.raises(ValueError):
             kv4_read(cache, table, lens, 3, out=wrong)
     attn_fwd_kv4(q[:1].expand(2, 4, 3, 64), cache, table, lens, out=torch.empty_like(q))  # an input may
     kv4_read(cache, table, lens, 3, out=(k, torch.empty_like(k)))
+    kv4_read(cache, table, lens, 3, out=(long[:, :, :3], long[:, :, 3:6]))
     torch.cuda.synchronize()
     assert get_status() == 0
