@@ -85,6 +85,47 @@ class LnParamsC(ctypes.Structure):
     ]
 
 
+class LnDropoutC(ctypes.Structure):
+    """ln_dropout_t of include/gbln.h."""
+    _fields_ = [
+        ("p", ctypes.c_double),
+        ("seed", ctypes.c_uint64),
+        ("offset", ctypes.c_uint64),
+        ("rng", ctypes.c_void_p),
+    ]
+
+
+class LnBwdParamsC(ctypes.Structure):
+    """ln_bwd_params_t of include/gbln.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("dy_stride", ctypes.c_int64),
+        ("dh_stride", ctypes.c_int64),
+        ("h_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64),
+        ("dr_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class EmbeddingParamsC(ctypes.Structure):
+    """attn_embedding_params_t of include/gbembed.h."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("w_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32),
+        ("ids_64", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+        ("padding_id", ctypes.c_int64),
+    ]
+
+
 class Kv4ParamsC(ctypes.Structure):
     """attn_kv4_params_t of include/gbkv4.h."""
     _fields_ = [
@@ -117,6 +158,10 @@ class Kv4ParamsC(ctypes.Structure):
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(ParamsC)
 _KP = ctypes.POINTER(Kv4ParamsC)
+_LP = ctypes.POINTER(LnParamsC)
+_BP = ctypes.POINTER(LnBwdParamsC)
+_DP = ctypes.POINTER(LnDropoutC)
+_EP = ctypes.POINTER(EmbeddingParamsC)
 SIGNATURES = {
     "attn_fwd_workspace_size": (ctypes.c_size_t, [_PP]),
     "attn_bwd_workspace_size": (ctypes.c_size_t, [_PP]),
@@ -137,7 +182,14 @@ SIGNATURES = {
     "attn_kv4_read": (ctypes.c_int, [_KP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     "attn_kv4_workspace_size": (ctypes.c_size_t, [_KP]),
     "attn_fwd_kv4": (ctypes.c_int, [_KP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
-    "ln_residual_fwd": (ctypes.c_int, [ctypes.POINTER(LnParamsC), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "ln_residual_fwd": (ctypes.c_int, [_LP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "ln_dropout_residual_fwd": (ctypes.c_int, [_LP, _DP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "ln_dropout": (ctypes.c_int, [_LP, _DP, _VP, _VP, _VP]),
+    "ln_residual_bwd_workspace_size": (ctypes.c_size_t, [_BP]),
+    "ln_residual_bwd": (ctypes.c_int, [_BP, _DP, *[_VP] * 11, ctypes.c_size_t, _VP]),
+    "attn_embedding_fwd": (ctypes.c_int, [_EP, _VP, _VP, _VP, _VP]),
+    "attn_embedding_bwd_workspace_size": (ctypes.c_size_t, [_EP]),
+    "attn_embedding_bwd": (ctypes.c_int, [_EP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
 }
 
 _lock = threading.Lock()

@@ -1,0 +1,524 @@
+// Embedding table: lookup with scaling, and the table's gradient by sorted tokens
+// (include/gbembed.h has the formulas).
+//
+// Lookup.  Bound by device memory; every thread has several vectors in flight, because a
+// row's address waits for its id.
+//
+// Gradient.  The tokens' places are sorted by id (k_embed_sort, a stable radix sort by
+// one cluster of blocks), cut in pieces of kPiece places, and each block adds the rows
+// of one piece over a stretch of columns: equal work however often a word comes.  A word
+// that lies inside one piece is written to the table at once; of one that
+// several pieces share each piece leaves a partial sum, and k_embed_join adds those in order.
+// No atomics: the order of the sums follows from the ids alone.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+
+#include "../../include/gbembed.h"
+#include "common.cuh"
+
+namespace gbattn {
+void set_last_error_text(const char* text);
+attn_status_t device_status(int** status, int* sms, unsigned long long* wait_ns);
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256;     // lookup, fill
+constexpr int kAtOnce = 4;        // vectors of a thread in flight
+constexpr int kPiece = 32;        // sorted places of one block of the gradient's sums
+constexpr int kSumThreads = 128;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBits = 9;       // of one pass's digit
+constexpr int kMaxCluster = 8;
+constexpr int64_t kMaxDim = 1 << 20;
+
+// N neighbouring elements of T as one load or store, widened to float32.
+template <class T, int N>
+struct Elems {
+  static_assert(sizeof(T) * N == 16 || sizeof(T) * N == 8 || sizeof(T) * N == 4 || sizeof(T) * N == 2, "one access");
+  union U {
+    T t[N];
+    uint4 w16;
+    uint2 w8;
+    uint32_t w4;
+    __device__ U() {}
+  };
+  __device__ static void load(const T* p, float (&v)[N]) {
+    U u;
+    if constexpr (sizeof(T) * N == 16) u.w16 = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (sizeof(T) * N == 8) u.w8 = *reinterpret_cast<const uint2*>(p);
+    else if constexpr (sizeof(T) * N == 4) u.w4 = *reinterpret_cast<const uint32_t*>(p);
+    else u.t[0] = *p;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f32(u.t[i]);
+  }
+  __device__ static void store(T* p, const float (&v)[N]) {
+    U u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) u.t[i] = from_f32<T>(v[i]);
+    if constexpr (sizeof(T) * N == 16) *reinterpret_cast<uint4*>(p) = u.w16;
+    else if constexpr (sizeof(T) * N == 8) *reinterpret_cast<uint2*>(p) = u.w8;
+    else if constexpr (sizeof(T) * N == 4) *reinterpret_cast<uint32_t*>(p) = u.w4;
+    else *p = u.t[0];
+  }
+};
+
+struct EmbedArgs {
+  const void* ids;
+  const void* x;        // weight, or dy
+  void* y;              // y, or dweight
+  int64_t tokens, vocab, dim;
+  int64_t x_stride, y_stride;
+  int64_t padding;
+  int64_t row_step, unit_step;  // lookup: all threads' vectors on, as rows and vectors of a row
+  float scale;
+  int ids_64, accumulate;
+  uint32_t* keys[2];    // gradient: ids and places, before and after a pass
+  uint32_t* place[2];
+  float* part;          // [pieces][2][dim]: sums of words that began before the piece, that go on after it
+  int passes, bits;
+  int* status;
+};
+
+__device__ __forceinline__ int64_t id_at(const EmbedArgs& a, int64_t i) {
+  return a.ids_64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+}
+
+template <class T, int N>
+__global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a) {
+  const int64_t units = a.dim / N;  // N divides dim
+  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  int64_t row = first / units, unit = first % units;
+  const T* W = static_cast<const T*>(a.x);
+  T* Y = static_cast<T*>(a.y);
+  while (row < a.tokens) {
+    int64_t rows[kAtOnce], at[kAtOnce];
+    float v[kAtOnce][N];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      rows[i] = row, at[i] = unit * N;
+      if (row < a.tokens) {
+        const int64_t id = id_at(a, row);
+        if (id >= 0 && id < a.vocab) {
+          Elems<T, N>::load(W + id * a.x_stride + at[i], v[i]);
+        } else {
+          set_status(a.status, kStatusBounds);
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[i][e] = 0.f;
+        }
+      }
+      row += a.row_step, unit += a.unit_step;
+      if (unit >= units) unit -= units, ++row;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (rows[i] >= a.tokens) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[i][e] *= a.scale;
+      Elems<T, N>::store(Y + rows[i] * a.y_stride + at[i], v[i]);
+    }
+  }
+}
+
+// Zeros over the whole table.
+template <class T, int N>
+__global__ void __launch_bounds__(kThreads) k_embed_fill(const EmbedArgs a) {
+  const int64_t units = a.dim / N;
+  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  int64_t row = first / units, unit = first % units;
+  const float zero[N] = {};
+  while (row < a.vocab) {
+    Elems<T, N>::store(static_cast<T*>(a.y) + row * a.y_stride + unit * N, zero);
+    row += a.row_step, unit += a.unit_step;
+    if (unit >= units) unit -= units, ++row;
+  }
+}
+
+// The sort key of place i: its id; `vocab`, behind all others, if its row of dy goes nowhere.
+__device__ __forceinline__ uint32_t key_at(const EmbedArgs& a, int64_t i) {
+  const int64_t id = id_at(a, i);
+  if (id < 0 || id >= a.vocab) {
+    set_status(a.status, kStatusBounds);
+    return (uint32_t)a.vocab;
+  }
+  return id == a.padding ? (uint32_t)a.vocab : (uint32_t)id;
+}
+
+// Stable sort of (id, place) by id: `passes` passes over digits of `bits` bits, least
+// significant first.  Every warp of the cluster owns a stretch of the input.  It counts its
+// digits; the counts of all warps in front of it and of all lower digits say where its
+// first of each digit goes; then it walks its stretch again, 32 at a time, and those
+// with equal digits find their order by a vote.  Ends in buffer passes % 2.
+__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) {
+  extern __shared__ uint32_t count[];  // [kSortWarps][digits]
+  __shared__ uint32_t total[1 << kMaxBits];
+  __shared__ uint32_t warp_total[kSortWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned rank = cluster.block_rank(), blocks = cluster.num_blocks();
+  const int digits = 1 << a.bits;
+  const int64_t warps = (int64_t)blocks * kSortWarps;
+  const int64_t each = ((a.tokens + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t begin = ((int64_t)rank * kSortWarps + warp) * each;
+  const int64_t end = begin + each < a.tokens ? begin + each : a.tokens;
+  uint32_t* mine = count + warp * digits;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+    const uint32_t* keys = a.keys[pass & 1];
+    const uint32_t* place = a.place[pass & 1];
+    for (int d = lane; d < digits; d += 32) mine[d] = 0;
+    __syncwarp();
+    for (int64_t i = begin + lane; i - lane < end; i += 32) {
+      const unsigned active = __ballot_sync(0xffffffffu, i < end);
+      if (i < end) {
+        const uint32_t key = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
+        const uint32_t d = (key >> shift) & (digits - 1);
+        const unsigned same = __match_any_sync(active, d);
+        if (lane == __ffs(same) - 1) mine[d] += __popc(same);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < digits) {  // exclusive over the block's warps
+      uint32_t sum = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = count[w * digits + threadIdx.x];
+        count[w * digits + threadIdx.x] = sum;
+        sum += n;
+      }
+      total[threadIdx.x] = sum;
+    }
+    cluster.sync();
+    uint32_t all = 0, before = 0;
+    if ((int)threadIdx.x < digits)
+      for (unsigned r = 0; r < blocks; ++r) {
+        const uint32_t n = cluster.map_shared_rank(total, r)[threadIdx.x];
+        all += n;
+        if (r < rank) before += n;
+      }
+    uint32_t upto = all;  // inclusive over the digits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t n = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += n;
+    }
+    if (lane == 31) warp_total[warp] = upto;
+    __syncthreads();
+    if ((int)threadIdx.x < digits) {
+      uint32_t start = before + upto - all;
+      for (int w = 0; w < warp; ++w) start += warp_total[w];
+      for (int w = 0; w < kSortWarps; ++w) count[w * digits + threadIdx.x] += start;
+    }
+    __syncthreads();
+    uint32_t* keys_to = a.keys[(pass + 1) & 1];
+    uint32_t* place_to = a.place[(pass + 1) & 1];
+    for (int64_t i = begin + lane; i - lane < end; i += 32) {
+      const unsigned active = __ballot_sync(0xffffffffu, i < end);
+      if (i < end) {
+        const uint32_t key = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
+        const uint32_t from = pass == 0 ? (uint32_t)i : __ldcg(place + i);
+        const uint32_t d = (key >> shift) & (digits - 1);
+        const unsigned same = __match_any_sync(active, d);
+        const uint32_t to = mine[d] + __popc(same & ((1u << lane) - 1));
+        if (bounds_ok(to < (uint64_t)a.tokens, a.status)) {
+          keys_to[to] = key;
+          place_to[to] = from;
+        }
+        __syncwarp(active);
+        if (lane == __ffs(same) - 1) mine[d] += __popc(same);
+      }
+      __syncwarp();
+    }
+    cluster.sync();  // the next pass reads what all blocks wrote; `total` may be written again
+  }
+}
+
+// The sums of one piece of sorted places over kSumThreads * N columns.
+template <class T, class W, int N>
+__global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
+  __shared__ uint32_t key[kPiece + 2];  // with the neighbours on both sides
+  __shared__ uint32_t place[kPiece];
+  const int64_t begin = (int64_t)blockIdx.x * kPiece;
+  const int n = (int)(a.tokens - begin < kPiece ? a.tokens - begin : kPiece);
+  const uint32_t* keys = a.keys[a.passes & 1];
+  const uint32_t none = (uint32_t)a.vocab;
+  for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
+    const int64_t at = begin + i - 1;
+    key[i] = at >= 0 && at < a.tokens ? keys[at] : none;
+    if (i >= 1 && i <= n) place[i - 1] = a.place[a.passes & 1][at];
+  }
+  __syncthreads();
+  const int64_t c0 = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * N;
+  if (c0 >= a.dim) return;
+  const T* DY = static_cast<const T*>(a.x) + c0;
+  float sum[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) sum[e] = 0.f;
+  int start = 1;
+  for (int i = 1; i <= n; ++i) {
+    const uint32_t k = key[i];
+    if (k >= none) break;  // sorted behind all words
+    float v[N];
+    if (bounds_ok(place[i - 1] < (uint64_t)a.tokens, a.status)) {
+      Elems<T, N>::load(DY + (int64_t)place[i - 1] * a.x_stride, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] += v[e];
+    }
+    if (i < n && key[i + 1] == k) continue;
+    const bool from_before = start == 1 && key[0] == k, goes_on = i == n && key[n + 1] == k;
+    if (from_before || goes_on) {
+      float* part = a.part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * a.dim + c0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) part[e] = sum[e];
+    } else {
+      W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c0;
+      float old[N];
+      if (a.accumulate) Elems<W, N>::load(to, old);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] = a.accumulate ? old[e] + a.scale * sum[e] : a.scale * sum[e];
+      Elems<W, N>::store(to, sum);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = 0.f;
+    start = i + 1;
+  }
+}
+
+// Words that several pieces share, from the piece in which they begin.
+template <class W>
+__global__ void __launch_bounds__(kSumThreads) k_embed_join(const EmbedArgs a) {
+  const uint32_t* keys = a.keys[a.passes & 1];
+  const int64_t begin = (int64_t)blockIdx.x * kPiece;
+  int64_t next = begin + kPiece;
+  if (next >= a.tokens) return;
+  const uint32_t k = keys[next];
+  if (k >= (uint32_t)a.vocab || keys[next - 1] != k || (begin > 0 && keys[begin - 1] == k)) return;
+  const int64_t c = (int64_t)blockIdx.y * kSumThreads + threadIdx.x;
+  if (c >= a.dim) return;
+  float sum = a.part[(2 * (int64_t)blockIdx.x + 1) * a.dim + c];
+  for (int64_t piece = blockIdx.x + 1; next < a.tokens && keys[next] == k; ++piece, next += kPiece)
+    sum += a.part[2 * piece * a.dim + c];
+  W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c;
+  *to = from_f32<W>(a.accumulate ? to_f32(*to) + a.scale * sum : a.scale * sum);
+}
+
+attn_status_t efail(attn_status_t s, const char* msg) {
+  char buf[200];
+  snprintf(buf, sizeof(buf), "embedding: %s", msg);
+  set_last_error_text(buf);
+  return s;
+}
+
+attn_status_t check_params(const attn_embedding_params_t* p, bool backward) {
+  if (!p) return efail(ATTN_ERR_INVALID_ARG, "params is NULL");
+  if ((p->dtype != ATTN_BF16 && p->dtype != ATTN_F32) ||
+      (backward && p->w_dtype != ATTN_BF16 && p->w_dtype != ATTN_F32))
+    return efail(ATTN_ERR_INVALID_ARG, "a dtype is not ATTN_F32 or ATTN_BF16");
+  if (p->tokens < 0 || p->vocab < 0 || p->dim < 0) return efail(ATTN_ERR_INVALID_ARG, "a size is negative");
+  const int64_t most = INT32_MAX;
+  if (p->tokens >= most || p->vocab >= most || p->dim > kMaxDim)
+    return efail(ATTN_ERR_UNSUPPORTED, "tokens or vocab of 2^31 - 1 or more, or dim above 2^20");
+  if (p->x_stride < p->dim || p->w_stride < p->dim) return efail(ATTN_ERR_INVALID_ARG, "a row stride is below dim");
+  if (!(p->scale - p->scale == 0.f)) return efail(ATTN_ERR_INVALID_ARG, "scale is not finite");
+  return ATTN_OK;
+}
+
+struct Layout {
+  size_t keys[2], place[2], part, total;
+};
+
+Layout layout_of(const attn_embedding_params_t* p) {
+  Layout l{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t n = (size_t)p->tokens;
+  for (int i = 0; i < 2; ++i) l.keys[i] = take(4 * n), l.place[i] = take(4 * n);
+  l.part = take((n + kPiece - 1) / kPiece * 2 * (size_t)p->dim * 4);
+  l.total = at;
+  return l;
+}
+
+int64_t blocks_for(int64_t rows, int64_t units, int64_t most, EmbedArgs* a) {
+  const int64_t blocks = std::min((rows * units + kThreads - 1) / kThreads, most);  // below 2^51
+  a->row_step = blocks * kThreads / units, a->unit_step = blocks * kThreads % units;
+  return blocks;
+}
+
+template <class T, int N>
+void launch_lookup(EmbedArgs a, int sms, cudaStream_t st) {
+  const int64_t blocks = blocks_for(a.tokens, a.dim / N, (int64_t)sms * 8, &a);
+  k_embed<T, N><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+}
+
+template <class W, int N>
+void launch_fill(EmbedArgs a, int sms, cudaStream_t st) {
+  const int64_t blocks = blocks_for(a.vocab, a.dim / N, (int64_t)sms * 8, &a);
+  k_embed_fill<W, N><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+}
+
+template <class T, class W, int N>
+void launch_sums(const EmbedArgs& a, cudaStream_t st) {
+  const unsigned pieces = (unsigned)((a.tokens + kPiece - 1) / kPiece);
+  k_embed_sum<T, W, N><<<dim3(pieces, (unsigned)((a.dim + kSumThreads * N - 1) / (kSumThreads * N))), kSumThreads, 0,
+                         st>>>(a);
+  if (pieces > 1)
+    k_embed_join<W><<<dim3(pieces - 1, (unsigned)((a.dim + kSumThreads - 1) / kSumThreads)), kSumThreads, 0, st>>>(a);
+}
+
+cudaError_t launch_sort(const EmbedArgs& a, cudaStream_t st) {
+  int blocks = 1;
+  while (blocks < kMaxCluster && (int64_t)blocks * kSortThreads < a.tokens) blocks *= 2;
+  const size_t smem = (size_t)kSortWarps * (sizeof(uint32_t) << a.bits);
+  cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(kSortWarps * (sizeof(uint32_t) << kMaxBits)));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = blocks, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_embed_sort, a);
+}
+
+// Elements of one access: whole 16-byte vectors of the 2-byte type (8) or of the 4-byte type
+// (4) where every address allows it, else pairs or single elements.
+int width(uintptr_t at, int64_t dim, size_t small) {
+  for (int n = small == 2 ? 8 : 4; n > 1; n /= 2)
+    if ((at & (n * small - 1)) == 0 && dim % n == 0) return n;
+  return 1;
+}
+
+}  // namespace
+}  // namespace gbattn
+
+using namespace gbattn;
+
+extern "C" {
+
+attn_status_t attn_embedding_fwd(const attn_embedding_params_t* p, const void* weight, const void* ids, void* y,
+                                 void* stream) {
+  attn_status_t s = check_params(p, false);
+  if (s != ATTN_OK) return s;
+  if (p->tokens == 0 || p->dim == 0) return ATTN_OK;
+  const uintptr_t esize = p->dtype == ATTN_BF16 ? 2 : 4;
+  if ((!weight && p->vocab > 0) || !ids || !y) return efail(ATTN_ERR_INVALID_ARG, "weight, ids or y is NULL");
+  const uintptr_t at = reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(y) |
+                       (uintptr_t)p->x_stride * esize | (uintptr_t)p->w_stride * esize;
+  if ((at & (esize - 1)) || (reinterpret_cast<uintptr_t>(ids) & (p->ids_64 ? 7u : 3u)))
+    return efail(ATTN_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  EmbedArgs a{};
+  int sms = 0;
+  unsigned long long wait_ns = 0;
+  if ((s = device_status(&a.status, &sms, &wait_ns))) return s;
+  a.ids = ids, a.x = weight, a.y = y;
+  a.tokens = p->tokens, a.vocab = p->vocab, a.dim = p->dim;
+  a.x_stride = p->w_stride, a.y_stride = p->x_stride;
+  a.scale = p->scale, a.ids_64 = p->ids_64;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int n = width(at, p->dim, esize);
+  if (p->dtype == ATTN_BF16) {
+    if (n == 8) launch_lookup<__nv_bfloat16, 8>(a, sms, st);
+    else if (n >= 2) launch_lookup<__nv_bfloat16, 2>(a, sms, st);
+    else launch_lookup<__nv_bfloat16, 1>(a, sms, st);
+  } else {
+    if (n == 4) launch_lookup<float, 4>(a, sms, st);
+    else launch_lookup<float, 1>(a, sms, st);
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : efail(ATTN_ERR_CUDA, "launch failed");
+}
+
+size_t attn_embedding_bwd_workspace_size(const attn_embedding_params_t* p) {
+  if (check_params(p, true) != ATTN_OK) return SIZE_MAX;
+  if (p->tokens == 0 || p->vocab == 0 || p->dim == 0) return 0;
+  return layout_of(p).total;
+}
+
+attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* dy, const void* ids, void* dweight,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  attn_status_t s = check_params(p, true);
+  if (s != ATTN_OK) return s;
+  if (p->vocab == 0 || p->dim == 0 || (p->tokens == 0 && p->accumulate)) return ATTN_OK;
+  const uintptr_t esize = p->dtype == ATTN_BF16 ? 2 : 4, wsize = p->w_dtype == ATTN_BF16 ? 2 : 4;
+  if (!dweight || (p->tokens > 0 && (!dy || !ids))) return efail(ATTN_ERR_INVALID_ARG, "dy, ids or dweight is NULL");
+  const uintptr_t at_x = reinterpret_cast<uintptr_t>(dy) | (uintptr_t)p->x_stride * esize;
+  const uintptr_t at_w = reinterpret_cast<uintptr_t>(dweight) | (uintptr_t)p->w_stride * wsize;
+  if ((at_x & (esize - 1)) || (at_w & (wsize - 1)) || (reinterpret_cast<uintptr_t>(ids) & (p->ids_64 ? 7u : 3u)))
+    return efail(ATTN_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  const size_t need = attn_embedding_bwd_workspace_size(p);
+  if (need && !workspace) return efail(ATTN_ERR_WORKSPACE, "workspace is NULL");
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return efail(ATTN_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  if (workspace_bytes < need) return efail(ATTN_ERR_WORKSPACE, "workspace is too small");
+  EmbedArgs a{};
+  int sms = 0;
+  unsigned long long wait_ns = 0;
+  if ((s = device_status(&a.status, &sms, &wait_ns))) return s;
+  a.ids = ids, a.x = dy, a.y = dweight;
+  a.tokens = p->tokens, a.vocab = p->vocab, a.dim = p->dim;
+  a.x_stride = p->x_stride, a.y_stride = p->w_stride;
+  a.scale = p->scale, a.ids_64 = p->ids_64, a.accumulate = p->accumulate != 0;
+  a.padding = p->padding_id < 0 ? -1 : p->padding_id;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!p->accumulate) {
+    const int n = width(at_w, p->dim, wsize);
+    if (wsize == 2) {
+      if (n == 8) launch_fill<__nv_bfloat16, 8>(a, sms, st);
+      else if (n >= 2) launch_fill<__nv_bfloat16, 2>(a, sms, st);
+      else launch_fill<__nv_bfloat16, 1>(a, sms, st);
+    } else {
+      if (n == 4) launch_fill<float, 4>(a, sms, st);
+      else launch_fill<float, 1>(a, sms, st);
+    }
+  }
+  if (p->tokens > 0) {
+    const Layout l = layout_of(p);
+    char* ws = static_cast<char*>(workspace);
+    for (int i = 0; i < 2; ++i) {
+      a.keys[i] = reinterpret_cast<uint32_t*>(ws + l.keys[i]);
+      a.place[i] = reinterpret_cast<uint32_t*>(ws + l.place[i]);
+    }
+    a.part = reinterpret_cast<float*>(ws + l.part);
+    int bits = 1;  // of the largest key, vocab
+    while (p->vocab >> bits) ++bits;
+    a.passes = (bits + kMaxBits - 1) / kMaxBits;
+    a.bits = (bits + a.passes - 1) / a.passes;
+    e = launch_sort(a, st);
+    if (e != cudaSuccess) return efail(ATTN_ERR_CUDA, "sort launch failed");
+    // one width for dy's elements and the table's: both addresses have to allow it
+    const int n = std::min(width(at_x, p->dim, esize), width(at_w, p->dim, wsize));
+    if (esize == 2 && wsize == 2) {
+      if (n == 8) launch_sums<__nv_bfloat16, __nv_bfloat16, 8>(a, st);
+      else if (n >= 2) launch_sums<__nv_bfloat16, __nv_bfloat16, 2>(a, st);
+      else launch_sums<__nv_bfloat16, __nv_bfloat16, 1>(a, st);
+    } else if (esize == 2) {
+      if (n == 4) launch_sums<__nv_bfloat16, float, 4>(a, st);
+      else launch_sums<__nv_bfloat16, float, 1>(a, st);
+    } else if (wsize == 2) {
+      if (n == 4) launch_sums<float, __nv_bfloat16, 4>(a, st);
+      else launch_sums<float, __nv_bfloat16, 1>(a, st);
+    } else {
+      if (n == 4) launch_sums<float, float, 4>(a, st);
+      else launch_sums<float, float, 1>(a, st);
+    }
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : efail(ATTN_ERR_CUDA, "launch failed");
+}
+
+}  // extern "C"

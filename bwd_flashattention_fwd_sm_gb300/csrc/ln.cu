@@ -27,7 +27,9 @@
 
 #include "../../include/gbln.h"
 #include "common.cuh"
+#include "dropout.cuh"
 #include "ptx.cuh"
+#include "rowvec.cuh"
 
 #include <algorithm>
 
@@ -122,46 +124,6 @@ __device__ __forceinline__ void block_stats(Stats st, bool eq, int lane, int war
   __syncthreads();
 }
 
-template <class T>
-struct Vec;  // one 16-byte vector of T
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int E = 8;
-  __device__ static void load(const __nv_bfloat16* p, float (&v)[8]) { unpack(*reinterpret_cast<const uint4*>(p), v); }
-  __device__ static void unpack(const uint4& u, float (&v)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  __device__ static void store(__nv_bfloat16* p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  __device__ static float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  __device__ static void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-};
-template <>
-struct Vec<float> {
-  static constexpr int E = 4;
-  __device__ static void load(const float* p, float (&v)[4]) { unpack(*reinterpret_cast<const uint4*>(p), v); }
-  __device__ static void unpack(const uint4& u, float (&v)[4]) {
-    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
-  }
-  __device__ static void store(float* p, const float (&v)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  }
-  __device__ static float load1(const float* p) { return *p; }
-  __device__ static void store1(float* p, float v) { *p = v; }
-};
-
 struct LnArgs {
   ln_params_t p;
   const void* x;
@@ -173,6 +135,7 @@ struct LnArgs {
   float* mean;
   float* rstd;
   int vec;  // every pointer (gamma, beta included) 16-byte aligned and every stride a whole number of vectors
+  DropArgs drop;  // of x, where the kernel's kDrop says so
 };
 
 // gamma and beta of columns c0 .. c0 + E - 1 (1 and 0 when absent), as float4
@@ -200,7 +163,7 @@ __device__ __forceinline__ void affine(const LnArgs& a, int64_t c0, int64_t cols
 
 // kVpt: 16-byte vectors per thread (cols <= 256 * kVpt * E).  Short rows leave
 // registers to spare: several CTAs per SM then keep more loads in flight.
-template <class T, int kVpt>
+template <class T, int kVpt, bool kDrop>
 __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4)) k_ln_residual(const LnArgs a) {
   constexpr int E = Vec<T>::E;
   __shared__ Stats warp_stats[kThreadsLn / 32];
@@ -216,6 +179,8 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
   const T* R = static_cast<const T*>(a.r);
   T* Y = static_cast<T*>(a.y);
   T* H = static_cast<T*>(a.h);
+  DropKey key{};
+  if constexpr (kDrop) key = drop_key(a.drop);
   for (int64_t row = blockIdx.x; row < a.p.rows; row += gridDim.x) {
     const T* xr = X + row * a.p.x_stride;
     const T* rr = R ? R + row * a.p.r_stride : nullptr;
@@ -244,6 +209,7 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
       if (vi < nvec) {
         if (!ragged || (a.vec && c0 + E <= cols)) {
           Vec<T>::unpack(ux[j], v[j]);
+          if constexpr (kDrop) drop_vector<E>(a.drop, key, c0, row, v[j]);
           if (rr) {
             float t[E];
             Vec<T>::unpack(ur[j], t);
@@ -260,9 +226,15 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
           for (int e = 0; e < E; ++e) {
             v[j][e] = 0.f;
             if (c0 + e < cols) {
-              v[j][e] = Vec<T>::load1(xr + c0 + e) + (rr ? Vec<T>::load1(rr + c0 + e) : 0.f);
+              v[j][e] = Vec<T>::load1(xr + c0 + e);
               ++cnt;
             }
+          }
+          if constexpr (kDrop) drop_vector<E>(a.drop, key, c0, row, v[j]);
+          if (rr) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (c0 + e < cols) v[j][e] += Vec<T>::load1(rr + c0 + e);
           }
         }
       }
@@ -320,14 +292,14 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
 }
 
 // Persistent grid: as many CTAs as fit on the SMs at once (at most one per row).
-template <class T, int kVpt>
+template <class T, int kVpt, bool kDrop>
 cudaError_t launch_ln_v(const LnArgs& a, int sms, cudaStream_t st) {
   int per_sm = 1;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_ln_residual<T, kVpt>, kThreadsLn, 0);
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_ln_residual<T, kVpt, kDrop>, kThreadsLn, 0);
   if (e != cudaSuccess) return e;
   const int64_t want = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
   const int grid = (int)(a.p.rows < want ? a.p.rows : want);
-  k_ln_residual<T, kVpt><<<grid, kThreadsLn, 0, st>>>(a);
+  k_ln_residual<T, kVpt, kDrop><<<grid, kThreadsLn, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -345,7 +317,7 @@ constexpr int kMaxStages = 8;
 template <int kVpt>
 constexpr int ring_ctas() { return kVpt <= 2 ? 4 : (kVpt == 4 ? 2 : 1); }
 
-template <class T, int kVpt>
+template <class T, int kVpt, bool kDrop>
 __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const LnArgs a, int stages, uint32_t row_bytes,
                                                            int* status, unsigned long long wait_ns) {
   constexpr int E = Vec<T>::E;
@@ -382,6 +354,8 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
     }
   T* Y = static_cast<T*>(a.y);
   T* H = static_cast<T*>(a.h);
+  DropKey key{};
+  if constexpr (kDrop) key = drop_key(a.drop);
   int64_t it = 0;
   bool ok = true;
   for (int64_t row = blockIdx.x; row < a.p.rows; row += gridDim.x, ++it) {
@@ -400,6 +374,7 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
       sv[j] = Stats{0.f, 0.f, 0.f};
       if (vi < nvec) {
         Vec<T>::load(reinterpret_cast<const T*>(xsm) + vi * E, v[j]);
+        if constexpr (kDrop) drop_vector<E>(a.drop, key, vi * E, row, v[j]);
         if (has_r) {
           float t[E];
           Vec<T>::load(reinterpret_cast<const T*>(xsm + row_bytes) + vi * E, t);
@@ -458,7 +433,7 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
   }
 }
 
-template <class T>
+template <class T, bool kDrop>
 cudaError_t launch_ln(const LnArgs& a, int sms, int* status, unsigned long long wait_ns, cudaStream_t st) {
   constexpr int E = Vec<T>::E;
   const int64_t per = (a.p.cols + (int64_t)kThreadsLn * E - 1) / ((int64_t)kThreadsLn * E);
@@ -485,16 +460,16 @@ cudaError_t launch_ln(const LnArgs& a, int sms, int* status, unsigned long long 
       kernel<<<grid, kThreadsLn, smem, st>>>(a, stages, row_bytes, status, wait_ns);
       return cudaGetLastError();
     };
-    if (per <= 1) return launch(k_ln_ring<T, 1>);
-    if (per <= 2) return launch(k_ln_ring<T, 2>);
-    if (per <= 4) return launch(k_ln_ring<T, 4>);
-    return launch(k_ln_ring<T, 8>);
+    if (per <= 1) return launch(k_ln_ring<T, 1, kDrop>);
+    if (per <= 2) return launch(k_ln_ring<T, 2, kDrop>);
+    if (per <= 4) return launch(k_ln_ring<T, 4, kDrop>);
+    return launch(k_ln_ring<T, 8, kDrop>);
   }
-  if (per <= 1) return launch_ln_v<T, 1>(a, sms, st);
-  if (per <= 2) return launch_ln_v<T, 2>(a, sms, st);
-  if (per <= 4) return launch_ln_v<T, 4>(a, sms, st);
-  if (per <= 8) return launch_ln_v<T, 8>(a, sms, st);
-  if (per <= 16) return launch_ln_v<T, 16>(a, sms, st);
+  if (per <= 1) return launch_ln_v<T, 1, kDrop>(a, sms, st);
+  if (per <= 2) return launch_ln_v<T, 2, kDrop>(a, sms, st);
+  if (per <= 4) return launch_ln_v<T, 4, kDrop>(a, sms, st);
+  if (per <= 8) return launch_ln_v<T, 8, kDrop>(a, sms, st);
+  if (per <= 16) return launch_ln_v<T, 16, kDrop>(a, sms, st);
   return cudaErrorInvalidValue;
 }
 
@@ -510,6 +485,12 @@ attn_status_t ln_fail(attn_status_t s, const char* msg) {
 extern "C" attn_status_t ln_residual_fwd(const ln_params_t* p, const void* x, const void* residual,
                                          const float* gamma, const float* beta, void* y, void* h, float* mean,
                                          float* rstd, void* stream) {
+  return ln_dropout_residual_fwd(p, nullptr, x, residual, gamma, beta, y, h, mean, rstd, stream);
+}
+
+extern "C" attn_status_t ln_dropout_residual_fwd(const ln_params_t* p, const ln_dropout_t* d, const void* x,
+                                                 const void* residual, const float* gamma, const float* beta, void* y,
+                                                 void* h, float* mean, float* rstd, void* stream) {
   using namespace gbattn;
   if (!p) return ln_fail(ATTN_ERR_INVALID_ARG, "ln_residual_fwd: params is NULL");
   if (p->dtype != ATTN_BF16 && p->dtype != ATTN_F32)
@@ -522,6 +503,11 @@ extern "C" attn_status_t ln_residual_fwd(const ln_params_t* p, const void* x, co
   if (bad_stride(p->x_stride, true) || bad_stride(p->y_stride, true) || bad_stride(p->r_stride, residual != nullptr) ||
       bad_stride(p->h_stride, h != nullptr))
     return ln_fail(ATTN_ERR_INVALID_ARG, "ln_residual_fwd: a row stride is below cols");
+  LnArgs a{*p, x, residual, gamma, beta, y, h, mean, rstd, 0, {}};
+  bool drops = false;
+  if (const char* wrong = resolve_dropout(d, &a.drop, &drops)) return ln_fail(ATTN_ERR_INVALID_ARG, wrong);
+  if (drops && p->rows >= (int64_t)1 << 32)
+    return ln_fail(ATTN_ERR_UNSUPPORTED, "ln_residual_fwd: dropout of 2^32 rows or more");
   if (p->rows == 0) return ATTN_OK;
   if (!x || !y) return ln_fail(ATTN_ERR_INVALID_ARG, "ln_residual_fwd: x or y is NULL");
   auto off = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & m) != 0; };
@@ -539,10 +525,15 @@ extern "C" attn_status_t ln_residual_fwd(const ln_params_t* p, const void* x, co
   unsigned long long wait_ns = 0;
   attn_status_t ds = device_status(&status, &sms, &wait_ns);
   if (ds != ATTN_OK) return ds;
-  LnArgs a{*p, x, residual, gamma, beta, y, h, mean, rstd, vec ? 1 : 0};
+  a.vec = vec ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = p->dtype == ATTN_BF16 ? launch_ln<__nv_bfloat16>(a, sms, status, wait_ns, st)
-                                        : launch_ln<float>(a, sms, status, wait_ns, st);
+  cudaError_t e;
+  if (p->dtype == ATTN_BF16)
+    e = drops ? launch_ln<__nv_bfloat16, true>(a, sms, status, wait_ns, st)
+              : launch_ln<__nv_bfloat16, false>(a, sms, status, wait_ns, st);
+  else
+    e = drops ? launch_ln<float, true>(a, sms, status, wait_ns, st)
+              : launch_ln<float, false>(a, sms, status, wait_ns, st);
   if (e != cudaSuccess) return ln_fail(ATTN_ERR_CUDA, "ln_residual_fwd: launch failed");
   return ATTN_OK;
 }

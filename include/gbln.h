@@ -1,5 +1,6 @@
 /*
- * gbln.h - fused residual add + LayerNorm for GB300 (sm_103a): C ABI.
+ * gbln.h - fused residual add + LayerNorm for GB300 (sm_103a), its backward pass,
+ * and dropout, alone and in front of the add: C ABI.
  *
  * The operation (lpqz.cn CUDA tutorial, sections 5.1-5.2): for each row of a
  * [rows, cols] matrix, h = x + residual, then
@@ -52,6 +53,74 @@ typedef struct {
  */
 attn_status_t ln_residual_fwd(const ln_params_t* p, const void* x, const void* residual, const float* gamma,
                               const float* beta, void* y, void* h, float* mean, float* rstd, void* stream);
+
+/*
+ * Dropout.  The mask is never stored: it follows from a seed, an offset and an
+ * element's place, so that the backward pass makes the same one.  Element (row,
+ * col) has 16 bits: with the counter (col / 8, row, offset low 32, offset high 32) and
+ * the key (seed low 32, seed high 32), Philox4x32 with 7 rounds (Salmon, Moraes,
+ * Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) gives four words;
+ * bits 16 (col % 8) .. 16 (col % 8) + 15 of them, words and bits lowest first.  With
+ * t = floor(65536 p + 1/2), an element whose 16 bits are below t is dropped: it becomes 0,
+ * whatever it held (NaN and infinities too).  Another is multiplied by 65536 / (65536 - t),
+ * so that the mean is that of the rate really used, t / 65536.
+ *
+ * seed and offset are modulo 2^64 the sums of the two members and, if rng is not
+ * NULL, of the pair {seed, offset} in device memory that the kernel reads when it
+ * runs: a captured graph drops anew when that pair is changed between replays.  The
+ * backward pass needs the values of the forward pass.
+ */
+typedef struct {
+  double p;            /* probability of being dropped, 0 <= p <= 1 */
+  uint64_t seed, offset;
+  const uint64_t* rng; /* device, 2 numbers, 8-byte aligned, or NULL */
+} ln_dropout_t;
+
+/*
+ * y = D(x) over [rows, cols] (x_stride, y_stride; the other strides and eps are not
+ * looked at), and, on a gradient, dropout's backward pass.  y may be x itself (with
+ * y_stride == x_stride).  rows and cols below 2^32.  d must not be NULL.  D is taken
+ * in float32 and rounded once.  16-byte vectors as above.
+ */
+attn_status_t ln_dropout(const ln_params_t* p, const ln_dropout_t* d, const void* x, void* y, void* stream);
+
+/*
+ * ln_residual_fwd with h = D(x) + residual: D(x) is not rounded before the sum.
+ * d may be NULL (no dropout); rows below 2^32.
+ */
+attn_status_t ln_dropout_residual_fwd(const ln_params_t* p, const ln_dropout_t* d, const void* x, const void* residual,
+                                      const float* gamma, const float* beta, void* y, void* h, float* mean,
+                                      float* rstd, void* stream);
+
+typedef struct {
+  int64_t rows, cols;
+  int64_t dy_stride, dh_stride, h_stride, dx_stride, dr_stride; /* elements between consecutive rows */
+  attn_dtype_t dtype; /* element type of dy, dh, h, dx, dr (ATTN_BF16 or ATTN_F32) */
+} ln_bwd_params_t;
+
+/*
+ * The backward pass of ln_dropout_residual_fwd, from the stored h, mean and rstd.  With
+ * xh = (h - mean) rstd and g = dy gamma, per row
+ *     dr = dh + rstd (g - sum(g) / cols - xh sum(g xh) / cols),   dx = D(dr),
+ * and over the rows dgamma = sum(dy xh), dbeta = sum(dy).  dy is the gradient at y,
+ * dh the one that arrives at h by another way (NULL: none); dr is the residual's
+ * gradient and dx that of x (D(dr) of the unrounded dr).  Without dropout (d NULL or t
+ * = 0) the two are equal and either may be NULL; so may either with dropout.  gamma
+ * NULL: 1.  dgamma and dbeta, float32 [cols], may be NULL each; where rows is 0 they are
+ * set to 0.  Arithmetic and sums in float32; a column's rows are added in a fixed order
+ * (the results are bit-identical from run to run).
+ *
+ * Constraints as for ln_residual_fwd; outputs must not overlap inputs or one another,
+ * except that dx or dr may be dy or dh itself, with the same stride.  workspace:
+ * device scratch, 256-byte aligned, >= ln_residual_bwd_workspace_size(p) bytes (SIZE_MAX
+ * if the parameters are invalid), not needed if dgamma and dbeta are NULL; calls that
+ * may overlap need one each.
+ */
+size_t ln_residual_bwd_workspace_size(const ln_bwd_params_t* p);
+attn_status_t ln_residual_bwd(const ln_bwd_params_t* p, const ln_dropout_t* d, const void* dy, const void* dh,
+                              const void* h, const float* mean, const float* rstd, const float* gamma, void* dx,
+                              void* dr, float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 #ifdef __cplusplus
 }
