@@ -73,6 +73,20 @@ __device__ __forceinline__ void drop_vector(const DropArgs& d, const DropKey& ke
   for (int e = 0; e < E; ++e) v[e] = drop_keeps(bits, e, d.below) ? v[e] * d.factor : 0.f;
 }
 
+// The same for pairs.
+template <int P>
+__device__ __forceinline__ void drop_pairs(const DropArgs& d, const DropKey& key, uint32_t c0, uint32_t row,
+                                           float2 (&v)[P]) {
+  static_assert(P == 2 || P == 4, "half a group or a whole one");
+  uint4 bits = drop_bits(key, c0 >> 3, row);
+  if (P == 2 && (c0 & 4)) bits.x = bits.z, bits.y = bits.w;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    v[i].x = drop_keeps(bits, 2 * i, d.below) ? v[i].x * d.factor : 0.f;
+    v[i].y = drop_keeps(bits, 2 * i + 1, d.below) ? v[i].y * d.factor : 0.f;
+  }
+}
+
 // Checks d and fills a: dropped stays false where nothing is dropped (d is NULL or t is 0).
 // Returns what is wrong, or NULL.
 inline const char* resolve_dropout(const ln_dropout_t* d, DropArgs* a, bool* drops) {

@@ -9,9 +9,9 @@ Tolerances, with u = 2^-24 (float32's half step), n columns, R rows, per element
         (|dr| + |dh|), and half a step of the type (finfo.eps / 2) of dr.
   dx    the same, times the factor, and three more roundings (3u |dx|).
   dgamma, dbeta
-        a column's term passes at most ceil(R / 304) additions in a thread (8 rows a block: fewer), 8 in a
-        block, 38 + 8 in the join, and has at most 4 roundings of its own:
-        (R / 304 + 64) u sum|terms|.
+        there are at least min(R, 152) blocks; a column's term passes at most R / 152 + 1 additions in a thread, 2 + 16
+        in a block, 608 / 8 + 8 in the join, and has at most 4 roundings of its own:
+        (R / 152 + 108) u sum|terms|.
   forward with dropout: as tests/test_gpu_ln.py, h in addition off by the factor's and the product's
         rounding: (eps / 2) |h| + 4u (|D(x)| + |h|).
 """
@@ -74,7 +74,7 @@ def check(got, inp, p=0.0, seed=0, offset=0, rows=None):
     else:
         assert np.array_equal(dx, dr)
     if rows is None and dgamma is not None:
-        n = (dy.shape[0] / 304 + 64) * U
+        n = (dy.shape[0] / 152 + 108) * U
         assert np.all(np.abs(dgamma - rgamma) <= n * np.abs(dy * xh).sum(0)), "dgamma"
         assert np.all(np.abs(dbeta - rbeta) <= n * np.abs(dy).sum(0)), "dbeta"
 

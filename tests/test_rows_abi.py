@@ -147,7 +147,7 @@ def test_bwd_strides_pointers_and_workspace(lib):
     for rows in (1, 1000, 1 << 40):
         for cols in (1, 64, 1000, 16384):
             p = bwd_params(rows=rows, cols=cols)
-            assert 8 * cols <= lib.ln_residual_bwd_workspace_size(p) < 4000 * cols
+            assert 8 * cols <= lib.ln_residual_bwd_workspace_size(p) < 5000 * cols
 
 
 @pytest.mark.parametrize("change, code", [
