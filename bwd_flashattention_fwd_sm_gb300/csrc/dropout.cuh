@@ -57,34 +57,56 @@ __device__ __forceinline__ uint4 drop_bits(const DropKey& key, uint32_t group, u
   return make_uint4(c0, c1, c2, c3);
 }
 
-__device__ __forceinline__ bool drop_keeps(const uint4& bits, int e, uint32_t below) {
-  const uint32_t w = e < 2 ? bits.x : e < 4 ? bits.y : e < 6 ? bits.z : bits.w;
-  return (e & 1 ? w >> 16 : w & 0xFFFFu) >= below;
+// What a thread compares with: t in both halves of a word, its top bits and the rest apart.
+struct DropRate {
+  uint32_t whole, low, none;  // none: 0 if everything is dropped (t is 65536), else all ones
+  float factor;
+};
+
+__device__ __forceinline__ DropRate drop_rate(const DropArgs& d) {
+  const uint32_t t = (d.below & 0xFFFFu) * 0x10001u;
+  return DropRate{t, t & 0x7FFF7FFFu, d.below > 0xFFFFu ? 0u : 0xFFFFFFFFu, d.factor};
 }
 
-// The E elements (4 or 8, at a column that is a multiple of E) v of one row, through the dropout.
-template <int E>
-__device__ __forceinline__ void drop_vector(const DropArgs& d, const DropKey& key, int64_t c0, int64_t row,
-                                            float (&v)[E]) {
-  static_assert(E == 4 || E == 8, "half a group or a whole one");
-  uint4 bits = drop_bits(key, (uint32_t)(c0 >> 3), (uint32_t)row);
-  if (E == 4 && (c0 & 4)) bits.x = bits.z, bits.y = bits.w;
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = drop_keeps(bits, e, d.below) ? v[e] * d.factor : 0.f;
+// Both halves u of a word against t at once: their top bits are set where u >= t.  Without the
+// top bits (u | top) - t cannot borrow from the other half; with them u >= t is u's bit if
+// the two differ and that difference's bit if not.
+__device__ __forceinline__ uint32_t drop_compare(uint32_t word, const DropRate& r) {
+  const uint32_t d = (word | 0x80008000u) - r.low;
+  return ((word & ~r.whole) | (~(word ^ r.whole) & d)) & r.none;
 }
 
-// The same for pairs.
-template <int P>
-__device__ __forceinline__ void drop_pairs(const DropArgs& d, const DropKey& key, uint32_t c0, uint32_t row,
-                                           float2 (&v)[P]) {
-  static_assert(P == 2 || P == 4, "half a group or a whole one");
+// Masks for what drop_compare gives, its top bits spread: of two 16-bit elements, of the lower
+// and of the upper 32-bit element.
+template <int kBytes>
+__device__ __forceinline__ uint32_t drop_spread(uint32_t c) {
+  uint32_t m;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(m) : "r"(c), "n"(kBytes));
+  return m;
+}
+__device__ __forceinline__ uint32_t drop_mask_pair(uint32_t c) { return drop_spread<0xBB99>(c); }
+__device__ __forceinline__ uint32_t drop_mask_low(uint32_t c) { return drop_spread<0x9999>(c); }
+__device__ __forceinline__ uint32_t drop_mask_high(uint32_t c) { return drop_spread<0xBBBB>(c); }
+
+// A 16-byte vector of T (at column c0 of its row) with 0 in the place of what is dropped; the
+// factor is the caller's to apply.
+template <class T>
+__device__ __forceinline__ uint4 drop_mask(uint4 v, uint32_t c0, uint32_t row, const DropKey& key, const DropRate& r) {
   uint4 bits = drop_bits(key, c0 >> 3, row);
-  if (P == 2 && (c0 & 4)) bits.x = bits.z, bits.y = bits.w;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    v[i].x = drop_keeps(bits, 2 * i, d.below) ? v[i].x * d.factor : 0.f;
-    v[i].y = drop_keeps(bits, 2 * i + 1, d.below) ? v[i].y * d.factor : 0.f;
+  if constexpr (sizeof(T) == 2) {
+    v.x &= drop_mask_pair(drop_compare(bits.x, r));
+    v.y &= drop_mask_pair(drop_compare(bits.y, r));
+    v.z &= drop_mask_pair(drop_compare(bits.z, r));
+    v.w &= drop_mask_pair(drop_compare(bits.w, r));
+  } else {
+    const bool upper = c0 & 4;
+    const uint32_t a = drop_compare(upper ? bits.z : bits.x, r), b = drop_compare(upper ? bits.w : bits.y, r);
+    v.x &= drop_mask_low(a);
+    v.y &= drop_mask_high(a);
+    v.z &= drop_mask_low(b);
+    v.w &= drop_mask_high(b);
   }
+  return v;
 }
 
 // Checks d and fills a: dropped stays false where nothing is dropped (d is NULL or t is 0).

@@ -77,7 +77,7 @@ struct EmbedArgs {
   int64_t tokens, vocab, dim;
   int64_t x_stride, y_stride;
   int64_t padding;
-  int64_t row_step, unit_step;  // lookup: all threads' vectors on, as rows and vectors of a row
+  int64_t row_step, unit_step;  // fill: all threads' vectors on, as rows and vectors of a row
   float scale;
   int ids_64, accumulate;
   uint32_t* keys[2];    // gradient: ids and places, before and after a pass
@@ -91,38 +91,34 @@ __device__ __forceinline__ int64_t id_at(const EmbedArgs& a, int64_t i) {
   return a.ids_64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
 }
 
+// `lanes` threads (a power of two) on a row; each has up to kAtOnce vectors of it in flight.
 template <class T, int N>
-__global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a) {
-  const int64_t units = a.dim / N;  // N divides dim
-  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  int64_t row = first / units, unit = first % units;
-  const T* W = static_cast<const T*>(a.x);
-  T* Y = static_cast<T*>(a.y);
-  while (row < a.tokens) {
-    int64_t rows[kAtOnce], at[kAtOnce];
+__global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a, int lanes_log) {
+  const int lanes = 1 << lanes_log;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads >> lanes_log) + (threadIdx.x >> lanes_log);
+  if (row >= a.tokens) return;
+  const int64_t id = id_at(a, row);
+  const bool there = id >= 0 && id < a.vocab;
+  if (!there) set_status(a.status, kStatusBounds);
+  const int units = (int)(a.dim / N);  // N divides dim
+  const T* w = static_cast<const T*>(a.x) + (there ? id : 0) * a.x_stride;
+  T* y = static_cast<T*>(a.y) + row * a.y_stride;
+  for (int u = threadIdx.x & (lanes - 1); u < units; u += kAtOnce * lanes) {
     float v[kAtOnce][N];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      rows[i] = row, at[i] = unit * N;
-      if (row < a.tokens) {
-        const int64_t id = id_at(a, row);
-        if (id >= 0 && id < a.vocab) {
-          Elems<T, N>::load(W + id * a.x_stride + at[i], v[i]);
-        } else {
-          set_status(a.status, kStatusBounds);
+      if (there && u + i * lanes < units) {
+        Elems<T, N>::load(w + (u + i * lanes) * N, v[i]);
+      } else {
 #pragma unroll
-          for (int e = 0; e < N; ++e) v[i][e] = 0.f;
-        }
+        for (int e = 0; e < N; ++e) v[i][e] = 0.f;
       }
-      row += a.row_step, unit += a.unit_step;
-      if (unit >= units) unit -= units, ++row;
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      if (rows[i] >= a.tokens) continue;
 #pragma unroll
       for (int e = 0; e < N; ++e) v[i][e] *= a.scale;
-      Elems<T, N>::store(Y + rows[i] * a.y_stride + at[i], v[i]);
+      if (u + i * lanes < units) Elems<T, N>::store(y + (u + i * lanes) * N, v[i]);
     }
   }
 }
@@ -356,9 +352,11 @@ int64_t blocks_for(int64_t rows, int64_t units, int64_t most, EmbedArgs* a) {
 }
 
 template <class T, int N>
-void launch_lookup(EmbedArgs a, int sms, cudaStream_t st) {
-  const int64_t blocks = blocks_for(a.tokens, a.dim / N, (int64_t)sms * 8, &a);
-  k_embed<T, N><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+void launch_lookup(const EmbedArgs& a, cudaStream_t st) {
+  int lanes_log = 0;
+  while ((1 << lanes_log) < kThreads && ((int64_t)kAtOnce << lanes_log) < a.dim / N) ++lanes_log;
+  const int rows = kThreads >> lanes_log;
+  k_embed<T, N><<<(unsigned)((a.tokens + rows - 1) / rows), kThreads, 0, st>>>(a, lanes_log);
 }
 
 template <class W, int N>
@@ -433,12 +431,12 @@ attn_status_t attn_embedding_fwd(const attn_embedding_params_t* p, const void* w
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int n = width(at, p->dim, esize);
   if (p->dtype == ATTN_BF16) {
-    if (n == 8) launch_lookup<__nv_bfloat16, 8>(a, sms, st);
-    else if (n >= 2) launch_lookup<__nv_bfloat16, 2>(a, sms, st);
-    else launch_lookup<__nv_bfloat16, 1>(a, sms, st);
+    if (n == 8) launch_lookup<__nv_bfloat16, 8>(a, st);
+    else if (n >= 2) launch_lookup<__nv_bfloat16, 2>(a, st);
+    else launch_lookup<__nv_bfloat16, 1>(a, st);
   } else {
-    if (n == 4) launch_lookup<float, 4>(a, sms, st);
-    else launch_lookup<float, 1>(a, sms, st);
+    if (n == 4) launch_lookup<float, 4>(a, st);
+    else launch_lookup<float, 1>(a, st);
   }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : efail(ATTN_ERR_CUDA, "launch failed");
 }

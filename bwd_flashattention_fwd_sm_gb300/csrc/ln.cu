@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
   T* Y = static_cast<T*>(a.y);
   T* H = static_cast<T*>(a.h);
   DropKey key{};
-  if constexpr (kDrop) key = drop_key(a.drop);
+  DropRate rate{};
+  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
   for (int64_t row = blockIdx.x; row < a.p.rows; row += gridDim.x) {
     const T* xr = X + row * a.p.x_stride;
     const T* rr = R ? R + row * a.p.r_stride : nullptr;
@@ -208,8 +209,12 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
       sv[j] = Stats{0.f, 0.f, 0.f};
       if (vi < nvec) {
         if (!ragged || (a.vec && c0 + E <= cols)) {
+          if constexpr (kDrop) ux[j] = drop_mask<T>(ux[j], (uint32_t)c0, (uint32_t)row, key, rate);
           Vec<T>::unpack(ux[j], v[j]);
-          if constexpr (kDrop) drop_vector<E>(a.drop, key, c0, row, v[j]);
+          if constexpr (kDrop) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[j][e] *= rate.factor;
+          }
           if (rr) {
             float t[E];
             Vec<T>::unpack(ur[j], t);
@@ -230,7 +235,11 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
               ++cnt;
             }
           }
-          if constexpr (kDrop) drop_vector<E>(a.drop, key, c0, row, v[j]);
+          if constexpr (kDrop) {
+            Vec<T>::unpack(drop_mask<T>(Vec<T>::pack(v[j]), (uint32_t)c0, (uint32_t)row, key, rate), v[j]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[j][e] *= rate.factor;
+          }
           if (rr) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -355,7 +364,8 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
   T* Y = static_cast<T*>(a.y);
   T* H = static_cast<T*>(a.h);
   DropKey key{};
-  if constexpr (kDrop) key = drop_key(a.drop);
+  DropRate rate{};
+  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
   int64_t it = 0;
   bool ok = true;
   for (int64_t row = blockIdx.x; row < a.p.rows; row += gridDim.x, ++it) {
@@ -373,8 +383,14 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
       const int64_t vi = tid + (int64_t)j * kThreadsLn;
       sv[j] = Stats{0.f, 0.f, 0.f};
       if (vi < nvec) {
-        Vec<T>::load(reinterpret_cast<const T*>(xsm) + vi * E, v[j]);
-        if constexpr (kDrop) drop_vector<E>(a.drop, key, vi * E, row, v[j]);
+        if constexpr (kDrop) {
+          const uint4 raw = reinterpret_cast<const uint4*>(xsm)[vi];
+          Vec<T>::unpack(drop_mask<T>(raw, (uint32_t)(vi * E), (uint32_t)row, key, rate), v[j]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][e] *= rate.factor;
+        } else {
+          Vec<T>::load(reinterpret_cast<const T*>(xsm) + vi * E, v[j]);
+        }
         if (has_r) {
           float t[E];
           Vec<T>::load(reinterpret_cast<const T*>(xsm + row_bytes) + vi * E, t);

@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
   const int64_t cols = a.p.cols;
   const float inv = 1.f / (float)cols;
   DropKey key{};
-  if constexpr (kDrop) key = drop_key(a.drop);
+  DropRate rate{};
+  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
   float sg[kVpt][E], sb[kVpt][E];
 #pragma unroll
   for (int j = 0; j < kVpt; ++j)
@@ -154,7 +155,11 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
       for (int e = 0; e < E; ++e) d[e] = ij[e] + rstd * (gj[e] - s0 - xj[e] * s1);
       if (a.dr) store_cols<T>(static_cast<T*>(a.dr) + row * a.p.dr_stride, c0, cols, a.vec, d);
       if (a.dx) {
-        if constexpr (kDrop) drop_vector<E>(a.drop, key, c0, row, d);
+        if constexpr (kDrop) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) d[e] *= rate.factor;
+          Vec<T>::unpack(drop_mask<T>(Vec<T>::pack(d), (uint32_t)c0, (uint32_t)row, key, rate), d);
+        }
         store_cols<T>(static_cast<T*>(a.dx) + row * a.p.dx_stride, c0, cols, a.vec, d);
       }
     }
@@ -180,7 +185,8 @@ __global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
   const int cols = (int)a.p.cols;
   const float inv = 1.f / (float)cols;
   DropKey key{};
-  if constexpr (kDrop) key = drop_key(a.drop);
+  DropRate rate{};
+  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
   float2 sg[kVpt][P], sb[kVpt][P], gamma[kVpt][P];
 #pragma unroll
   for (int j = 0; j < kVpt; ++j)
@@ -269,11 +275,12 @@ __global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
       Vec<T>::pairs(in[j], d);
 #pragma unroll
       for (int i = 0; i < P; ++i) d[i] = pair_fma(pair_fma(xh[j][i], n1, pair_add(g[j][i], n0)), r2, d[i]);
-      auto store = [&](void* base, int64_t stride) {
+      auto store = [&](void* base, int64_t stride, uint4 v) {
         T* out = static_cast<T*>(base) + row * stride + c0;
         if (kWhole || (a.vec && c0 + E <= cols)) {
-          *reinterpret_cast<uint4*>(out) = Vec<T>::pack(d);
+          *reinterpret_cast<uint4*>(out) = v;
         } else {
+          Vec<T>::pairs(v, d);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             if (c0 + 2 * i < cols) Vec<T>::store1(out + 2 * i, d[i].x);
@@ -281,11 +288,15 @@ __global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
           }
         }
       };
-      if (a.dr) store(a.dr, a.p.dr_stride);
-      if (a.dx) {
-        if constexpr (kDrop) drop_pairs<P>(a.drop, key, (uint32_t)c0, (uint32_t)row, d);
-        store(a.dx, a.p.dx_stride);
+      uint4 dx = Vec<T>::pack(d);
+      const uint4 dr = dx;
+      if constexpr (kDrop) {  // of the unrounded dr
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = pair_mul(d[i], make_float2(rate.factor, rate.factor));
+        dx = drop_mask<T>(Vec<T>::pack(d), (uint32_t)c0, (uint32_t)row, key, rate);
       }
+      if (a.dr) store(a.dr, a.p.dr_stride, dr);
+      if (a.dx) store(a.dx, a.p.dx_stride, dx);
     }
   }
   if (!a.part) return;
@@ -369,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     }
   }
   DropKey key{};
-  if constexpr (kDrop) key = drop_key(a.drop);
+  DropRate rate{};
+  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
   float2 sg[kVpt][P], sb[kVpt][P], keep[kKeepGamma ? kVpt : 1][P];
   auto gamma_at = [&](int j, float2 (&g)[P]) {
     const int c0 = (tid + j * kThreads) * E;
@@ -456,10 +468,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         g[i] = pair_fma(g[i], kKeepGamma ? keep[kKeepGamma ? j : 0][i] : w[i], n0);
         d[i] = pair_fma(pair_fma(xh[i], n1, g[i]), scale2, d[i]);
       }
-      if (a.dr) *reinterpret_cast<uint4*>(static_cast<T*>(a.dr) + row * a.p.dr_stride + c0) = Vec<T>::pack(d);
+      uint4 dx = Vec<T>::pack(d);
+      if (a.dr) *reinterpret_cast<uint4*>(static_cast<T*>(a.dr) + row * a.p.dr_stride + c0) = dx;
       if (a.dx) {
-        if constexpr (kDrop) drop_pairs<P>(a.drop, key, (uint32_t)c0, (uint32_t)row, d);
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.p.dx_stride + c0) = Vec<T>::pack(d);
+        if constexpr (kDrop) {  // of the unrounded dr
+#pragma unroll
+          for (int i = 0; i < P; ++i) d[i] = pair_mul(d[i], make_float2(rate.factor, rate.factor));
+          dx = drop_mask<T>(Vec<T>::pack(d), (uint32_t)c0, (uint32_t)row, key, rate);
+        }
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.p.dx_stride + c0) = dx;
       }
     }
     last = s;
