@@ -9,9 +9,8 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib
 from ._lib import LnDropoutC, LnParamsC, check
-from .rows import DTYPES, as_rows, on_stream
+from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library
 
 _MOD = 1 << 64
 
@@ -47,15 +46,16 @@ def dropout(x, p: float, *, seed: int = 0, offset: int = 0, rng=None, stream=Non
     if out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device
                             or not out.is_contiguous()):
         raise ValueError("out must be contiguous and match x in shape, dtype and device")
-    d = dropout_params(p, seed, offset, rng, x.device) or LnDropoutC()
-
-    def call(handle):
-        cols = x.shape[-1]
-        src, stride = as_rows(x, cols)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        if y.numel():
-            c = LnParamsC(y.numel() // cols, cols, stride, cols, cols, cols, 0.0, dtype)
-            check(_lib.load().ln_dropout(c, d, src.data_ptr(), y.data_ptr(), handle), "ln_dropout")
-        return y
-
-    return on_stream(x.device, stream, (x, rng, out), call)
+    device = x.device
+    if stream is not None or device.index != current_device():
+        with elsewhere(device, stream, (x, rng, out)):
+            return dropout(x, p, seed=seed, offset=offset, rng=rng, out=out)
+    d = dropout_params(p, seed, offset, rng, device) or LnDropoutC()
+    cols = x.shape[-1]
+    src, stride = as_rows(x, cols)
+    y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
+    n = y.numel()
+    if n:
+        c = LnParamsC(n // cols, cols, stride, cols, cols, cols, 0.0, dtype)
+        check(library().ln_dropout(c, d, src.data_ptr(), y.data_ptr(), current_stream(device.index)), "ln_dropout")
+    return y

@@ -9,10 +9,9 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib
 from ._lib import EmbeddingParamsC, check
 from .attention import _workspace
-from .rows import DTYPES, as_rows, on_stream
+from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library
 
 
 def _check_ids(ids, device):
@@ -30,19 +29,19 @@ def embedding(weight, ids, *, scale: float = 1.0, stream=None):
     dtype = DTYPES.get(weight.dtype)
     if dtype is None or weight.dim() != 2:
         raise ValueError("weight must be bfloat16 or float32, [vocab, dim]")
-    _check_ids(ids, weight.device)
-
-    def call(handle):
-        vocab, dim = weight.shape
-        w, w_stride = as_rows(weight, dim)
-        i = ids.contiguous()
-        y = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=weight.device)
-        p = EmbeddingParamsC(i.numel(), vocab, dim, dim, w_stride, scale, dtype, dtype, i.dtype == torch.int64, 0, -1)
-        check(_lib.load().attn_embedding_fwd(p, w.data_ptr(), i.data_ptr(), y.data_ptr(), handle),
-              "attn_embedding_fwd")
-        return y
-
-    return on_stream(weight.device, stream, (weight, ids), call)
+    device = weight.device
+    _check_ids(ids, device)
+    if stream is not None or device.index != current_device():
+        with elsewhere(device, stream, (weight, ids)):
+            return embedding(weight, ids, scale=scale)
+    vocab, dim = weight.shape
+    weight, w_stride = as_rows(weight, dim)
+    ids = ids.contiguous()
+    y = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=device)
+    p = EmbeddingParamsC(ids.numel(), vocab, dim, dim, w_stride, scale, dtype, dtype, ids.dtype == torch.int64, 0, -1)
+    check(library().attn_embedding_fwd(p, weight.data_ptr(), ids.data_ptr(), y.data_ptr(),
+                                       current_stream(device.index)), "attn_embedding_fwd")
+    return y
 
 
 def embedding_bwd(dy, ids, num_embeddings: int, *, scale: float = 1.0, padding_id: int | None = None, dtype=None,
@@ -71,19 +70,23 @@ def embedding_bwd(dy, ids, num_embeddings: int, *, scale: float = 1.0, padding_i
     if dy.shape[:-1] != ids.shape:
         raise ValueError(f"dy {tuple(dy.shape)} does not match ids {tuple(ids.shape)}")
 
-    def call(handle):
-        lib = _lib.load()
-        dim = dy.shape[-1]
-        a, stride = as_rows(dy, dim)
-        i = ids.contiguous()
-        dw = torch.empty((num_embeddings, dim), dtype=grad, device=device) if out is None else out
-        p = EmbeddingParamsC(i.numel(), num_embeddings, dim, stride, as_rows(dw, dim)[1], scale, DTYPES[dy.dtype],
-                             DTYPES[grad], i.dtype == torch.int64, out is not None,
-                             -1 if padding_id is None else padding_id)
-        need = lib.attn_embedding_bwd_workspace_size(p)
-        ws = _workspace(need, device, workspace)
-        check(lib.attn_embedding_bwd(p, a.data_ptr(), i.data_ptr(), dw.data_ptr(),
-                                     None if ws is None else ws.data_ptr(), need, handle), "attn_embedding_bwd")
-        return dw
-
-    return on_stream(device, stream, (dy, ids, workspace, out), call)
+    if stream is not None or device.index != current_device():
+        with elsewhere(device, stream, (dy, ids, workspace, out)):
+            return embedding_bwd(dy, ids, num_embeddings, scale=scale, padding_id=padding_id, dtype=grad,
+                                 workspace=workspace, out=out)
+    lib = library()
+    dim = dy.shape[-1]
+    dy, stride = as_rows(dy, dim)
+    ids = ids.contiguous()
+    dw, w_stride = out, dim
+    if out is None:
+        dw = torch.empty((num_embeddings, dim), dtype=grad, device=device)
+    else:
+        w_stride = as_rows(out, dim)[1]
+    p = EmbeddingParamsC(ids.numel(), num_embeddings, dim, stride, w_stride, scale, DTYPES[dy.dtype], DTYPES[grad],
+                         ids.dtype == torch.int64, out is not None, -1 if padding_id is None else padding_id)
+    need = lib.attn_embedding_bwd_workspace_size(p)
+    ws = _workspace(need, device, workspace)
+    check(lib.attn_embedding_bwd(p, dy.data_ptr(), ids.data_ptr(), dw.data_ptr(), None if ws is None else ws.data_ptr(),
+                                 need, current_stream(device.index)), "attn_embedding_bwd")
+    return dw

@@ -9,11 +9,10 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib
 from ._lib import LnBwdParamsC, LnParamsC, check
 from .attention import _workspace
 from .drop import dropout_params
-from .rows import DTYPES, as_rows, on_stream
+from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library
 
 
 def _ptr(t):
@@ -49,34 +48,37 @@ def layernorm_residual(x, residual=None, gamma=None, beta=None, *, eps: float = 
     if dtype is None:
         raise ValueError("x must be bfloat16 or float32")
     cols = _cols(x)
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
-                                 or residual.device != x.device):
+    device = x.device
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.device != device):
         raise ValueError("residual must match x in shape, dtype and device")
     _check_weight("gamma", gamma, cols)
     _check_weight("beta", beta, cols)
-    d = dropout_params(dropout_p, seed, offset, rng, x.device)
-
-    def call(handle):
-        a, a_stride = as_rows(x, cols)
-        r, r_stride = (None, cols) if residual is None else as_rows(residual, cols)
-        g = None if gamma is None else gamma.contiguous()
-        b = None if beta is None else beta.contiguous()
-        rows = x.numel() // cols
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        h = torch.empty_like(y) if return_sum else None
-        mean, rstd = (torch.empty((2, rows), dtype=torch.float32, device=x.device).unbind(0) if return_stats
-                      else (None, None))
-        p = LnParamsC(rows, cols, a_stride, r_stride, cols, cols, float(eps), dtype)
-        check(_lib.load().ln_dropout_residual_fwd(p, d, a.data_ptr(), _ptr(r), _ptr(g), _ptr(b), y.data_ptr(),
-                                                  _ptr(h), _ptr(mean), _ptr(rstd), handle), "ln_residual_fwd")
-        out = [y]
-        if return_sum:
-            out.append(h)
-        if return_stats:
-            out += [mean, rstd]
-        return out[0] if len(out) == 1 else tuple(out)
-
-    return on_stream(x.device, stream, (x, residual, gamma, beta, rng), call)
+    if stream is not None or device.index != current_device():
+        with elsewhere(device, stream, (x, residual, gamma, beta, rng)):
+            return layernorm_residual(x, residual, gamma, beta, eps=eps, return_sum=return_sum,
+                                      return_stats=return_stats, dropout_p=dropout_p, seed=seed, offset=offset, rng=rng)
+    d = dropout_params(dropout_p, seed, offset, rng, device)
+    x, x_stride = as_rows(x, cols)
+    r_stride = cols
+    if residual is not None:
+        residual, r_stride = as_rows(residual, cols)
+    gamma = None if gamma is None else gamma.contiguous()
+    beta = None if beta is None else beta.contiguous()
+    rows = x.numel() // cols
+    y = torch.empty(x.shape, dtype=x.dtype, device=device)
+    h = mean = rstd = None
+    if return_sum:
+        h = torch.empty_like(y)
+    if return_stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=device)
+        rstd = torch.empty_like(mean)
+    p = LnParamsC(rows, cols, x_stride, r_stride, cols, cols, float(eps), dtype)
+    check(library().ln_dropout_residual_fwd(p, d, x.data_ptr(), _ptr(residual), _ptr(gamma), _ptr(beta), y.data_ptr(),
+                                            _ptr(h), _ptr(mean), _ptr(rstd), current_stream(device.index)),
+          "ln_residual_fwd")
+    if return_sum:
+        return (y, h, mean, rstd) if return_stats else (y, h)
+    return (y, mean, rstd) if return_stats else y
 
 
 def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p: float = 0.0, seed: int = 0,
@@ -103,27 +105,30 @@ def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p:
         if t.dtype != torch.float32 or t.numel() != rows or t.device != device:
             raise ValueError(f"{name} must be a float32 CUDA tensor of {rows} elements")
     _check_weight("gamma", gamma, cols)
+    if stream is not None or device.index != current_device():
+        with elsewhere(device, stream, (dy, h, mean, rstd, gamma, dh, rng, workspace)):
+            return layernorm_residual_bwd(dy, h, mean, rstd, gamma, dh, dropout_p=dropout_p, seed=seed, offset=offset,
+                                          rng=rng, weight_grads=weight_grads, workspace=workspace)
     d = dropout_params(dropout_p, seed, offset, rng, device)
-
-    def call(handle):
-        lib = _lib.load()
-        a, a_stride = as_rows(dy, cols)
-        b, b_stride = as_rows(h, cols)
-        c, c_stride = (None, cols) if dh is None else as_rows(dh, cols)
-        m, s = mean.contiguous(), rstd.contiguous()
-        g = None if gamma is None else gamma.contiguous()
-        dr = torch.empty(dy.shape, dtype=dy.dtype, device=device)
-        dx = dr if d is None else torch.empty_like(dr)
-        p = LnBwdParamsC(rows, cols, a_stride, c_stride, b_stride, cols, cols, dtype)
-        dgamma = dbeta = ws = None
-        need = 0
-        if weight_grads:
-            dgamma, dbeta = torch.empty((2, cols), dtype=torch.float32, device=device).unbind(0)
-            need = lib.ln_residual_bwd_workspace_size(p)
-            ws = _workspace(need, device, workspace)
-        check(lib.ln_residual_bwd(p, d, a.data_ptr(), _ptr(c), b.data_ptr(), m.data_ptr(), s.data_ptr(), _ptr(g),
-                                  None if d is None else dx.data_ptr(), dr.data_ptr(), _ptr(dgamma), _ptr(dbeta),
-                                  _ptr(ws), need, handle), "ln_residual_bwd")
-        return dx, dr, dgamma, dbeta
-
-    return on_stream(device, stream, (dy, h, mean, rstd, gamma, dh, rng, workspace), call)
+    lib = library()
+    dy, dy_stride = as_rows(dy, cols)
+    h, h_stride = as_rows(h, cols)
+    dh_stride = cols
+    if dh is not None:
+        dh, dh_stride = as_rows(dh, cols)
+    mean, rstd = mean.contiguous(), rstd.contiguous()
+    gamma = None if gamma is None else gamma.contiguous()
+    dr = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+    dx = dr if d is None else torch.empty_like(dr)
+    p = LnBwdParamsC(rows, cols, dy_stride, dh_stride, h_stride, cols, cols, dtype)
+    dgamma = dbeta = ws = None
+    need = 0
+    if weight_grads:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=device)
+        dbeta = torch.empty_like(dgamma)
+        need = lib.ln_residual_bwd_workspace_size(p)
+        ws = _workspace(need, device, workspace)
+    check(lib.ln_residual_bwd(p, d, dy.data_ptr(), _ptr(dh), h.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                              _ptr(gamma), None if d is None else dx.data_ptr(), dr.data_ptr(), _ptr(dgamma),
+                              _ptr(dbeta), _ptr(ws), need, current_stream(device.index)), "ln_residual_bwd")
+    return dx, dr, dgamma, dbeta

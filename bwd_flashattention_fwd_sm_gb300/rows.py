@@ -5,7 +5,11 @@ from __future__ import annotations
 
 import torch
 
+from . import _lib
 from ._lib import ATTN_BF16, ATTN_F32
+
+current_device = torch.cuda.current_device
+current_stream = torch._C._cuda_getCurrentRawStream  # of a device's index, as the handle that the library takes
 
 DTYPES = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}
 
@@ -35,16 +39,30 @@ def as_rows(t, cols: int):
     return t.contiguous(), cols
 
 
-def on_stream(device, stream, tensors, call):
-    """call(handle) with ``device`` current and, where ``stream`` is given, that stream: what is allocated for
-    the call then belongs to the stream that it runs on, and what comes from another stream (``tensors``) is not
-    given away before the call has run."""
-    index = device.index
-    if stream is None and index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+class elsewhere:
+    """With ``device`` current and, where ``stream`` is given, that stream: what is allocated for a call then belongs
+    to the stream that it runs on, and what comes from another stream (``tensors``) is not given away before
+    the call has run."""
+
+    def __init__(self, device, stream, tensors):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self._device, self._stream, self._tensors = torch.cuda.device(device), torch.cuda.stream(stream), ()
         if stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        return call(torch._C._cuda_getCurrentRawStream(index))
+            self._tensors = [t for t in tensors if t is not None]
+            self._on = stream
+
+    def __enter__(self):
+        self._device.__enter__()
+        self._stream.__enter__()
+        for t in self._tensors:
+            t.record_stream(self._on)
+
+    def __exit__(self, *error):
+        self._stream.__exit__(*error)
+        self._device.__exit__(*error)
+
+
+def library():
+    """The loaded library."""
+    return _lib._lib or _lib.load()
