@@ -109,6 +109,40 @@ __device__ __forceinline__ uint4 drop_mask(uint4 v, uint32_t c0, uint32_t row, c
   return v;
 }
 
+// The same at any column c0, where kAny says so: the vector's elements may belong to two groups (of
+// a group in front of the row only elements that are no column).
+template <class T, bool kAny>
+__device__ __forceinline__ uint4 drop_mask_at(uint4 v, int c0, uint32_t row, const DropKey& key, const DropRate& r) {
+  if constexpr (!kAny) {
+    return drop_mask<T>(v, (uint32_t)c0, row, key, r);
+  } else {
+    const uint4 a = drop_bits(key, (uint32_t)(c0 >> 3), row), b = drop_bits(key, (uint32_t)(c0 >> 3) + 1, row);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    // the vector's 16-bit numbers to the front: by four, by two, by one
+    if (c0 & 4)
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    if (c0 & 2)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (c0 & 1) * 16);
+    if constexpr (sizeof(T) == 2) {
+      v.x &= drop_mask_pair(drop_compare(w[0], r));
+      v.y &= drop_mask_pair(drop_compare(w[1], r));
+      v.z &= drop_mask_pair(drop_compare(w[2], r));
+      v.w &= drop_mask_pair(drop_compare(w[3], r));
+    } else {
+      const uint32_t x = drop_compare(w[0], r), y = drop_compare(w[1], r);
+      v.x &= drop_mask_low(x);
+      v.y &= drop_mask_high(x);
+      v.z &= drop_mask_low(y);
+      v.w &= drop_mask_high(y);
+    }
+    return v;
+  }
+}
+
 // Checks d and fills a: dropped stays false where nothing is dropped (d is NULL or t is 0).
 // Returns what is wrong, or NULL.
 inline const char* resolve_dropout(const ln_dropout_t* d, DropArgs* a, bool* drops) {

@@ -220,7 +220,7 @@ def test_c_entry_writes_nothing_between_rows_or_behind(cols, step, dtype):
         assert bool((sums[32 + 2 * cols:] == 7).all())
         got = (dx[1][:, :cols], dr[1][:, :cols], sums[16:16 + cols], sums[32 + cols:32 + 2 * cols])
         check(got, inp, 0.2, 3, 1)
-        if (step * dt.itemsize) % 16 == 0:
+        if (step * dt.itemsize) % 16 == 0 and (cols * dt.itemsize) % 16 == 0:  # else the order of the sums differs
             assert all(torch.equal(x, y) for x, y in zip(ref, got))
 
 
