@@ -4,12 +4,13 @@
 // Lookup.  Bound by device memory; every thread has several vectors in flight, because a
 // row's address waits for its id.
 //
-// Gradient.  The tokens' places are sorted by id (k_embed_sort, a stable radix sort by
-// one cluster of blocks), cut in pieces of kPiece places, and each block adds the rows
-// of one piece over a stretch of columns: equal work however often a word comes.  A word
+// Gradient.  One launch sorts the tokens' places by id (a stable radix sort by one cluster of
+// blocks, all in shared memory but the hand-over between passes) while its other blocks write
+// zeros over the table.  The sorted places are cut in pieces of kPiece, and each block adds the rows of
+// one piece over a stretch of columns: equal work however often a word comes.  A word
 // that lies inside one piece is written to the table at once; of one that
 // several pieces share each piece leaves a partial sum, and k_embed_join adds those in order.
-// No atomics: the order of the sums follows from the ids alone.
+// No atomics on sums: their order follows from the ids alone.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -17,6 +18,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
 #include "../../include/gbembed.h"
 #include "common.cuh"
@@ -33,10 +35,15 @@ constexpr int kThreads = 256;     // lookup, fill
 constexpr int kAtOnce = 4;        // vectors of a thread in flight
 constexpr int kPiece = 32;        // sorted places of one block of the gradient's sums
 constexpr int kSumThreads = 128;
+constexpr int kSumAtOnce = 8;     // rows of dy in flight
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxBits = 9;       // of one pass's digit
+constexpr int kMaxBits = 10;      // of one pass's digit: a thread a digit
+constexpr int kHeld = 8;          // places that a thread keeps in registers
 constexpr int kMaxCluster = 8;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinCols = 128;    // of a warp: four each lane
 constexpr int64_t kMaxDim = 1 << 20;
 
 // N neighbouring elements of T as one load or store, widened to float32.
@@ -50,15 +57,25 @@ struct Elems {
     uint32_t w4;
     __device__ U() {}
   };
-  __device__ static void load(const T* p, float (&v)[N]) {
+  __device__ static U raw(const T* p) {
     U u;
     if constexpr (sizeof(T) * N == 16) u.w16 = *reinterpret_cast<const uint4*>(p);
     else if constexpr (sizeof(T) * N == 8) u.w8 = *reinterpret_cast<const uint2*>(p);
     else if constexpr (sizeof(T) * N == 4) u.w4 = *reinterpret_cast<const uint32_t*>(p);
     else u.t[0] = *p;
+    return u;
+  }
+  __device__ static U zero() {
+    U u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) u.t[i] = from_f32<T>(0.f);
+    return u;
+  }
+  __device__ static void widen(const U& u, float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = to_f32(u.t[i]);
   }
+  __device__ static void load(const T* p, float (&v)[N]) { widen(raw(p), v); }
   __device__ static void store(T* p, const float (&v)[N]) {
     U u;
 #pragma unroll
@@ -83,6 +100,7 @@ struct EmbedArgs {
   uint32_t* keys[2];    // gradient: ids and places, before and after a pass
   uint32_t* place[2];
   float* part;          // [pieces][2][dim]: sums of words that began before the piece, that go on after it
+  uint32_t* shared;     // how many words several pieces share, and the pieces in which they begin (in any order)
   int passes, bits;
   int* status;
 };
@@ -123,15 +141,15 @@ __global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a, int lanes
   }
 }
 
-// Zeros over the whole table.
-template <class T, int N>
-__global__ void __launch_bounds__(kThreads) k_embed_fill(const EmbedArgs a) {
+// Zeros over the whole table, by `blocks` blocks of which this one is number `block`.
+template <class W, int N>
+__device__ __forceinline__ void fill_table(const EmbedArgs& a, int64_t block, int64_t blocks) {
   const int64_t units = a.dim / N;
-  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  int64_t row = first / units, unit = first % units;
+  const int64_t at = block * blockDim.x + threadIdx.x;
+  int64_t row = at / units, unit = at % units;
   const float zero[N] = {};
   while (row < a.vocab) {
-    Elems<T, N>::store(static_cast<T*>(a.y) + row * a.y_stride + unit * N, zero);
+    Elems<W, N>::store(static_cast<W*>(a.y) + row * a.y_stride + unit * N, zero);
     row += a.row_step, unit += a.unit_step;
     if (unit >= units) unit -= units, ++row;
   }
@@ -150,10 +168,11 @@ __device__ __forceinline__ uint32_t key_at(const EmbedArgs& a, int64_t i) {
 // Stable sort of (id, place) by id: `passes` passes over digits of `bits` bits, least
 // significant first.  Every warp of the cluster owns a stretch of the input.  It counts its
 // digits; the counts of all warps in front of it and of all lower digits say where its
-// first of each digit goes; then it walks its stretch again, 32 at a time, and those
-// with equal digits find their order by a vote.  Ends in buffer passes % 2.
-__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) {
-  extern __shared__ uint32_t count[];  // [kSortWarps][digits]
+// first of each digit goes; then it takes its stretch in order, 32 at a time, and those
+// with equal digits find their order by a vote.  Ends in buffer passes % 2.  Up to kHeld * 32 places
+// of a warp stay in registers between the two (65536 tokens); longer stretches are read twice.
+// Bound by the latency of its steps: a pass takes about 4 us.
+__device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
   __shared__ uint32_t total[1 << kMaxBits];
   __shared__ uint32_t warp_total[kSortWarps];
   cg::cluster_group cluster = cg::this_cluster();
@@ -164,41 +183,61 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) 
   const int64_t each = ((a.tokens + warps - 1) / warps + 31) / 32 * 32;
   const int64_t begin = ((int64_t)rank * kSortWarps + warp) * each;
   const int64_t end = begin + each < a.tokens ? begin + each : a.tokens;
+  const bool held = each <= kHeld * 32;
   uint32_t* mine = count + warp * digits;
+  if (rank == 0 && threadIdx.x == 0) *a.shared = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
     const uint32_t* keys = a.keys[pass & 1];
     const uint32_t* place = a.place[pass & 1];
+    uint32_t* keys_to = a.keys[(pass + 1) & 1];
+    uint32_t* place_to = a.place[(pass + 1) & 1];
+    uint32_t key[kHeld], from[kHeld];
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        const int64_t i = begin + j * 32 + lane;
+        key[j] = from[j] = 0;
+        if (i < end) {
+          key[j] = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
+          from[j] = pass == 0 ? (uint32_t)i : __ldcg(place + i);
+        }
+      }
+    }
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
-    for (int64_t i = begin + lane; i - lane < end; i += 32) {
-      const unsigned active = __ballot_sync(0xffffffffu, i < end);
-      if (i < end) {
-        const uint32_t key = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
-        const uint32_t d = (key >> shift) & (digits - 1);
-        const unsigned same = __match_any_sync(active, d);
-        if (lane == __ffs(same) - 1) mine[d] += __popc(same);
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (begin + j * 32 + lane < end) atomicAdd(&mine[(key[j] >> shift) & (digits - 1)], 1u);
+    } else {
+      for (int64_t i = begin + lane; i < end; i += 32) {
+        const uint32_t k = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
+        atomicAdd(&mine[(k >> shift) & (digits - 1)], 1u);
       }
-      __syncwarp();
     }
     __syncthreads();
-    if ((int)threadIdx.x < digits) {  // exclusive over the block's warps
-      uint32_t sum = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t n = count[w * digits + threadIdx.x];
-        count[w * digits + threadIdx.x] = sum;
-        sum += n;
-      }
+    uint32_t counts[kSortWarps], sum = 0;  // of this thread's digit
+    if ((int)threadIdx.x < digits) {
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) counts[w] = count[w * digits + threadIdx.x];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) sum += counts[w];
       total[threadIdx.x] = sum;
     }
-    cluster.sync();
-    uint32_t all = 0, before = 0;
-    if ((int)threadIdx.x < digits)
-      for (unsigned r = 0; r < blocks; ++r) {
-        const uint32_t n = cluster.map_shared_rank(total, r)[threadIdx.x];
-        all += n;
-        if (r < rank) before += n;
+    if (blocks > 1) cluster.sync();
+    uint32_t all = sum, before = 0;
+    if (blocks > 1 && (int)threadIdx.x < digits) {
+      uint32_t n[kMaxCluster];
+#pragma unroll
+      for (unsigned r = 0; r < kMaxCluster; ++r) n[r] = r < blocks ? cluster.map_shared_rank(total, r)[threadIdx.x] : 0;
+      all = 0;
+#pragma unroll
+      for (unsigned r = 0; r < kMaxCluster; ++r) {
+        all += n[r];
+        if (r < rank) before += n[r];
       }
+    }
     uint32_t upto = all;  // inclusive over the digits
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -210,30 +249,60 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) 
     if ((int)threadIdx.x < digits) {
       uint32_t start = before + upto - all;
       for (int w = 0; w < warp; ++w) start += warp_total[w];
-      for (int w = 0; w < kSortWarps; ++w) count[w * digits + threadIdx.x] += start;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        count[w * digits + threadIdx.x] = start;
+        start += counts[w];
+      }
     }
     __syncthreads();
-    uint32_t* keys_to = a.keys[(pass + 1) & 1];
-    uint32_t* place_to = a.place[(pass + 1) & 1];
-    for (int64_t i = begin + lane; i - lane < end; i += 32) {
-      const unsigned active = __ballot_sync(0xffffffffu, i < end);
-      if (i < end) {
-        const uint32_t key = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
-        const uint32_t from = pass == 0 ? (uint32_t)i : __ldcg(place + i);
-        const uint32_t d = (key >> shift) & (digits - 1);
+    auto put = [&](bool there, uint32_t k, uint32_t f) {  // the whole warp
+      const unsigned active = __ballot_sync(0xffffffffu, there);
+      if (there) {
+        const uint32_t d = (k >> shift) & (digits - 1);
         const unsigned same = __match_any_sync(active, d);
         const uint32_t to = mine[d] + __popc(same & ((1u << lane) - 1));
         if (bounds_ok(to < (uint64_t)a.tokens, a.status)) {
-          keys_to[to] = key;
-          place_to[to] = from;
+          keys_to[to] = k;
+          place_to[to] = f;
         }
         __syncwarp(active);
         if (lane == __ffs(same) - 1) mine[d] += __popc(same);
       }
       __syncwarp();
+    };
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (begin + j * 32 < end) put(begin + j * 32 + lane < end, key[j], from[j]);
+    } else {
+      for (int64_t i = begin + lane; i - lane < end; i += 32) {
+        const bool there = i < end;
+        put(there, !there ? 0 : pass == 0 ? key_at(a, i) : __ldcg(keys + i),
+            !there || pass == 0 ? (uint32_t)i : __ldcg(place + i));
+      }
     }
-    cluster.sync();  // the next pass reads what all blocks wrote; `total` may be written again
+    if (blocks > 1)
+      cluster.sync();  // the next pass reads what all blocks wrote; `total` may be written again
+    else
+      __syncthreads();
   }
+}
+
+// The first cluster sorts, the other blocks write zeros.
+template <class W, int N>
+__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) {
+  extern __shared__ uint32_t count[];  // [kSortWarps][digits]
+  const unsigned sorting = cg::this_cluster().num_blocks();
+  if (blockIdx.x < sorting)
+    sort_places(a, count);
+  else
+    fill_table<W, N>(a, blockIdx.x - sorting, gridDim.x - sorting);
+}
+
+template <class W, int N>
+__global__ void __launch_bounds__(kThreads) k_embed_fill(const EmbedArgs a) {
+  fill_table<W, N>(a, blockIdx.x, gridDim.x);
 }
 
 // The sums of one piece of sorted places over kSumThreads * N columns.
@@ -245,12 +314,17 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
   const int n = (int)(a.tokens - begin < kPiece ? a.tokens - begin : kPiece);
   const uint32_t* keys = a.keys[a.passes & 1];
   const uint32_t none = (uint32_t)a.vocab;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // sorted, and zeros written
   for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
     const int64_t at = begin + i - 1;
     key[i] = at >= 0 && at < a.tokens ? keys[at] : none;
     if (i >= 1 && i <= n) place[i - 1] = a.place[a.passes & 1][at];
   }
   __syncthreads();
+  if (blockIdx.y == 0 && threadIdx.x == 0) {  // a word that begins here and goes on
+    const uint32_t k = key[n];
+    if (k < none && key[n + 1] == k && (key[1] != k || key[0] != k)) a.shared[1 + atomicAdd(a.shared, 1u)] = blockIdx.x;
+  }
   const int64_t c0 = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * N;
   if (c0 >= a.dim) return;
   const T* DY = static_cast<const T*>(a.x) + c0;
@@ -258,51 +332,120 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
 #pragma unroll
   for (int e = 0; e < N; ++e) sum[e] = 0.f;
   int start = 1;
-  for (int i = 1; i <= n; ++i) {
-    const uint32_t k = key[i];
-    if (k >= none) break;  // sorted behind all words
-    float v[N];
-    if (bounds_ok(place[i - 1] < (uint64_t)a.tokens, a.status)) {
-      Elems<T, N>::load(DY + (int64_t)place[i - 1] * a.x_stride, v);
+  for (int i0 = 1; i0 <= n; i0 += kSumAtOnce) {
+    if (key[i0] >= none) break;  // sorted behind all words
+    typename Elems<T, N>::U v[kSumAtOnce];
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum[e] += v[e];
-    }
-    if (i < n && key[i + 1] == k) continue;
-    const bool from_before = start == 1 && key[0] == k, goes_on = i == n && key[n + 1] == k;
-    if (from_before || goes_on) {
-      float* part = a.part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * a.dim + c0;
-#pragma unroll
-      for (int e = 0; e < N; ++e) part[e] = sum[e];
-    } else {
-      W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c0;
-      float old[N];
-      if (a.accumulate) Elems<W, N>::load(to, old);
-#pragma unroll
-      for (int e = 0; e < N; ++e) sum[e] = a.accumulate ? old[e] + a.scale * sum[e] : a.scale * sum[e];
-      Elems<W, N>::store(to, sum);
+    for (int u = 0; u < kSumAtOnce; ++u) {
+      const int i = i0 + u;
+      v[u] = Elems<T, N>::zero();
+      if (i <= n && key[i] < none && bounds_ok(place[i - 1] < (uint64_t)a.tokens, a.status))
+        v[u] = Elems<T, N>::raw(DY + (int64_t)place[i - 1] * a.x_stride);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) sum[e] = 0.f;
-    start = i + 1;
+    for (int u = 0; u < kSumAtOnce; ++u) {
+      const int i = i0 + u;
+      const uint32_t k = i <= n ? key[i] : none;
+      if (k >= none) continue;
+      float w[N];
+      Elems<T, N>::widen(v[u], w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] += w[e];
+      if (i < n && key[i + 1] == k) continue;
+      const bool from_before = start == 1 && key[0] == k, goes_on = i == n && key[n + 1] == k;
+      if (from_before || goes_on) {
+        float* part = a.part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * a.dim + c0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) part[e] = sum[e];
+      } else {
+        W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c0;
+        float old[N];
+        if (a.accumulate) Elems<W, N>::load(to, old);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[e] = a.accumulate ? old[e] + a.scale * sum[e] : a.scale * sum[e];
+        Elems<W, N>::store(to, sum);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] = 0.f;
+      start = i + 1;
+    }
   }
 }
 
-// Words that several pieces share, from the piece in which they begin.
+// Words that several pieces share: the partial sums of the piece in which a word begins, and of those
+// after it.  A block takes kJoinWarps * kJoinCols columns of a word: of few partial sums a warp kJoinCols
+// columns alone, of many all warps a stretch of them each, added in order.
 template <class W>
-__global__ void __launch_bounds__(kSumThreads) k_embed_join(const EmbedArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) {
+  __shared__ float sums[kJoinWarps][kJoinCols];
   const uint32_t* keys = a.keys[a.passes & 1];
-  const int64_t begin = (int64_t)blockIdx.x * kPiece;
-  int64_t next = begin + kPiece;
-  if (next >= a.tokens) return;
-  const uint32_t k = keys[next];
-  if (k >= (uint32_t)a.vocab || keys[next - 1] != k || (begin > 0 && keys[begin - 1] == k)) return;
-  const int64_t c = (int64_t)blockIdx.y * kSumThreads + threadIdx.x;
-  if (c >= a.dim) return;
-  float sum = a.part[(2 * (int64_t)blockIdx.x + 1) * a.dim + c];
-  for (int64_t piece = blockIdx.x + 1; next < a.tokens && keys[next] == k; ++piece, next += kPiece)
-    sum += a.part[2 * piece * a.dim + c];
-  W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c;
-  *to = from_f32<W>(a.accumulate ? to_f32(*to) + a.scale * sum : a.scale * sum);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t pieces = (a.tokens + kPiece - 1) / kPiece;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
+  const uint32_t words = *a.shared;
+  for (uint32_t word = blockIdx.x; word < words; word += gridDim.x) {
+    const int64_t first = a.shared[1 + word];
+    const uint32_t k = keys[(first + 1) * kPiece];
+    // the last piece that begins with this word
+    int64_t lo = first + 1, hi = pieces - 1;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) / 2;
+      if (keys[mid * kPiece] == k) lo = mid;
+      else hi = mid - 1;
+    }
+    const int64_t n = lo - first;  // partial sums after the first
+    auto add = [&](int64_t from, int64_t to, int64_t c, float (&s)[4]) {  // pieces first + 1 + from ..
+      const float* p = a.part + 2 * (first + 1 + from) * a.dim + c;
+      for (int64_t i = from; i < to; i += kSumAtOnce, p += 2 * kSumAtOnce * a.dim) {
+        float v[kSumAtOnce][4];
+#pragma unroll
+        for (int u = 0; u < kSumAtOnce; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[u][e] = i + u < to && c + 32 * e < a.dim ? p[2 * u * a.dim + 32 * e] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kSumAtOnce; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] += v[u][e];
+      }
+    };
+    auto finish = [&](int64_t c, const float (&s)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (c + 32 * e >= a.dim) continue;
+        W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c + 32 * e;
+        *to = from_f32<W>(a.accumulate ? to_f32(*to) + a.scale * s[e] : a.scale * s[e]);
+      }
+    };
+    auto begin = [&](int64_t c, float (&s)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = c + 32 * e < a.dim ? a.part[(2 * first + 1) * a.dim + c + 32 * e] : 0.f;
+    };
+    const int64_t c0 = (int64_t)blockIdx.y * kJoinWarps * kJoinCols;
+    if (n <= 2 * kSumAtOnce) {
+      const int64_t c = c0 + warp * kJoinCols + lane;
+      float s[4];
+      begin(c, s);
+      add(0, n, c, s);
+      finish(c, s);
+    } else {
+      const int64_t each = (n + kJoinWarps - 1) / kJoinWarps;
+      for (int64_t c = c0 + lane; c - lane < a.dim && c - lane < c0 + kJoinWarps * kJoinCols; c += kJoinCols) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        if (warp == 0) begin(c, s);
+        add(warp * each, n < (warp + 1) * each ? n : (warp + 1) * each, c, s);
+        __syncthreads();  // the last columns' sums have been read
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[warp][lane + 32 * e] = s[e];
+        __syncthreads();
+        if (warp == 0) {
+          for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += sums[w][lane + 32 * e];
+          finish(c, s);
+        }
+      }
+    }
+  }
 }
 
 attn_status_t efail(attn_status_t s, const char* msg) {
@@ -327,7 +470,7 @@ attn_status_t check_params(const attn_embedding_params_t* p, bool backward) {
 }
 
 struct Layout {
-  size_t keys[2], place[2], part, total;
+  size_t keys[2], place[2], part, shared, total;
 };
 
 Layout layout_of(const attn_embedding_params_t* p) {
@@ -340,15 +483,18 @@ Layout layout_of(const attn_embedding_params_t* p) {
   };
   const size_t n = (size_t)p->tokens;
   for (int i = 0; i < 2; ++i) l.keys[i] = take(4 * n), l.place[i] = take(4 * n);
-  l.part = take((n + kPiece - 1) / kPiece * 2 * (size_t)p->dim * 4);
+  const size_t pieces = (n + kPiece - 1) / kPiece;
+  l.part = take(pieces * 2 * (size_t)p->dim * 4);
+  l.shared = take((1 + pieces) * 4);
   l.total = at;
   return l;
 }
 
-int64_t blocks_for(int64_t rows, int64_t units, int64_t most, EmbedArgs* a) {
-  const int64_t blocks = std::min((rows * units + kThreads - 1) / kThreads, most);  // below 2^51
-  a->row_step = blocks * kThreads / units, a->unit_step = blocks * kThreads % units;
-  return blocks;
+constexpr int kSms = 152;
+
+// The steps of a fill by `blocks` blocks of `threads`.
+void fill_steps(EmbedArgs* a, int64_t units, int64_t blocks, int threads) {
+  a->row_step = blocks * threads / units, a->unit_step = blocks * threads % units;
 }
 
 template <class T, int N>
@@ -360,38 +506,80 @@ void launch_lookup(const EmbedArgs& a, cudaStream_t st) {
 }
 
 template <class W, int N>
-void launch_fill(EmbedArgs a, int sms, cudaStream_t st) {
-  const int64_t blocks = blocks_for(a.vocab, a.dim / N, (int64_t)sms * 8, &a);
+void launch_fill(EmbedArgs a, cudaStream_t st) {
+  const int64_t units = a.dim / N;
+  const int64_t blocks = std::min<int64_t>((a.vocab * units + kThreads - 1) / kThreads, kSms * 8);  // below 2^51
+  fill_steps(&a, units, blocks, kThreads);
   k_embed_fill<W, N><<<(unsigned)blocks, kThreads, 0, st>>>(a);
 }
 
-template <class T, class W, int N>
-void launch_sums(const EmbedArgs& a, cudaStream_t st) {
-  const unsigned pieces = (unsigned)((a.tokens + kPiece - 1) / kPiece);
-  k_embed_sum<T, W, N><<<dim3(pieces, (unsigned)((a.dim + kSumThreads * N - 1) / (kSumThreads * N))), kSumThreads, 0,
-                         st>>>(a);
-  if (pieces > 1)
-    k_embed_join<W><<<dim3(pieces - 1, (unsigned)((a.dim + kSumThreads - 1) / kSumThreads)), kSumThreads, 0, st>>>(a);
+// A kernel that may be set up while the one before it runs.
+template <class K>
+cudaError_t launch_after(K kernel, dim3 grid, int threads, const EmbedArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-cudaError_t launch_sort(const EmbedArgs& a, cudaStream_t st) {
-  int blocks = 1;
-  while (blocks < kMaxCluster && (int64_t)blocks * kSortThreads < a.tokens) blocks *= 2;
+template <class T, class W, int N>
+cudaError_t launch_sums(const EmbedArgs& a, cudaStream_t st) {
+  const unsigned pieces = (unsigned)((a.tokens + kPiece - 1) / kPiece);
+  const unsigned stretches = (unsigned)((a.dim + kSumThreads * N - 1) / (kSumThreads * N));
+  const cudaError_t e = launch_after(k_embed_sum<T, W, N>, dim3(pieces, stretches), kSumThreads, a, st);
+  if (e != cudaSuccess || pieces == 1) return e;
+  const unsigned cols = kJoinWarps * kJoinCols, parts = (unsigned)((a.dim + cols - 1) / cols);
+  // a block or more on every SM; each takes one word after the other
+  const unsigned blocks = std::min<unsigned>(pieces - 1, std::max<unsigned>(1, 8 * kSms / parts));
+  return launch_after(k_embed_join<W>, dim3(blocks, parts), kJoinThreads, a, st);
+}
+
+template <class W, int N>
+cudaError_t launch_sort(EmbedArgs a, cudaStream_t st) {
+  int sorting = 1;
+  while (sorting < kMaxCluster && (int64_t)sorting * kSortThreads < a.tokens) sorting *= 2;
   const size_t smem = (size_t)kSortWarps * (sizeof(uint32_t) << a.bits);
-  cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_embed_sort<W, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(kSortWarps * (sizeof(uint32_t) << kMaxBits)));
   if (e != cudaSuccess) return e;
+  int64_t filling = 0;  // blocks, in whole clusters
+  if (!a.accumulate) {
+    const int64_t units = a.dim / N;
+    // many, because whole clusters do not fit on all SMs at once
+    filling = std::min<int64_t>((a.vocab * units + 4 * kSortThreads - 1) / (4 * kSortThreads), 8 * kSms);
+    filling = (filling + sorting - 1) / sorting * sorting;
+    fill_steps(&a, units, filling, kSortThreads);
+  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = dim3((unsigned)(sorting + filling));
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute cluster{};
   cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = blocks, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cluster.val.clusterDim.x = sorting, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_embed_sort, a);
+  return cudaLaunchKernelEx(&cfg, k_embed_sort<W, N>, a);
+}
+
+// launch(W{}, N) for the table's element type and its widest access.
+template <class F>
+cudaError_t for_table(bool bf16, int n, F launch) {
+  using std::integral_constant;
+  if (bf16) {
+    if (n == 8) return launch(__nv_bfloat16(), integral_constant<int, 8>());
+    if (n >= 2) return launch(__nv_bfloat16(), integral_constant<int, 2>());
+    return launch(__nv_bfloat16(), integral_constant<int, 1>());
+  }
+  if (n == 4) return launch(float(), integral_constant<int, 4>());
+  return launch(float(), integral_constant<int, 1>());
 }
 
 // Elements of one access: whole 16-byte vectors of the 2-byte type (8) or of the 4-byte type
@@ -474,18 +662,13 @@ attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* d
   a.padding = p->padding_id < 0 ? -1 : p->padding_id;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (!p->accumulate) {
-    const int n = width(at_w, p->dim, wsize);
-    if (wsize == 2) {
-      if (n == 8) launch_fill<__nv_bfloat16, 8>(a, sms, st);
-      else if (n >= 2) launch_fill<__nv_bfloat16, 2>(a, sms, st);
-      else launch_fill<__nv_bfloat16, 1>(a, sms, st);
-    } else {
-      if (n == 4) launch_fill<float, 4>(a, sms, st);
-      else launch_fill<float, 1>(a, sms, st);
-    }
-  }
-  if (p->tokens > 0) {
+  const int n_w = width(at_w, p->dim, wsize);
+  if (p->tokens == 0) {
+    e = for_table(wsize == 2, n_w, [&](auto w, auto n) {
+      launch_fill<decltype(w), decltype(n)::value>(a, st);
+      return cudaGetLastError();
+    });
+  } else {
     const Layout l = layout_of(p);
     char* ws = static_cast<char*>(workspace);
     for (int i = 0; i < 2; ++i) {
@@ -493,30 +676,28 @@ attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* d
       a.place[i] = reinterpret_cast<uint32_t*>(ws + l.place[i]);
     }
     a.part = reinterpret_cast<float*>(ws + l.part);
+    a.shared = reinterpret_cast<uint32_t*>(ws + l.shared);
     int bits = 1;  // of the largest key, vocab
     while (p->vocab >> bits) ++bits;
     a.passes = (bits + kMaxBits - 1) / kMaxBits;
     a.bits = (bits + a.passes - 1) / a.passes;
-    e = launch_sort(a, st);
+    e = for_table(wsize == 2, n_w, [&](auto w, auto n) { return launch_sort<decltype(w), decltype(n)::value>(a, st); });
     if (e != cudaSuccess) return efail(ATTN_ERR_CUDA, "sort launch failed");
     // one width for dy's elements and the table's: both addresses have to allow it
-    const int n = std::min(width(at_x, p->dim, esize), width(at_w, p->dim, wsize));
+    const int n = std::min(width(at_x, p->dim, esize), n_w);
     if (esize == 2 && wsize == 2) {
-      if (n == 8) launch_sums<__nv_bfloat16, __nv_bfloat16, 8>(a, st);
-      else if (n >= 2) launch_sums<__nv_bfloat16, __nv_bfloat16, 2>(a, st);
-      else launch_sums<__nv_bfloat16, __nv_bfloat16, 1>(a, st);
+      if (n == 8) e = launch_sums<__nv_bfloat16, __nv_bfloat16, 8>(a, st);
+      else if (n >= 2) e = launch_sums<__nv_bfloat16, __nv_bfloat16, 2>(a, st);
+      else e = launch_sums<__nv_bfloat16, __nv_bfloat16, 1>(a, st);
     } else if (esize == 2) {
-      if (n == 4) launch_sums<__nv_bfloat16, float, 4>(a, st);
-      else launch_sums<__nv_bfloat16, float, 1>(a, st);
+      e = n == 4 ? launch_sums<__nv_bfloat16, float, 4>(a, st) : launch_sums<__nv_bfloat16, float, 1>(a, st);
     } else if (wsize == 2) {
-      if (n == 4) launch_sums<float, __nv_bfloat16, 4>(a, st);
-      else launch_sums<float, __nv_bfloat16, 1>(a, st);
+      e = n == 4 ? launch_sums<float, __nv_bfloat16, 4>(a, st) : launch_sums<float, __nv_bfloat16, 1>(a, st);
     } else {
-      if (n == 4) launch_sums<float, float, 4>(a, st);
-      else launch_sums<float, float, 1>(a, st);
+      e = n == 4 ? launch_sums<float, float, 4>(a, st) : launch_sums<float, float, 1>(a, st);
     }
   }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : efail(ATTN_ERR_CUDA, "launch failed");
+  return e == cudaSuccess ? ATTN_OK : efail(ATTN_ERR_CUDA, "launch failed");
 }
 
 }  // extern "C"
