@@ -28,7 +28,8 @@ LIB_CHECKED = os.path.join(BUILD, "libgbattn_checked.so")
 
 SOURCES = ["api.cu", "sched.cu", "bwd_aux.cu", "simt_attn.cu", "tma_host.cu", "tc_fwd.cu", "tc_bwd.cu", "tc_dq.cu",
            "noalloc.cu", "ln.cu", "fp8.cu", "tc_bwd256.cu", "kv4.cu", "kv4_attn.cu", "kv4_tc.cu",
-           "ln_bwd.cu", "ln_bwd_bf16.cu", "ln_bwd_f32.cu", "dropout.cu", "embed.cu"]
+           "ln_bwd.cu", "ln_bwd_bf16.cu", "ln_bwd_f32.cu", "ln_drop_bf16.cu", "ln_drop_f32.cu",
+           "dropout.cu", "embed.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", CSRC, "-I", INCLUDE]

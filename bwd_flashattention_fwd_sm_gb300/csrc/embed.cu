@@ -35,15 +35,15 @@ constexpr int kThreads = 256;     // lookup, fill
 constexpr int kAtOnce = 4;        // vectors of a thread in flight
 constexpr int kPiece = 32;        // sorted places of one block of the gradient's sums
 constexpr int kSumThreads = 128;
-constexpr int kSumAtOnce = 8;     // rows of dy in flight
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 10;      // of one pass's digit: a thread a digit
-constexpr int kHeld = 8;          // places that a thread keeps in registers
+constexpr int kHeld = 8;          // places of a lane that stay in shared memory
 constexpr int kMaxCluster = 8;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinCols = 128;    // of a warp: four each lane
+constexpr int kJoinCols = 128;    // columns taken together: four each lane
+constexpr int kFew = 16;          // partial sums (after a word's first) that one warp adds
 constexpr int64_t kMaxDim = 1 << 20;
 
 // N neighbouring elements of T as one load or store, widened to float32.
@@ -94,13 +94,15 @@ struct EmbedArgs {
   int64_t tokens, vocab, dim;
   int64_t x_stride, y_stride;
   int64_t padding;
-  int64_t row_step, unit_step;  // fill: all threads' vectors on, as rows and vectors of a row
+  uint32_t row_step, unit_step;  // fill: all threads' vectors on, as rows and vectors of a row
   float scale;
   int ids_64, accumulate;
   uint32_t* keys[2];    // gradient: ids and places, before and after a pass
   uint32_t* place[2];
   float* part;          // [pieces][2][dim]: sums of words that began before the piece, that go on after it
-  uint32_t* shared;     // how many words several pieces share, and the pieces in which they begin (in any order)
+  // Words that several pieces share: how many of few partial sums and of many, and the pieces in which they
+  // begin (in any order): the few from the front of [pieces] numbers, the many from the back.
+  uint32_t* shared;
   int passes, bits;
   int* status;
 };
@@ -144,12 +146,12 @@ __global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a, int lanes
 // Zeros over the whole table, by `blocks` blocks of which this one is number `block`.
 template <class W, int N>
 __device__ __forceinline__ void fill_table(const EmbedArgs& a, int64_t block, int64_t blocks) {
-  const int64_t units = a.dim / N;
-  const int64_t at = block * blockDim.x + threadIdx.x;
-  int64_t row = at / units, unit = at % units;
+  const uint32_t units = (uint32_t)a.dim / N, at = (uint32_t)(block * blockDim.x + threadIdx.x);  // grids are small
+  uint32_t unit = at % units;
+  int64_t row = at / units;
   const float zero[N] = {};
   while (row < a.vocab) {
-    Elems<W, N>::store(static_cast<W*>(a.y) + row * a.y_stride + unit * N, zero);
+    Elems<W, N>::store(static_cast<W*>(a.y) + row * a.y_stride + (int64_t)unit * N, zero);
     row += a.row_step, unit += a.unit_step;
     if (unit >= units) unit -= units, ++row;
   }
@@ -169,76 +171,64 @@ __device__ __forceinline__ uint32_t key_at(const EmbedArgs& a, int64_t i) {
 // significant first.  Every warp of the cluster owns a stretch of the input.  It counts its
 // digits; the counts of all warps in front of it and of all lower digits say where its
 // first of each digit goes; then it takes its stretch in order, 32 at a time, and those
-// with equal digits find their order by a vote.  Ends in buffer passes % 2.  Up to kHeld * 32 places
-// of a warp stay in registers between the two (65536 tokens); longer stretches are read twice.
-// Bound by the latency of its steps: a pass takes about 4 us.
+// with equal digits find their order by a vote.  Ends in buffer passes % 2.  A warp's first kHeld * 32
+// places (65536 tokens of the cluster) stay in shared memory between the two; later ones are read twice.
+// Bound by the latency of its steps and by fetching its instructions, which run once or a
+// few times: loops stay rolled (a pass unrolled over a thread's places took 9 us, most of it fetches).
 __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
   __shared__ uint32_t total[1 << kMaxBits];
   __shared__ uint32_t warp_total[kSortWarps];
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned rank = cluster.block_rank(), blocks = cluster.num_blocks();
-  const int digits = 1 << a.bits;
-  const int64_t warps = (int64_t)blocks * kSortWarps;
-  const int64_t each = ((a.tokens + warps - 1) / warps + 31) / 32 * 32;
-  const int64_t begin = ((int64_t)rank * kSortWarps + warp) * each;
-  const int64_t end = begin + each < a.tokens ? begin + each : a.tokens;
-  const bool held = each <= kHeld * 32;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster.block_rank(), blocks = cluster.num_blocks();
+  const uint32_t digits = 1u << a.bits, tokens = (uint32_t)a.tokens;  // below 2^31
+  const uint32_t each = (tokens / (blocks * kSortWarps) / 32 + 1) * 32;
+  const uint32_t begin = min(tokens, (rank * kSortWarps + warp) * each), end = min(tokens, begin + each);
   uint32_t* mine = count + warp * digits;
-  if (rank == 0 && threadIdx.x == 0) *a.shared = 0;
+  uint32_t* held_key = count + kSortWarps * digits + warp * kHeld * 32;
+  uint32_t* held_place = held_key + kSortWarps * kHeld * 32;
+  if (rank == 0 && threadIdx.x < 2) a.shared[threadIdx.x] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
     const uint32_t* keys = a.keys[pass & 1];
     const uint32_t* place = a.place[pass & 1];
     uint32_t* keys_to = a.keys[(pass + 1) & 1];
     uint32_t* place_to = a.place[(pass + 1) & 1];
-    uint32_t key[kHeld], from[kHeld];
-    if (held) {
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) {
-        const int64_t i = begin + j * 32 + lane;
-        key[j] = from[j] = 0;
-        if (i < end) {
-          key[j] = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
-          from[j] = pass == 0 ? (uint32_t)i : __ldcg(place + i);
-        }
-      }
-    }
-    for (int d = lane; d < digits; d += 32) mine[d] = 0;
+#pragma unroll 1
+    for (uint32_t d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
-    if (held) {
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j)
-        if (begin + j * 32 + lane < end) atomicAdd(&mine[(key[j] >> shift) & (digits - 1)], 1u);
-    } else {
-      for (int64_t i = begin + lane; i < end; i += 32) {
-        const uint32_t k = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
-        atomicAdd(&mine[(k >> shift) & (digits - 1)], 1u);
-      }
+#pragma unroll 4
+    for (uint32_t i = begin + lane; i < end; i += 32) {
+      const uint32_t k = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
+      const uint32_t f = pass == 0 ? i : __ldcg(place + i);
+      atomicAdd(&mine[(k >> shift) & (digits - 1)], 1u);
+      if (i - begin < kHeld * 32) held_key[i - begin] = k, held_place[i - begin] = f;
     }
     __syncthreads();
-    uint32_t counts[kSortWarps], sum = 0;  // of this thread's digit
-    if ((int)threadIdx.x < digits) {
-#pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) counts[w] = count[w * digits + threadIdx.x];
-#pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) sum += counts[w];
+    uint32_t sum = 0;  // of this thread's digit; counts become those of the warps in front
+    if (threadIdx.x < digits) {
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = count[w * digits + threadIdx.x];
+        count[w * digits + threadIdx.x] = sum;
+        sum += n;
+      }
       total[threadIdx.x] = sum;
     }
     if (blocks > 1) cluster.sync();
     uint32_t all = sum, before = 0;
-    if (blocks > 1 && (int)threadIdx.x < digits) {
+    if (blocks > 1 && threadIdx.x < digits) {
       uint32_t n[kMaxCluster];
 #pragma unroll
-      for (unsigned r = 0; r < kMaxCluster; ++r) n[r] = r < blocks ? cluster.map_shared_rank(total, r)[threadIdx.x] : 0;
+      for (uint32_t r = 0; r < kMaxCluster; ++r) n[r] = r < blocks ? cluster.map_shared_rank(total, r)[threadIdx.x] : 0;
       all = 0;
 #pragma unroll
-      for (unsigned r = 0; r < kMaxCluster; ++r) {
+      for (uint32_t r = 0; r < kMaxCluster; ++r) {
         all += n[r];
         if (r < rank) before += n[r];
       }
     }
-    uint32_t upto = all;  // inclusive over the digits
+    uint32_t upto = all;  // inclusive over the digits of a warp, then of the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t n = __shfl_up_sync(0xffffffffu, upto, o);
@@ -246,23 +236,26 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
     }
     if (lane == 31) warp_total[warp] = upto;
     __syncthreads();
-    if ((int)threadIdx.x < digits) {
-      uint32_t start = before + upto - all;
-      for (int w = 0; w < warp; ++w) start += warp_total[w];
-#pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) {
-        count[w * digits + threadIdx.x] = start;
-        start += counts[w];
-      }
+    uint32_t in_front = lane < warp ? warp_total[lane] : 0;
+    in_front = __reduce_add_sync(0xffffffffu, in_front);
+    if (threadIdx.x < digits) {
+      const uint32_t start = in_front + before + upto - all;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) count[w * digits + threadIdx.x] += start;
     }
     __syncthreads();
-    auto put = [&](bool there, uint32_t k, uint32_t f) {  // the whole warp
-      const unsigned active = __ballot_sync(0xffffffffu, there);
-      if (there) {
+#pragma unroll 1
+    for (uint32_t i0 = begin; i0 < end; i0 += 32) {
+      const uint32_t i = i0 + lane, at = i - begin;
+      const unsigned active = __ballot_sync(0xffffffffu, i < end);
+      if (i < end) {
+        const bool held = at < kHeld * 32;
+        const uint32_t k = held ? held_key[at] : pass == 0 ? key_at(a, i) : __ldcg(keys + i);
+        const uint32_t f = held ? held_place[at] : pass == 0 ? i : __ldcg(place + i);
         const uint32_t d = (k >> shift) & (digits - 1);
         const unsigned same = __match_any_sync(active, d);
         const uint32_t to = mine[d] + __popc(same & ((1u << lane) - 1));
-        if (bounds_ok(to < (uint64_t)a.tokens, a.status)) {
+        if (bounds_ok(to < tokens, a.status)) {
           keys_to[to] = k;
           place_to[to] = f;
         }
@@ -270,17 +263,6 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
         if (lane == __ffs(same) - 1) mine[d] += __popc(same);
       }
       __syncwarp();
-    };
-    if (held) {
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j)
-        if (begin + j * 32 < end) put(begin + j * 32 + lane < end, key[j], from[j]);
-    } else {
-      for (int64_t i = begin + lane; i - lane < end; i += 32) {
-        const bool there = i < end;
-        put(there, !there ? 0 : pass == 0 ? key_at(a, i) : __ldcg(keys + i),
-            !there || pass == 0 ? (uint32_t)i : __ldcg(place + i));
-      }
     }
     if (blocks > 1)
       cluster.sync();  // the next pass reads what all blocks wrote; `total` may be written again
@@ -292,8 +274,9 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
 // The first cluster sorts, the other blocks write zeros.
 template <class W, int N>
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) {
-  extern __shared__ uint32_t count[];  // [kSortWarps][digits]
+  extern __shared__ uint32_t count[];  // [kSortWarps][digits], and twice [kSortWarps][kHeld * 32]
   const unsigned sorting = cg::this_cluster().num_blocks();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x < sorting)
     sort_places(a, count);
   else
@@ -305,146 +288,172 @@ __global__ void __launch_bounds__(kThreads) k_embed_fill(const EmbedArgs a) {
   fill_table<W, N>(a, blockIdx.x, gridDim.x);
 }
 
-// The sums of one piece of sorted places over kSumThreads * N columns.
-template <class T, class W, int N>
+// The sums of one piece of sorted places over kSumThreads * N * kLoads columns: kLoads accesses of N
+// columns a thread, kRows rows of dy in flight.
+template <class T, class W, int N, int kLoads, int kRows>
 __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
   __shared__ uint32_t key[kPiece + 2];  // with the neighbours on both sides
   __shared__ uint32_t place[kPiece];
-  const int64_t begin = (int64_t)blockIdx.x * kPiece;
-  const int n = (int)(a.tokens - begin < kPiece ? a.tokens - begin : kPiece);
+  const uint32_t begin = blockIdx.x * kPiece, tokens = (uint32_t)a.tokens;
+  const int n = (int)min(tokens - begin, (uint32_t)kPiece);
   const uint32_t* keys = a.keys[a.passes & 1];
   const uint32_t none = (uint32_t)a.vocab;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // sorted, and zeros written
-  for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
-    const int64_t at = begin + i - 1;
-    key[i] = at >= 0 && at < a.tokens ? keys[at] : none;
-    if (i >= 1 && i <= n) place[i - 1] = a.place[a.passes & 1][at];
+  if ((int)threadIdx.x < n + 2) {
+    const uint32_t at = begin + threadIdx.x - 1;  // wraps in front of the first
+    key[threadIdx.x] = at < tokens ? keys[at] : none;
+    if (threadIdx.x >= 1 && (int)threadIdx.x <= n) place[threadIdx.x - 1] = a.place[a.passes & 1][at];
   }
   __syncthreads();
   if (blockIdx.y == 0 && threadIdx.x == 0) {  // a word that begins here and goes on
     const uint32_t k = key[n];
-    if (k < none && key[n + 1] == k && (key[1] != k || key[0] != k)) a.shared[1 + atomicAdd(a.shared, 1u)] = blockIdx.x;
+    if (k < none && key[n + 1] == k && (key[1] != k || key[0] != k)) {
+      const uint64_t far = (uint64_t)begin + (kFew + 1) * kPiece;
+      const bool many = far < tokens && keys[far] == k;
+      const uint32_t at = atomicAdd(a.shared + many, 1u);
+      a.shared[2 + (many ? gridDim.x - 1 - at : at)] = blockIdx.x;
+    }
   }
-  const int64_t c0 = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * N;
-  if (c0 >= a.dim) return;
+  constexpr int kApart = kSumThreads * N;  // columns between a thread's accesses
+  const int dim = (int)a.dim, c0 = blockIdx.y * kApart * kLoads + threadIdx.x * N;
+  if (c0 >= dim) return;
   const T* DY = static_cast<const T*>(a.x) + c0;
-  float sum[N];
+  float sum[kLoads][N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) sum[e] = 0.f;
-  int start = 1;
-  for (int i0 = 1; i0 <= n; i0 += kSumAtOnce) {
+  for (int l = 0; l < kLoads; ++l)
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[l][e] = 0.f;
+  bool from_before = key[0] == key[1];
+#pragma unroll 1
+  for (int i0 = 1; i0 <= n; i0 += kRows) {
     if (key[i0] >= none) break;  // sorted behind all words
-    typename Elems<T, N>::U v[kSumAtOnce];
+    typename Elems<T, N>::U v[kRows][kLoads];
 #pragma unroll
-    for (int u = 0; u < kSumAtOnce; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       const int i = i0 + u;
-      v[u] = Elems<T, N>::zero();
-      if (i <= n && key[i] < none && bounds_ok(place[i - 1] < (uint64_t)a.tokens, a.status))
-        v[u] = Elems<T, N>::raw(DY + (int64_t)place[i - 1] * a.x_stride);
+      const bool there = i <= n && key[i] < none && bounds_ok(place[i - 1] < (uint64_t)a.tokens, a.status);
+      const T* row = DY + (there ? (int64_t)place[i - 1] * a.x_stride : 0);
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        v[u][l] = Elems<T, N>::zero();
+        if (there && c0 + l * kApart < dim) v[u][l] = Elems<T, N>::raw(row + l * kApart);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < kSumAtOnce; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       const int i = i0 + u;
       const uint32_t k = i <= n ? key[i] : none;
       if (k >= none) continue;
-      float w[N];
-      Elems<T, N>::widen(v[u], w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum[e] += w[e];
-      if (i < n && key[i + 1] == k) continue;
-      const bool from_before = start == 1 && key[0] == k, goes_on = i == n && key[n + 1] == k;
-      if (from_before || goes_on) {
-        float* part = a.part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * a.dim + c0;
+      for (int l = 0; l < kLoads; ++l) {
+        float w[N];
+        Elems<T, N>::widen(v[u][l], w);
 #pragma unroll
-        for (int e = 0; e < N; ++e) part[e] = sum[e];
-      } else {
-        W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c0;
-        float old[N];
-        if (a.accumulate) Elems<W, N>::load(to, old);
-#pragma unroll
-        for (int e = 0; e < N; ++e) sum[e] = a.accumulate ? old[e] + a.scale * sum[e] : a.scale * sum[e];
-        Elems<W, N>::store(to, sum);
+        for (int e = 0; e < N; ++e) sum[l][e] += w[e];
       }
+      const bool goes_on = key[i + 1] == k;
+      if (goes_on && i < n) continue;
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum[e] = 0.f;
-      start = i + 1;
+      for (int l = 0; l < kLoads; ++l) {
+        if (c0 + l * kApart >= dim) continue;
+        if (from_before || goes_on) {
+          float* part = a.part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * dim + c0 + l * kApart;
+#pragma unroll
+          for (int e = 0; e < N; ++e) part[e] = sum[l][e];
+        } else {
+          W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c0 + l * kApart;
+          float old[N];
+          if (a.accumulate) Elems<W, N>::load(to, old);
+#pragma unroll
+          for (int e = 0; e < N; ++e) sum[l][e] = a.accumulate ? old[e] + a.scale * sum[l][e] : a.scale * sum[l][e];
+          Elems<W, N>::store(to, sum[l]);
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[l][e] = 0.f;
+      }
+      from_before = false;
     }
   }
 }
 
 // Words that several pieces share: the partial sums of the piece in which a word begins, and of those
-// after it.  A block takes kJoinWarps * kJoinCols columns of a word: of few partial sums a warp kJoinCols
-// columns alone, of many all warps a stretch of them each, added in order.
+// after it.  Few: a warp adds kJoinCols columns of them in order.  Many: a block does, each warp a
+// stretch of them, and then the warps' sums in order.
 template <class W>
 __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) {
   __shared__ float sums[kJoinWarps][kJoinCols];
   const uint32_t* keys = a.keys[a.passes & 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t pieces = (a.tokens + kPiece - 1) / kPiece;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tokens = (uint32_t)a.tokens;
+  const uint32_t dim = (uint32_t)a.dim, groups = (dim + kJoinCols - 1) / kJoinCols;
+  const uint32_t pieces = (tokens + kPiece - 1) / kPiece;
+  // partial sums `from` .. `to` - 1 after the first of the word that begins in piece `first`
+  auto add = [&](uint32_t first, uint32_t from, uint32_t to, uint32_t col, float (&s)[4]) {
+    const float* p = a.part + 2 * (int64_t)(first + 1 + from) * dim + col;
+#pragma unroll 1
+    for (uint32_t i = from; i < to; i += 4, p += 8 * (int64_t)dim) {
+      float v[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[u][e] = i + u < to && col + 32 * e < dim ? p[2 * u * (int64_t)dim + 32 * e] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[u][e];
+    }
+  };
+  auto begin = [&](uint32_t first, uint32_t col, float (&s)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = col + 32 * e < dim ? a.part[(2 * (int64_t)first + 1) * dim + col + 32 * e] : 0.f;
+  };
+  auto finish = [&](uint32_t k, uint32_t col, const float (&s)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (col + 32 * e >= dim) continue;
+      W* out = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + col + 32 * e;
+      *out = from_f32<W>(a.accumulate ? to_f32(*out) + a.scale * s[e] : a.scale * s[e]);
+    }
+  };
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
-  const uint32_t words = *a.shared;
-  for (uint32_t word = blockIdx.x; word < words; word += gridDim.x) {
-    const int64_t first = a.shared[1 + word];
+  const uint64_t few = (uint64_t)a.shared[0] * groups, many = (uint64_t)a.shared[1] * groups;
+#pragma unroll 1
+  for (uint64_t i = (uint64_t)blockIdx.x * kJoinWarps + warp; i < few; i += (uint64_t)gridDim.x * kJoinWarps) {
+    const uint32_t first = a.shared[2 + i / groups], col = (uint32_t)(i % groups) * kJoinCols + lane;
+    const uint32_t at = (first + 1 + lane) * kPiece;  // below 2^32: tokens is below 2^31
+    float s[4];
+    begin(first, col, s);
     const uint32_t k = keys[(first + 1) * kPiece];
-    // the last piece that begins with this word
-    int64_t lo = first + 1, hi = pieces - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) / 2;
-      if (keys[mid * kPiece] == k) lo = mid;
-      else hi = mid - 1;
+    // sorted: the pieces that begin with this word are the next ones
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, at < tokens && keys[at] == k));
+    add(first, 0, n, col, s);
+    finish(k, col, s);
+  }
+#pragma unroll 1
+  for (uint64_t i = blockIdx.x; i < many; i += gridDim.x) {
+    const uint32_t first = a.shared[2 + pieces - 1 - i / groups], col = (uint32_t)(i % groups) * kJoinCols + lane;
+    const uint32_t k = keys[(first + 1) * kPiece];
+    uint32_t n = 0, found;
+    do {
+      const uint64_t at = ((uint64_t)first + 1 + n + threadIdx.x) * kPiece;
+      found = __syncthreads_count(at < tokens && keys[at] == k);
+      n += found;
+    } while (found == kJoinThreads);
+    const uint32_t each = (n + kJoinWarps - 1) / kJoinWarps, from = min(n, warp * each);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (warp == 0) begin(first, col, s);
+    add(first, from, min(n, from + each), col, s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[warp][lane + 32 * e] = s[e];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll 1
+      for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += sums[w][lane + 32 * e];
+      finish(k, col, s);
     }
-    const int64_t n = lo - first;  // partial sums after the first
-    auto add = [&](int64_t from, int64_t to, int64_t c, float (&s)[4]) {  // pieces first + 1 + from ..
-      const float* p = a.part + 2 * (first + 1 + from) * a.dim + c;
-      for (int64_t i = from; i < to; i += kSumAtOnce, p += 2 * kSumAtOnce * a.dim) {
-        float v[kSumAtOnce][4];
-#pragma unroll
-        for (int u = 0; u < kSumAtOnce; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[u][e] = i + u < to && c + 32 * e < a.dim ? p[2 * u * a.dim + 32 * e] : 0.f;
-#pragma unroll
-        for (int u = 0; u < kSumAtOnce; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[e] += v[u][e];
-      }
-    };
-    auto finish = [&](int64_t c, const float (&s)[4]) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (c + 32 * e >= a.dim) continue;
-        W* to = static_cast<W*>(a.y) + (int64_t)k * a.y_stride + c + 32 * e;
-        *to = from_f32<W>(a.accumulate ? to_f32(*to) + a.scale * s[e] : a.scale * s[e]);
-      }
-    };
-    auto begin = [&](int64_t c, float (&s)[4]) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = c + 32 * e < a.dim ? a.part[(2 * first + 1) * a.dim + c + 32 * e] : 0.f;
-    };
-    const int64_t c0 = (int64_t)blockIdx.y * kJoinWarps * kJoinCols;
-    if (n <= 2 * kSumAtOnce) {
-      const int64_t c = c0 + warp * kJoinCols + lane;
-      float s[4];
-      begin(c, s);
-      add(0, n, c, s);
-      finish(c, s);
-    } else {
-      const int64_t each = (n + kJoinWarps - 1) / kJoinWarps;
-      for (int64_t c = c0 + lane; c - lane < a.dim && c - lane < c0 + kJoinWarps * kJoinCols; c += kJoinCols) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        if (warp == 0) begin(c, s);
-        add(warp * each, n < (warp + 1) * each ? n : (warp + 1) * each, c, s);
-        __syncthreads();  // the last columns' sums have been read
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sums[warp][lane + 32 * e] = s[e];
-        __syncthreads();
-        if (warp == 0) {
-          for (int w = 1; w < kJoinWarps; ++w)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += sums[w][lane + 32 * e];
-          finish(c, s);
-        }
-      }
-    }
+    __syncthreads();  // sums may be written again
   }
 }
 
@@ -485,7 +494,7 @@ Layout layout_of(const attn_embedding_params_t* p) {
   for (int i = 0; i < 2; ++i) l.keys[i] = take(4 * n), l.place[i] = take(4 * n);
   const size_t pieces = (n + kPiece - 1) / kPiece;
   l.part = take(pieces * 2 * (size_t)p->dim * 4);
-  l.shared = take((1 + pieces) * 4);
+  l.shared = take((2 + pieces) * 4);
   l.total = at;
   return l;
 }
@@ -494,7 +503,7 @@ constexpr int kSms = 152;
 
 // The steps of a fill by `blocks` blocks of `threads`.
 void fill_steps(EmbedArgs* a, int64_t units, int64_t blocks, int threads) {
-  a->row_step = blocks * threads / units, a->unit_step = blocks * threads % units;
+  a->row_step = (uint32_t)(blocks * threads / units), a->unit_step = (uint32_t)(blocks * threads % units);
 }
 
 template <class T, int N>
@@ -530,23 +539,26 @@ cudaError_t launch_after(K kernel, dim3 grid, int threads, const EmbedArgs& a, c
 
 template <class T, class W, int N>
 cudaError_t launch_sums(const EmbedArgs& a, cudaStream_t st) {
+  // narrow accesses: several a thread, which share the work of finding a word's end
+  constexpr int kLoads = sizeof(T) * N >= 8 ? 1 : 4, kRows = kLoads == 1 ? 8 : 4;
   const unsigned pieces = (unsigned)((a.tokens + kPiece - 1) / kPiece);
-  const unsigned stretches = (unsigned)((a.dim + kSumThreads * N - 1) / (kSumThreads * N));
-  const cudaError_t e = launch_after(k_embed_sum<T, W, N>, dim3(pieces, stretches), kSumThreads, a, st);
+  const unsigned stretches = (unsigned)((a.dim + kSumThreads * N * kLoads - 1) / (kSumThreads * N * kLoads));
+  const cudaError_t e = launch_after(k_embed_sum<T, W, N, kLoads, kRows>, dim3(pieces, stretches), kSumThreads, a, st);
   if (e != cudaSuccess || pieces == 1) return e;
-  const unsigned cols = kJoinWarps * kJoinCols, parts = (unsigned)((a.dim + cols - 1) / cols);
-  // a block or more on every SM; each takes one word after the other
-  const unsigned blocks = std::min<unsigned>(pieces - 1, std::max<unsigned>(1, 8 * kSms / parts));
-  return launch_after(k_embed_join<W>, dim3(blocks, parts), kJoinThreads, a, st);
+  // what there is to join only the device knows: at most a word in every second piece
+  const int64_t warps = (int64_t)((pieces + 1) / 2) * ((a.dim + kJoinCols - 1) / kJoinCols);
+  const unsigned blocks = (unsigned)std::min<int64_t>((warps + kJoinWarps - 1) / kJoinWarps, 4 * kSms);
+  return launch_after(k_embed_join<W>, dim3(blocks), kJoinThreads, a, st);
 }
 
 template <class W, int N>
 cudaError_t launch_sort(EmbedArgs a, cudaStream_t st) {
   int sorting = 1;
   while (sorting < kMaxCluster && (int64_t)sorting * kSortThreads < a.tokens) sorting *= 2;
-  const size_t smem = (size_t)kSortWarps * (sizeof(uint32_t) << a.bits);
+  auto shared_bytes = [](int bits) { return kSortWarps * sizeof(uint32_t) * ((1u << bits) + 2 * kHeld * 32); };
+  const size_t smem = shared_bytes(a.bits);
   cudaError_t e = cudaFuncSetAttribute(k_embed_sort<W, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(kSortWarps * (sizeof(uint32_t) << kMaxBits)));
+                                       (int)shared_bytes(kMaxBits));
   if (e != cudaSuccess) return e;
   int64_t filling = 0;  // blocks, in whole clusters
   if (!a.accumulate) {

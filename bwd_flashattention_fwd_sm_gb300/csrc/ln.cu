@@ -28,6 +28,7 @@
 #include "../../include/gbln.h"
 #include "common.cuh"
 #include "dropout.cuh"
+#include "ln_drop.cuh"
 #include "ptx.cuh"
 #include "rowvec.cuh"
 
@@ -36,6 +37,10 @@
 namespace gbattn {
 void set_last_error_text(const char* text);
 attn_status_t device_status(int** status, int* sms, unsigned long long* wait_ns);
+
+extern template bool launch_ln_drop<__nv_bfloat16>(const LnDropArgs&, bool, int*, unsigned long long, cudaStream_t,
+                                                   cudaError_t*);
+extern template bool launch_ln_drop<float>(const LnDropArgs&, bool, int*, unsigned long long, cudaStream_t, cudaError_t*);
 }
 
 namespace gbattn {
@@ -161,6 +166,7 @@ __device__ __forceinline__ void affine(const LnArgs& a, int64_t c0, int64_t cols
   }
 }
 
+// kDrop: x goes through the dropout; for rows that k_ln_drop does not take (ln_drop.cuh).
 // kVpt: 16-byte vectors per thread (cols <= 256 * kVpt * E).  Short rows leave
 // registers to spare: several CTAs per SM then keep more loads in flight.
 template <class T, int kVpt, bool kDrop>
@@ -326,7 +332,7 @@ constexpr int kMaxStages = 8;
 template <int kVpt>
 constexpr int ring_ctas() { return kVpt <= 2 ? 4 : (kVpt == 4 ? 2 : 1); }
 
-template <class T, int kVpt, bool kDrop>
+template <class T, int kVpt>
 __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const LnArgs a, int stages, uint32_t row_bytes,
                                                            int* status, unsigned long long wait_ns) {
   constexpr int E = Vec<T>::E;
@@ -363,9 +369,6 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
     }
   T* Y = static_cast<T*>(a.y);
   T* H = static_cast<T*>(a.h);
-  DropKey key{};
-  DropRate rate{};
-  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
   int64_t it = 0;
   bool ok = true;
   for (int64_t row = blockIdx.x; row < a.p.rows; row += gridDim.x, ++it) {
@@ -383,14 +386,7 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
       const int64_t vi = tid + (int64_t)j * kThreadsLn;
       sv[j] = Stats{0.f, 0.f, 0.f};
       if (vi < nvec) {
-        if constexpr (kDrop) {
-          const uint4 raw = reinterpret_cast<const uint4*>(xsm)[vi];
-          Vec<T>::unpack(drop_mask<T>(raw, (uint32_t)(vi * E), (uint32_t)row, key, rate), v[j]);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] *= rate.factor;
-        } else {
-          Vec<T>::load(reinterpret_cast<const T*>(xsm) + vi * E, v[j]);
-        }
+        Vec<T>::load(reinterpret_cast<const T*>(xsm) + vi * E, v[j]);
         if (has_r) {
           float t[E];
           Vec<T>::load(reinterpret_cast<const T*>(xsm + row_bytes) + vi * E, t);
@@ -463,7 +459,7 @@ cudaError_t launch_ln(const LnArgs& a, int sms, int* status, unsigned long long 
   // bf16 or 2048 float32 columns and below) go through registers: on [16384,
   // 4096] bf16 the register path with its loads issued first and division-free
   // statistics measured 5.03-5.08 TB/s against 4.66-4.75 for the ring
-  if (a.vec && a.p.cols % E == 0 && stages >= 2 && per > 2 && per <= 8) {
+  if (!kDrop && a.vec && a.p.cols % E == 0 && stages >= 2 && per > 2 && per <= 8) {
     auto launch = [&](auto kernel) -> cudaError_t {
       const size_t smem = (size_t)stages * stage_bytes;
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -476,10 +472,10 @@ cudaError_t launch_ln(const LnArgs& a, int sms, int* status, unsigned long long 
       kernel<<<grid, kThreadsLn, smem, st>>>(a, stages, row_bytes, status, wait_ns);
       return cudaGetLastError();
     };
-    if (per <= 1) return launch(k_ln_ring<T, 1, kDrop>);
-    if (per <= 2) return launch(k_ln_ring<T, 2, kDrop>);
-    if (per <= 4) return launch(k_ln_ring<T, 4, kDrop>);
-    return launch(k_ln_ring<T, 8, kDrop>);
+    if (per <= 1) return launch(k_ln_ring<T, 1>);
+    if (per <= 2) return launch(k_ln_ring<T, 2>);
+    if (per <= 4) return launch(k_ln_ring<T, 4>);
+    return launch(k_ln_ring<T, 8>);
   }
   if (per <= 1) return launch_ln_v<T, 1, kDrop>(a, sms, st);
   if (per <= 2) return launch_ln_v<T, 2, kDrop>(a, sms, st);
@@ -544,6 +540,19 @@ extern "C" attn_status_t ln_dropout_residual_fwd(const ln_params_t* p, const ln_
   a.vec = vec ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  if (drops) {  // one pass over the ring, where all tensors' rows begin at the same place within 16 bytes
+    const bool whole = vec && p->cols % per_vec == 0;
+    auto alike = [&](const void* q, int64_t stride) {
+      return !q || (!off(reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(q) ^ reinterpret_cast<uintptr_t>(x)), 15) &&
+                    stride == p->x_stride);
+    };
+    if (whole || (alike(residual, p->r_stride) && alike(y, p->y_stride) && alike(h, p->h_stride))) {
+      const LnDropArgs d{*p, x, residual, gamma, beta, y, h, mean, rstd, a.drop};
+      const bool taken = p->dtype == ATTN_BF16 ? launch_ln_drop<__nv_bfloat16>(d, !whole, status, wait_ns, st, &e)
+                                               : launch_ln_drop<float>(d, !whole, status, wait_ns, st, &e);
+      if (taken) return e == cudaSuccess ? ATTN_OK : ln_fail(ATTN_ERR_CUDA, "ln_residual_fwd: launch failed");
+    }
+  }
   if (p->dtype == ATTN_BF16)
     e = drops ? launch_ln<__nv_bfloat16, true>(a, sms, status, wait_ns, st)
               : launch_ln<__nv_bfloat16, false>(a, sms, status, wait_ns, st);

@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "dropout.cuh"
 #include "ptx.cuh"
+#include "row_group.cuh"
 #include "rowvec.cuh"
 
 namespace gbattn {
@@ -195,6 +196,7 @@ template <class T, int kRow, int kRows, bool kDrop, bool kRagged>
 __global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
   constexpr int E = Vec<T>::E, P = E / 2;
   extern __shared__ float column[];  // [2][cols]
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % kRow, groups = blockDim.x / kRow;
   const int cols = (int)a.p.cols;
   const float inv = 1.f / (float)cols;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int o = kRow; o <= 16; o *= 2) {
+        for (int o = kRow; o < 32; o *= 2) {
           sg[i].x += __shfl_xor_sync(0xffffffffu, sg[i].x, o);
           sg[i].y += __shfl_xor_sync(0xffffffffu, sg[i].y, o);
           sb[i].x += __shfl_xor_sync(0xffffffffu, sb[i].x, o);
@@ -375,28 +377,6 @@ __global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
 // then for dr), which leaves the registers to the columns' sums.  Waits are bounded: a
 // group that gives up records ATTN_ERR_DEVICE_TIMEOUT, waits (bounded) for its own copies and
 // stops, and its block leaves no partial sums.
-constexpr int kMaxStages = 8;
-
-template <int kRow, int kGroups>
-__device__ __forceinline__ bool group_any(int group, bool x) {
-  if constexpr (kRow == 32) {
-    return __any_sync(0xffffffffu, x);
-  } else if constexpr (kGroups == 1) {
-    return __syncthreads_or(x);
-  } else {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(1 + group), "n"(kRow)
-        : "memory");
-    return r != 0;
-  }
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -430,6 +410,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   __shared__ __align__(16) float sums_all[kGroups][2][2][kParts];
   __shared__ ptx::Abort abort;
   const int group = threadIdx.x / kRow, tid = threadIdx.x % kRow, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int groups = blockDim.x / kRow;  // kGroups, or fewer where there are few rows
   uint64_t* full = full_all[group];
   const uint32_t rank = kCluster > 1 ? cluster_rank() : 0;
@@ -465,8 +446,8 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   // The vectors at the two ends, by elements: of which element this thread moves, the address in the
   // first row and the place in a stage (negative: none).  Places that are no columns get 0 in dy
   // (address NULL) and a column's value in h, so that they add nothing to any sum.
-  const T* edge_from[kEdge];
-  int edge_to[kEdge];
+  const T* edge_from[kEdge] = {};
+  int edge_to[kEdge] = {};
   if constexpr (kRagged) {
 #pragma unroll
     for (int k = 0; k < kEdge; ++k) {

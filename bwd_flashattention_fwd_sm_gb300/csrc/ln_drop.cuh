@@ -1,0 +1,316 @@
+// Dropout, residual add and LayerNorm in one pass (include/gbln.h has the formulas), for one element
+// type; ln.cu has the entry, and the form without dropout.
+//
+// A row belongs to a group of kRow threads, kVpt vectors each, and a block holds kGroups such
+// groups.  Rows stream through a ring of stages in shared memory that bulk copies fill some rows
+// ahead.  h is made once and stays in registers; its mean and then the sum of its squared
+// distances from that mean are two sums over the group, so nothing cancels.  Bound by device memory
+// at long rows; the mask (some 60 instructions for eight elements) and the two barriers a row are next.
+// Rows that are no whole vectors are moved as shifted aligned vectors, as in the backward pass
+// (ln_bwd.cuh), where the rows of all tensors begin at the same place within 16 bytes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gbln.h"
+#include "common.cuh"
+#include "dropout.cuh"
+#include "ptx.cuh"
+#include "row_group.cuh"
+#include "rowvec.cuh"
+
+namespace gbattn {
+
+struct LnDropArgs {
+  ln_params_t p;
+  const void* x;
+  const void* r;
+  const float* gamma;
+  const float* beta;
+  void* y;
+  void* h;
+  float* mean;
+  float* rstd;
+  DropArgs drop;
+};
+
+// Launches the kernel; false: it does not take rows of this length (nothing was launched).
+template <class T>
+bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
+                    cudaError_t* error);
+
+namespace {
+
+template <class T, int kRow, int kGroups, int kVpt, int kBlocks, bool kRagged>
+__global__ void __launch_bounds__(kRow* kGroups, kBlocks)
+    k_ln_drop(const LnDropArgs a, int stages, int slots, int* status, unsigned long long wait_ns) {
+  constexpr int E = Vec<T>::E, P = E / 2, kWarps = kRow / 32;
+  constexpr bool kKeep = kVpt * E <= 16;            // gamma and beta in registers
+  constexpr int kEdge = (4 * E + kRow - 1) / kRow;  // elements at a row's ends, of one thread
+  extern __shared__ __align__(128) uint8_t ring[];  // [groups][stages][1 or 2][slots] vectors
+  __shared__ uint64_t full_all[kGroups][kMaxStages];
+  __shared__ float sums_all[kGroups][2][kWarps];
+  __shared__ ptx::Abort abort;
+  const int group = threadIdx.x / kRow, tid = threadIdx.x % kRow, lane = tid & 31, warp = tid >> 5;
+  const int groups = blockDim.x / kRow;  // kGroups, or fewer where there are few rows
+  uint64_t* full = full_all[group];
+  float (&sums)[2][kWarps] = sums_all[group];
+  const int64_t first = (int64_t)blockIdx.x * groups + group, step = (int64_t)gridDim.x * groups;
+  const int turns = first < a.p.rows ? (int)((a.p.rows - first + step - 1) / step) : 0;
+  const int cols = (int)a.p.cols;
+  const float inv = 1.f / (float)cols;
+  const bool has_r = a.r != nullptr;
+  const int tensors = has_r ? 2 : 1;
+  const T* in[2] = {static_cast<const T*>(a.x) + first * a.p.x_stride,
+                    static_cast<const T*>(a.r) + (has_r ? first * a.p.r_stride : 0)};
+  const int64_t ahead[2] = {step * a.p.x_stride, step * a.p.r_stride};
+  int shift = 0;
+  if constexpr (kRagged) shift = (int)(reinterpret_cast<uintptr_t>(in[0]) & 15) / (int)sizeof(T);
+  const int vectors = (shift + cols + E - 1) / E;  // <= slots
+  const int whole0 = shift > 0 ? 1 : 0, whole1 = (shift + cols) / E;
+  const uint32_t slot_bytes = (uint32_t)slots * 16, copy_bytes = whole1 > whole0 ? (uint32_t)(whole1 - whole0) * 16 : 0;
+  const uint32_t stage_bytes = slot_bytes * tensors;
+  uint8_t* stage0 = ring + (size_t)group * stages * stage_bytes;
+  auto issue = [&](int s, int turn) {  // thread 0 only
+    uint8_t* to = stage0 + (size_t)s * stage_bytes + whole0 * 16;
+    ptx::mbar_arrive_expect_tx(&full[s], copy_bytes * tensors);
+    if (copy_bytes) {
+      const int c = whole0 * E - shift;
+      ptx::bulk_load(to, in[0] + turn * ahead[0] + c, copy_bytes, &full[s]);
+      if (has_r) ptx::bulk_load(to + slot_bytes, in[1] + turn * ahead[1] + c, copy_bytes, &full[s]);
+    }
+  };
+  // The vectors at the two ends, by elements: the address in the first row (NULL: no column, 0) and
+  // the place in a stage (negative: none) of those that this thread moves.
+  const T* edge_from[kEdge] = {};
+  int edge_to[kEdge] = {};
+  if constexpr (kRagged) {
+#pragma unroll
+    for (int k = 0; k < kEdge; ++k) {
+      const int i = tid + k * kRow, t = i / (2 * E), e = i % E;
+      const bool right = (i / E) & 1;
+      const int v = right ? (shift + cols) / E : 0, c = v * E - shift + e;
+      const bool there = i < 2 * E * tensors && (right ? (shift + cols) % E != 0 : shift > 0);
+      edge_to[k] = there ? (int)(t * slot_bytes) + (v * E + e) * (int)sizeof(T) : -1;
+      edge_from[k] = there && c >= 0 && c < cols ? (t == 0 ? in[0] : in[1]) + c : nullptr;
+    }
+  }
+  auto edge_load = [&](int k, int turn) {
+    return edge_from[k] ? edge_from[k][turn * ahead[0]] : from_f32<T>(0.f);
+  };
+  auto edge_store = [&](int k, int s, T x) {
+    if (edge_to[k] >= 0) *reinterpret_cast<T*>(stage0 + (size_t)s * stage_bytes + edge_to[k]) = x;
+  };
+  int issued = 0;  // thread 0: turns whose copies are on their way
+  if (threadIdx.x == 0) abort.flag = 0;
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
+    ptx::fence_mbar_init();
+    for (; issued < stages && issued < turns; ++issued) issue(issued, issued);
+  }
+  if constexpr (kRagged) {
+    for (int s = 0; s < stages && s < turns; ++s)
+#pragma unroll
+      for (int k = 0; k < kEdge; ++k) edge_store(k, s, edge_load(k, s));
+  }
+  const DropKey key = drop_key(a.drop);
+  const DropRate rate = drop_rate(a.drop);
+  const float2 factor = make_float2(rate.factor, rate.factor);
+  const int c_first = tid * E - shift;
+  auto columns = [&](const float* from, float other, int c0, float2 (&g)[P]) {  // of gamma or beta
+    if (!kRagged) {
+#pragma unroll
+      for (int i = 0; i < P; i += 2) {
+        const float4 v = from ? __ldg(reinterpret_cast<const float4*>(from + c0 + 2 * i))
+                              : make_float4(other, other, other, other);
+        g[i] = make_float2(v.x, v.y), g[i + 1] = make_float2(v.z, v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int c = c0 + 2 * i;
+        g[i].x = from && c >= 0 && c < cols ? __ldg(from + c) : other;
+        g[i].y = from && c + 1 >= 0 && c + 1 < cols ? __ldg(from + c + 1) : other;
+      }
+    }
+  };
+  float2 gamma[kKeep ? kVpt : 1][P], beta[kKeep ? kVpt : 1][P];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j)
+      if (tid + j * kRow < vectors) {
+        columns(a.gamma, 1.f, c_first + j * kRow * E, gamma[j]);
+        columns(a.beta, 0.f, c_first + j * kRow * E, beta[j]);
+      }
+  }
+  T* y = static_cast<T*>(a.y) + first * a.p.y_stride + c_first;
+  T* h_to = a.h ? static_cast<T*>(a.h) + first * a.p.h_stride + c_first : nullptr;
+  const int64_t y_step = step * a.p.y_stride, h_step = step * a.p.h_stride;
+  __syncthreads();
+  int s = 0;
+  uint32_t phase = 0, row = (uint32_t)first;
+  int turn = 0;
+  bool ok = true;
+  for (; turn < turns; ++turn) {
+    const bool mine = ptx::mbar_wait(&full[s], phase, &abort, status, wait_ns);
+    const uint4* x = reinterpret_cast<const uint4*>(stage0 + (size_t)s * stage_bytes) + tid;
+    const uint4* r = x + slots;
+    auto store = [&](T* out, int c0, uint4 v) {
+      if (!kRagged || (c0 >= 0 && c0 + E <= cols)) {
+        *reinterpret_cast<uint4*>(out) = v;
+      } else {
+        float2 o[P];
+        Vec<T>::pairs(v, o);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int c = c0 + 2 * i;
+          if (c >= 0 && c < cols) Vec<T>::store1(out + 2 * i, o[i].x);
+          if (c + 1 >= 0 && c + 1 < cols) Vec<T>::store1(out + 2 * i + 1, o[i].y);
+        }
+      }
+    };
+    float2 h[kVpt][P], sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+      if (tid + j * kRow >= vectors) continue;
+      const int c0 = c_first + j * kRow * E;
+      float2 w[P];
+      Vec<T>::pairs(drop_mask_at<T, kRagged>(x[j * kRow], c0, row, key, rate), h[j]);
+      Vec<T>::pairs(has_r ? r[j * kRow] : make_uint4(0u, 0u, 0u, 0u), w);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        h[j][i] = pair_fma(h[j][i], factor, w[i]);
+        sum = pair_add(h[j][i], sum);
+      }
+    }
+    auto total = [&](float m, int kind) {  // over the group; the barrier is the caller's
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (kRow > 32 && lane == 0) sums[kind][warp] = m;
+      return m;
+    };
+    auto joined = [&](float m, int kind) {
+      if constexpr (kRow == 32) return m;
+      m = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m += sums[kind][w];
+      return m;
+    };
+    float m = total(sum.x + sum.y, 0);
+    // the barrier also says that every warp is done with the stage
+    if (group_any<kRow, kGroups>(group, !mine)) { ok = false; break; }
+    const bool refill = turn + stages < turns;
+    if (tid == 0 && refill) issue(s, issued++);
+    T edge[kEdge];
+    if constexpr (kRagged) {
+      if (refill)
+#pragma unroll
+        for (int k = 0; k < kEdge; ++k) edge[k] = edge_load(k, turn + stages);
+    }
+    const float mean = joined(m, 0) * inv;
+    const float2 shift2 = make_float2(-mean, -mean);
+    sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+      if (tid + j * kRow >= vectors) continue;
+      const int c0 = c_first + j * kRow * E;
+      if (h_to) {
+        store(h_to + j * kRow * E, c0, Vec<T>::pack(h[j]));
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) h[j][i] = pair_add(h[j][i], shift2);
+      if (kRagged && (c0 < 0 || c0 + E > cols)) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int c = c0 + 2 * i;
+          if (c < 0 || c >= cols) h[j][i].x = 0.f;
+          if (c + 1 < 0 || c + 1 >= cols) h[j][i].y = 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) sum = pair_fma(h[j][i], h[j][i], sum);
+    }
+    m = total(sum.x + sum.y, 1);
+    group_any<kRow, kGroups>(group, false);
+    const float rstd = 1.f / sqrtf(joined(m, 1) * inv + a.p.eps);
+    const float2 scale2 = make_float2(rstd, rstd);
+    if (tid == 0) {
+      if (a.mean) a.mean[first + turn * step] = mean;
+      if (a.rstd) a.rstd[first + turn * step] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+      if (tid + j * kRow >= vectors) continue;
+      const int c0 = c_first + j * kRow * E;
+      float2 g[P], b[P];
+      if constexpr (!kKeep) {
+        columns(a.gamma, 1.f, c0, g);
+        columns(a.beta, 0.f, c0, b);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        h[j][i] = pair_fma(pair_mul(h[j][i], scale2), kKeep ? gamma[kKeep ? j : 0][i] : g[i],
+                           kKeep ? beta[kKeep ? j : 0][i] : b[i]);
+      store(y + j * kRow * E, c0, Vec<T>::pack(h[j]));
+    }
+    if constexpr (kRagged) {  // read only after the next barriers
+      if (refill)
+#pragma unroll
+        for (int k = 0; k < kEdge; ++k) edge_store(k, s, edge[k]);
+    }
+    y += y_step;
+    if (h_to) h_to += h_step;
+    row += (uint32_t)step;
+    if (++s == stages) s = 0, phase ^= 1;
+  }
+  if (!ok && tid == 0) {  // copies that this group issued and did not wait for
+    ptx::Abort none;
+    none.flag = 0;
+    for (int j = turn; j < issued; ++j)
+      ptx::mbar_wait(&full[j % stages], (uint32_t)((j / stages) & 1), &none, status, wait_ns);
+  }
+}
+
+template <class T, int kRow, int kGroups, int kVpt, int kBlocks>
+bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
+                 cudaError_t* error) {
+  constexpr int kSms = 152;
+  const int slots = (int)((a.p.cols + Vec<T>::E - 1) / Vec<T>::E) + (ragged ? 1 : 0);
+  const int stage = slots * 16 * (a.r ? 2 : 1);
+  // an SM's shared memory over its blocks, less what they hold beside the ring
+  const int stages = std::min(kMaxStages, (224 * 1024 / kBlocks - 2048) / kGroups / stage);
+  if (stages < 2) return false;
+  int groups = 1;  // where rows are few, on as many SMs as there are
+  while (groups < kGroups && (a.p.rows + groups - 1) / groups > kSms) groups *= 2;
+  // rows of a group are a multiple of 8 apart wherever it has more than one: the grids are multiples of 8
+  const int blocks = (int)std::min<int64_t>((a.p.rows + groups - 1) / groups, kBlocks * kSms);
+  const size_t smem = (size_t)groups * stages * stage;
+  auto kernel = ragged ? k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, true> : k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, false>;
+  *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (*error != cudaSuccess) return true;
+  kernel<<<blocks, kRow * groups, smem, st>>>(a, stages, slots, status, wait_ns);
+  *error = cudaGetLastError();
+  return true;
+}
+
+}  // namespace
+
+template <class T>
+bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
+                    cudaError_t* error) {
+  const int64_t m = (a.p.cols + Vec<T>::E - 1) / Vec<T>::E + (ragged ? 1 : 0);  // vectors of a row, at most
+  if (m <= 32) return launch_drop<T, 32, 8, 1, 2>(a, ragged, status, wait_ns, st, error);
+  if (m <= 64) return launch_drop<T, 32, 8, 2, 2>(a, ragged, status, wait_ns, st, error);
+  if (m <= 128) return launch_drop<T, 64, 4, 2, 2>(a, ragged, status, wait_ns, st, error);
+  if (m <= 256) return launch_drop<T, 128, 2, 2, 2>(a, ragged, status, wait_ns, st, error);
+  if (m <= 512) return launch_drop<T, 256, 1, 2, 2>(a, ragged, status, wait_ns, st, error);
+  if (m <= 1024) return launch_drop<T, 512, 1, 2, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 2048) return launch_drop<T, 512, 1, 4, 1>(a, ragged, status, wait_ns, st, error);
+  return false;
+}
+
+}  // namespace gbattn

@@ -1,0 +1,32 @@
+// Groups of threads that share a row, several of them in a block.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gbattn {
+
+constexpr int kMaxStages = 8;  // of a group's ring
+
+// Whether x holds for any of a group's kRow threads; a barrier of the group.
+template <int kRow, int kGroups>
+__device__ __forceinline__ bool group_any(int group, bool x) {
+  if constexpr (kRow == 32) {
+    return __any_sync(0xffffffffu, x);
+  } else if constexpr (kGroups == 1) {
+    return __syncthreads_or(x);
+  } else {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(1 + group), "n"(kRow)
+        : "memory");
+    return r != 0;
+  }
+}
+
+}  // namespace gbattn
