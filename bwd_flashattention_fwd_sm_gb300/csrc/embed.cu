@@ -32,7 +32,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;     // lookup, fill
-constexpr int kAtOnce = 4;        // vectors of a thread in flight
+template <class T, int N>
+constexpr int kAtOnce = sizeof(T) * N >= 8 ? 4 : 8;  // accesses of a thread in flight
 constexpr int kPiece = 32;        // sorted places of one block of the gradient's sums
 constexpr int kSumThreads = 128;
 constexpr int kSortThreads = 1024;
@@ -111,9 +112,10 @@ __device__ __forceinline__ int64_t id_at(const EmbedArgs& a, int64_t i) {
   return a.ids_64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
 }
 
-// `lanes` threads (a power of two) on a row; each has up to kAtOnce vectors of it in flight.
+// `lanes` threads (a power of two) on a row; each has up to kAtOnce accesses of it in flight.
 template <class T, int N>
-__global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a, int lanes_log) {
+__global__ void __launch_bounds__(kThreads, 6) k_embed(const EmbedArgs a, int lanes_log) {
+  constexpr int kAt = kAtOnce<T, N>;
   const int lanes = 1 << lanes_log;
   const int64_t row = (int64_t)blockIdx.x * (kThreads >> lanes_log) + (threadIdx.x >> lanes_log);
   if (row >= a.tokens) return;
@@ -123,22 +125,21 @@ __global__ void __launch_bounds__(kThreads) k_embed(const EmbedArgs a, int lanes
   const int units = (int)(a.dim / N);  // N divides dim
   const T* w = static_cast<const T*>(a.x) + (there ? id : 0) * a.x_stride;
   T* y = static_cast<T*>(a.y) + row * a.y_stride;
-  for (int u = threadIdx.x & (lanes - 1); u < units; u += kAtOnce * lanes) {
-    float v[kAtOnce][N];
+  for (int u = threadIdx.x & (lanes - 1); u < units; u += kAt * lanes) {
+    typename Elems<T, N>::U v[kAt];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (there && u + i * lanes < units) {
-        Elems<T, N>::load(w + (u + i * lanes) * N, v[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[i][e] = 0.f;
-      }
+    for (int i = 0; i < kAt; ++i) {
+      v[i] = Elems<T, N>::zero();
+      if (there && u + i * lanes < units) v[i] = Elems<T, N>::raw(w + (u + i * lanes) * N);
     }
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
+    for (int i = 0; i < kAt; ++i) {
+      if (u + i * lanes >= units) continue;
+      float x[N];
+      Elems<T, N>::widen(v[i], x);
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[i][e] *= a.scale;
-      if (u + i * lanes < units) Elems<T, N>::store(y + (u + i * lanes) * N, v[i]);
+      for (int e = 0; e < N; ++e) x[e] *= a.scale;
+      Elems<T, N>::store(y + (u + i * lanes) * N, x);
     }
   }
 }
@@ -509,7 +510,7 @@ void fill_steps(EmbedArgs* a, int64_t units, int64_t blocks, int threads) {
 template <class T, int N>
 void launch_lookup(const EmbedArgs& a, cudaStream_t st) {
   int lanes_log = 0;
-  while ((1 << lanes_log) < kThreads && ((int64_t)kAtOnce << lanes_log) < a.dim / N) ++lanes_log;
+  while ((1 << lanes_log) < kThreads && ((int64_t)kAtOnce<T, N> << lanes_log) < a.dim / N) ++lanes_log;
   const int rows = kThreads >> lanes_log;
   k_embed<T, N><<<(unsigned)((a.tokens + rows - 1) / rows), kThreads, 0, st>>>(a, lanes_log);
 }

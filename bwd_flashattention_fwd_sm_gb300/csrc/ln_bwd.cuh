@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
 // A short row: kRow lanes of a warp, a vector each, kRows rows of a lane at a time with all their
 // loads in flight.  kRagged: see above.
 template <class T, int kRow, int kRows, bool kDrop, bool kRagged>
-__global__ void __launch_bounds__(512) k_ln_bwd_warp(const BwdLnArgs a) {
+__global__ void __launch_bounds__(512, 2) k_ln_bwd_warp(const BwdLnArgs a) {
   constexpr int E = Vec<T>::E, P = E / 2;
   extern __shared__ float column[];  // [2][cols]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -790,7 +790,7 @@ cudaError_t launch_ln_bwd(const BwdLnArgs& a, bool drops, int* parts, int* statu
   const bool ragged = !(a.vec && a.p.cols % E == 0);
   const int64_t n = div_up(a.p.cols, E), m = n + (ragged ? 1 : 0);  // vectors of a row, at most
   if (!ragged || a.alike) {
-    constexpr int kRows = E == 8 ? 2 : 4;  // what 128 registers hold without spills
+    constexpr int kRows = E == 8 ? 1 : 2;  // what 64 registers hold
     if (m <= 8) return launch_warp<T, 8, kRows>(a, drops, ragged, parts, st);
     if (m <= 16) return launch_warp<T, 16, kRows>(a, drops, ragged, parts, st);
     if (m <= 32) return launch_warp<T, 32, kRows>(a, drops, ragged, parts, st);

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import LnBwdParamsC, LnParamsC, check
+from ._lib import SIZE_MAX, LnBwdParamsC, LnParamsC, check
 from .attention import _workspace
 from .drop import dropout_params
 from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library
@@ -95,15 +95,16 @@ def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p:
     dtype = DTYPES.get(dy.dtype)
     if dtype is None:
         raise ValueError("dy must be bfloat16 or float32")
-    device = dy.device
-    for name, t in (("h", h), ("dh", dh)):
-        if t is not None and (t.shape != dy.shape or t.dtype != dy.dtype or t.device != device):
-            raise ValueError(f"{name} must match dy in shape, dtype and device")
+    device, shape = dy.device, dy.shape
     cols = _cols(dy)
     rows = dy.numel() // cols
-    for name, t in (("mean", mean), ("rstd", rstd)):
+    if h.shape != shape or h.dtype != dy.dtype or h.device != device:
+        raise ValueError("h must match dy in shape, dtype and device")
+    if dh is not None and (dh.shape != shape or dh.dtype != dy.dtype or dh.device != device):
+        raise ValueError("dh must match dy in shape, dtype and device")
+    for t in (mean, rstd):
         if t.dtype != torch.float32 or t.numel() != rows or t.device != device:
-            raise ValueError(f"{name} must be a float32 CUDA tensor of {rows} elements")
+            raise ValueError(f"mean and rstd must be float32 CUDA tensors of {rows} elements")
     _check_weight("gamma", gamma, cols)
     if stream is not None or device.index != current_device():
         with elsewhere(device, stream, (dy, h, mean, rstd, gamma, dh, rng, workspace)):
@@ -118,7 +119,7 @@ def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p:
         dh, dh_stride = as_rows(dh, cols)
     mean, rstd = mean.contiguous(), rstd.contiguous()
     gamma = None if gamma is None else gamma.contiguous()
-    dr = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+    dr = torch.empty(shape, dtype=dy.dtype, device=device)
     dx = dr if d is None else torch.empty_like(dr)
     p = LnBwdParamsC(rows, cols, dy_stride, dh_stride, h_stride, cols, cols, dtype)
     dgamma = dbeta = ws = None
@@ -127,7 +128,10 @@ def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p:
         dgamma = torch.empty(cols, dtype=torch.float32, device=device)
         dbeta = torch.empty_like(dgamma)
         need = lib.ln_residual_bwd_workspace_size(p)
-        ws = _workspace(need, device, workspace)
+        if workspace is None and 0 < need < SIZE_MAX:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            ws = _workspace(need, device, workspace)
     check(lib.ln_residual_bwd(p, d, dy.data_ptr(), _ptr(dh), h.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
                               _ptr(gamma), None if d is None else dx.data_ptr(), dr.data_ptr(), _ptr(dgamma),
                               _ptr(dbeta), _ptr(ws), need, current_stream(device.index)), "ln_residual_bwd")
