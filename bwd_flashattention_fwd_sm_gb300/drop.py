@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import LnDropoutC, LnParamsC, check
-from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library
+from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library, like
 
 _MOD = 1 << 64
 
@@ -53,7 +53,7 @@ def dropout(x, p: float, *, seed: int = 0, offset: int = 0, rng=None, stream=Non
     d = dropout_params(p, seed, offset, rng, device) or LnDropoutC()
     cols = x.shape[-1]
     src, stride = as_rows(x, cols)
-    y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
+    y = like(x) if out is None else out
     n = y.numel()
     if n:
         c = LnParamsC(n // cols, cols, stride, cols, cols, cols, 0.0, dtype)

@@ -12,7 +12,7 @@ import torch
 from ._lib import SIZE_MAX, LnBwdParamsC, LnParamsC, check
 from .attention import _workspace
 from .drop import dropout_params
-from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library
+from .rows import DTYPES, as_rows, current_device, current_stream, elsewhere, library, like
 
 
 def _ptr(t):
@@ -26,9 +26,9 @@ def _cols(t):
     return t.shape[-1]
 
 
-def _check_weight(name, t, cols):
-    if t is not None and (t.dtype != torch.float32 or t.numel() != cols or not t.is_cuda):
-        raise ValueError(f"{name} must be a float32 CUDA tensor of {cols} elements")
+def _check_weight(name, t, cols, device):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != cols or t.device != device):
+        raise ValueError(f"{name} must be a float32 CUDA tensor of {cols} elements on the other arguments' device")
 
 
 def layernorm_residual(x, residual=None, gamma=None, beta=None, *, eps: float = 1e-5, return_sum: bool = True,
@@ -51,13 +51,14 @@ def layernorm_residual(x, residual=None, gamma=None, beta=None, *, eps: float = 
     device = x.device
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.device != device):
         raise ValueError("residual must match x in shape, dtype and device")
-    _check_weight("gamma", gamma, cols)
-    _check_weight("beta", beta, cols)
+    _check_weight("gamma", gamma, cols, device)
+    _check_weight("beta", beta, cols, device)
     if stream is not None or device.index != current_device():
         with elsewhere(device, stream, (x, residual, gamma, beta, rng)):
             return layernorm_residual(x, residual, gamma, beta, eps=eps, return_sum=return_sum,
                                       return_stats=return_stats, dropout_p=dropout_p, seed=seed, offset=offset, rng=rng)
     d = dropout_params(dropout_p, seed, offset, rng, device)
+    y = like(x)
     x, x_stride = as_rows(x, cols)
     r_stride = cols
     if residual is not None:
@@ -65,7 +66,6 @@ def layernorm_residual(x, residual=None, gamma=None, beta=None, *, eps: float = 
     gamma = None if gamma is None else gamma.contiguous()
     beta = None if beta is None else beta.contiguous()
     rows = x.numel() // cols
-    y = torch.empty(x.shape, dtype=x.dtype, device=device)
     h = mean = rstd = None
     if return_sum:
         h = torch.empty_like(y)
@@ -105,13 +105,14 @@ def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p:
     for t in (mean, rstd):
         if t.dtype != torch.float32 or t.numel() != rows or t.device != device:
             raise ValueError(f"mean and rstd must be float32 CUDA tensors of {rows} elements")
-    _check_weight("gamma", gamma, cols)
+    _check_weight("gamma", gamma, cols, device)
     if stream is not None or device.index != current_device():
         with elsewhere(device, stream, (dy, h, mean, rstd, gamma, dh, rng, workspace)):
             return layernorm_residual_bwd(dy, h, mean, rstd, gamma, dh, dropout_p=dropout_p, seed=seed, offset=offset,
                                           rng=rng, weight_grads=weight_grads, workspace=workspace)
     d = dropout_params(dropout_p, seed, offset, rng, device)
     lib = library()
+    dr = like(dy)
     dy, dy_stride = as_rows(dy, cols)
     h, h_stride = as_rows(h, cols)
     dh_stride = cols
@@ -119,7 +120,6 @@ def layernorm_residual_bwd(dy, h, mean, rstd, gamma=None, dh=None, *, dropout_p:
         dh, dh_stride = as_rows(dh, cols)
     mean, rstd = mean.contiguous(), rstd.contiguous()
     gamma = None if gamma is None else gamma.contiguous()
-    dr = torch.empty(shape, dtype=dy.dtype, device=device)
     dx = dr if d is None else torch.empty_like(dr)
     p = LnBwdParamsC(rows, cols, dy_stride, dh_stride, h_stride, cols, cols, dtype)
     dgamma = dbeta = ws = None

@@ -63,6 +63,11 @@ class elsewhere:
         self._device.__exit__(*error)
 
 
+def like(t):
+    """A new contiguous tensor of t's shape and type (on the host a microsecond faster than torch.empty)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def library():
     """The loaded library."""
     return _lib._lib or _lib.load()

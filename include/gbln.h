@@ -79,14 +79,14 @@ typedef struct {
 /*
  * y = D(x) over [rows, cols] (x_stride, y_stride; the other strides and eps are not
  * looked at), and, on a gradient, dropout's backward pass.  y may be x itself (with
- * y_stride == x_stride).  rows and cols below 2^32.  d must not be NULL.  D is taken
+ * y_stride == x_stride); other rows that share an element are refused.  rows and cols below 2^32.  d must not be NULL.  D is taken
  * in float32 and rounded once.  16-byte vectors as above.
  */
 attn_status_t ln_dropout(const ln_params_t* p, const ln_dropout_t* d, const void* x, void* y, void* stream);
 
 /*
  * ln_residual_fwd with h = D(x) + residual: D(x) is not rounded before the sum.
- * d may be NULL (no dropout); rows below 2^32.
+ * d may be NULL (no dropout: the same call as ln_residual_fwd); with dropout rows below 2^32.
  */
 attn_status_t ln_dropout_residual_fwd(const ln_params_t* p, const ln_dropout_t* d, const void* x, const void* residual,
                                       const float* gamma, const float* beta, void* y, void* h, float* mean,
@@ -107,8 +107,9 @@ typedef struct {
  * gradient and dx that of x (D(dr) of the unrounded dr).  Without dropout (d NULL or t
  * = 0) the two are equal and either may be NULL; so may either with dropout.  gamma
  * NULL: 1.  dgamma and dbeta, float32 [cols], may be NULL each; where rows is 0 they are
- * set to 0.  Arithmetic and sums in float32; a column's rows are added in a fixed order
- * (the results are bit-identical from run to run).
+ * set to 0.  Arithmetic and sums in float32; a row's columns and a column's rows are added in an
+ * order that sizes and alignment decide (the results are bit-identical from run to run).  A dy, h,
+ * mean or rstd that is not finite reaches its row and the columns' sums; a dh its own element.
  *
  * Constraints as for ln_residual_fwd; outputs must not overlap inputs or one another,
  * except that dx or dr may be dy or dh itself, with the same stride.  workspace:

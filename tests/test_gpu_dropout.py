@@ -11,6 +11,7 @@ import pytest
 import torch
 
 from bwd_flashattention_fwd_sm_gb300 import dropout, get_status, layernorm_residual, layernorm_residual_bwd
+from bwd_flashattention_fwd_sm_gb300._lib import AttnError
 from oracle import rows as R
 
 pytestmark = pytest.mark.gpu
@@ -89,6 +90,9 @@ def test_views_and_in_place(dtype):
     out = dropout(x, 0.2, seed=8, offset=1, out=x)
     assert out.data_ptr() == x.data_ptr()
     check(out, base, 0.2, 8, 1)
+    whole = base.clone().view(-1)
+    with pytest.raises(AttnError, match="overlap"):
+        dropout(whole[:-8], 0.2, out=whole[8:])
     with pytest.raises(ValueError, match="out"):
         dropout(base, 0.2, out=torch.empty(20, 3, 160, device="cuda", dtype=base.dtype)[..., ::2])
 

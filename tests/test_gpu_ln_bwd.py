@@ -179,6 +179,31 @@ def test_views():
     assert shaped[0].shape == (4, 6, 208) and torch.equal(shaped[0].view(24, 208), ref[0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [5, 130, 1000, 2049, 4096, 7001, 12288, 16384])
+def test_tensors_that_begin_at_different_places(cols, dtype):
+    """h one element off 16 bytes, dh with wider rows, dy and the outputs in place: no form that moves whole rows."""
+    inp = make(70, cols, dtype, seed=cols)
+    d = {n: None if t is None else t.cuda() for n, t in inp.items()}
+    off = torch.full((70 * cols + 1,), float("nan"), dtype=DTYPES[dtype], device="cuda")
+    off[1:] = d["h"].view(-1)
+    wide = torch.full((70, cols + 24), float("nan"), dtype=DTYPES[dtype], device="cuda")
+    wide[:, :cols] = d["dh"]
+    got = layernorm_residual_bwd(d["dy"], off[1:].view(70, cols), d["mean"], d["rstd"], d["gamma"], wide[:, :cols],
+                                 dropout_p=0.2, seed=3)
+    check(got, inp, 0.2, 3, 0)
+    # the same in the forward pass
+    x, r = inp["dy"], inp["dh"]
+    off[1:] = x.cuda().view(-1)
+    y, h, mean, rstd = layernorm_residual(off[1:].view(70, cols), wide[:, :cols], d["gamma"], return_stats=True,
+                                          dropout_p=0.2, seed=3)
+    ref = R.ln_dropout_residual(f64(x), f64(r), f64(inp["gamma"]), None, 1e-5, 0.2, 3, 0)
+    if cols > 5:  # five columns may be nearly alike, and y then as far off as 1 / std says
+        compare("y", f64(y), ref[0], dtype)
+    half = torch.finfo(x.dtype).eps / 2
+    assert np.all(np.abs(f64(h) - ref[1]) <= half * np.abs(ref[1]) + 4 * U * (np.abs(f64(x)) / 0.8 + np.abs(ref[1])))
+
+
 @pytest.mark.parametrize("cols, step", [(100, 104), (100, 101), (1024, 1032), (2048, 2056), (4096, 4100), (9000, 9008)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_c_entry_writes_nothing_between_rows_or_behind(cols, step, dtype):

@@ -105,6 +105,14 @@ def test_dropout_pointers(lib):
     assert dropout(lib, ln_params(), drop(), x=None) == INVALID
     assert dropout(lib, ln_params(), drop(), y=FAKE + 1) == INVALID
     assert dropout(lib, ln_params(dtype=_lib.ATTN_F32), drop(), y=FAKE + 2) == INVALID
+    # 8 rows of 64 bf16, 64 or 128 elements apart: y on x's elements, beside them, between them, x itself
+    wide = dict(x_stride=128, y_stride=128)
+    for change, y, code in (({}, FAKE + 128, INVALID), ({}, FAKE + 1024, NO_GPU), ({}, FAKE, NO_GPU),
+                            (wide, FAKE + 128, NO_GPU), (wide, FAKE - 128, NO_GPU), (wide, FAKE + 126, INVALID),
+                            (wide, FAKE + 130, INVALID), (wide, FAKE + 256, INVALID), (wide, FAKE, NO_GPU),
+                            ({"x_stride": 128}, FAKE, INVALID), ({"x_stride": 128}, FAKE + 2048, NO_GPU),
+                            ({"rows": 1, "x_stride": 128}, FAKE, NO_GPU), ({"rows": 1}, FAKE + 126, INVALID)):
+        assert dropout(lib, ln_params(**change), drop(), y=y) == code, (change, y - FAKE)
     for empty in ({"rows": 0}, {"cols": 0, "x_stride": 0, "y_stride": 0}):
         assert dropout(lib, ln_params(**empty), drop(), x=None, y=None) == _lib.ATTN_OK
 
