@@ -84,6 +84,7 @@ extern "C" {
 
 size_t ln_residual_bwd_workspace_size(const ln_bwd_params_t* p) {
   if (check_params(p) != ATTN_OK) return SIZE_MAX;
+  if (ln_bwd_joins(*p)) return 0;
   return (size_t)std::min<int64_t>(p->rows, kLnMaxParts) * 2 * (size_t)p->cols * sizeof(float);
 }
 
@@ -93,7 +94,7 @@ attn_status_t ln_residual_bwd(const ln_bwd_params_t* p, const ln_dropout_t* d, c
                               void* stream) {
   attn_status_t s = check_params(p);
   if (s != ATTN_OK) return s;
-  BwdLnArgs a{*p, dy, dh, h, mean, rstd, gamma, dx, dr, nullptr, 0, 1, {}};
+  BwdLnArgs a{*p, dy, dh, h, mean, rstd, gamma, dx, dr, nullptr, nullptr, nullptr, false, 0, 1, {}};
   bool drops = false;
   if (const char* wrong = resolve_dropout(d, &a.drop, &drops)) return bfail(ATTN_ERR_INVALID_ARG, wrong);
   if (drops && p->rows >= (int64_t)1 << 32)
@@ -126,14 +127,19 @@ attn_status_t ln_residual_bwd(const ln_bwd_params_t* p, const ln_dropout_t* d, c
   unsigned long long wait_ns = 0;
   if ((s = device_status(&status, &sms, &wait_ns))) return s;
   a.vec = ((at | reinterpret_cast<uintptr_t>(gamma)) & 15) == 0;
-  a.part = weights ? static_cast<float*>(workspace) : nullptr;
+  if (weights && p->rows > 0) {
+    if (ln_bwd_joins(*p))
+      a.join = true, a.dgamma = dgamma, a.dbeta = dbeta;
+    else
+      a.part = static_cast<float*>(workspace);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int blocks = 0;
   cudaError_t e = cudaSuccess;
   if (p->rows > 0)
     e = p->dtype == ATTN_BF16 ? launch_ln_bwd<__nv_bfloat16>(a, drops, &blocks, status, wait_ns, st)
                               : launch_ln_bwd<float>(a, drops, &blocks, status, wait_ns, st);
-  if (e == cudaSuccess && weights) e = launch_join(a, blocks, dgamma, dbeta, st);
+  if (e == cudaSuccess && weights && !a.join) e = launch_join(a, blocks, dgamma, dbeta, st);
   if (e != cudaSuccess) return bfail(ATTN_ERR_CUDA, "ln_residual_bwd: launch failed");
   return ATTN_OK;
 }

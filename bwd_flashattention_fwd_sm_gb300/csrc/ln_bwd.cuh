@@ -35,6 +35,8 @@ namespace gbattn {
 // workspace and the order of the sums are the same everywhere.
 constexpr int kLnSms = 152;
 constexpr int kLnMaxParts = 2 * kLnSms;
+constexpr int kLnCluster = 8;             // blocks of the cluster that does little work alone
+constexpr int64_t kLnFewBytes = 1 << 16;  // of one tensor
 
 struct BwdLnArgs {
   ln_bwd_params_t p;
@@ -46,11 +48,22 @@ struct BwdLnArgs {
   const float* gamma;
   void* dx;
   void* dr;
-  float* part;  // [blocks][2][cols]: sums of dy xh, and of dy; NULL: not wanted
+  float* part;  // [blocks][2][cols]: sums of dy xh, and of dy; NULL: not wanted, or joined at once
+  float* dgamma;  // where the grid is one cluster, which joins its blocks' sums itself; else NULL
+  float* dbeta;
+  bool join;
   int vec;      // every pointer 16-byte aligned and every stride a whole number of vectors
   int alike;    // every tensor's pointer the same modulo 16 bytes, and every stride the same
   DropArgs drop;
 };
+
+// So little work that one cluster does it and joins its blocks' sums over shared memory: one launch and
+// no workspace.  [32, 1024] bf16 takes the GPU 7.0 us this way and 4.6 with k_ln_bwd_join, but the host
+// issues a call in 25 us instead of 32, and calls of this size wait for the host.  By sizes alone,
+// because the workspace's size says so too.
+inline bool ln_bwd_joins(const ln_bwd_params_t& p) {
+  return p.rows <= kLnFewBytes / (p.cols * (p.dtype == ATTN_BF16 ? 2 : 4));
+}
 
 // Launches the kernel for a.p's rows; *parts: how many rows of partial sums it leaves.
 template <class T>
@@ -58,6 +71,57 @@ cudaError_t launch_ln_bwd(const BwdLnArgs& a, bool drops, int* parts, int* statu
                           cudaStream_t st);
 
 namespace {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// dgamma and dbeta from the blocks' columns [2][cols] in shared memory, the blocks in order.  All threads of all
+// blocks of the cluster come here; good: this block's columns hold sums.
+__device__ __forceinline__ void join_columns(const float* column, int cols, float* dgamma, float* dbeta, bool good) {
+  uint32_t blocks;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(blocks));
+  __syncthreads();
+  cluster_barrier();
+  if (good) {
+    for (int c = cluster_rank() * blockDim.x + threadIdx.x; c < 2 * cols; c += blocks * blockDim.x) {
+      float v[kLnCluster], s = 0.f;
+#pragma unroll
+      for (uint32_t r = 0; r < kLnCluster; ++r) {
+        uint32_t from;
+        v[r] = 0.f;
+        if (r < blocks) {
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(ptx::smem_u32(column + c)), "r"(r));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(from) : "memory");
+        }
+      }
+#pragma unroll
+      for (uint32_t r = 0; r < kLnCluster; ++r) s += v[r];
+      float* to = c < cols ? dgamma : dbeta;
+      if (to) to[c < cols ? c : c - cols] = s;
+    }
+    __syncwarp();
+  }
+  cluster_barrier();  // no block leaves while another reads its columns
+}
+
+// The sums of a block's groups, each group's [2][cols] at its place in shared memory (`apart` floats on), in
+// order: to `part`, or (NULL) to the first group's place.
+__device__ __forceinline__ void add_groups(float* column, int groups, int apart, int cols, float* part) {
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) {
+    float s = column[c];
+#pragma unroll 8
+    for (int g = 1; g < groups; ++g) s += column[g * apart + c];
+    (part ? part : column)[c] = s;
+  }
+}
 
 // The widened vector at column c0 of a row; 0 behind the row's end.
 template <class T>
@@ -89,6 +153,7 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
   constexpr bool kHold = kVpt * E <= 16;
   constexpr int H = kHold ? kVpt : 1;
   __shared__ float2 warp_sum[2][kWarps];
+  extern __shared__ float column[];  // [2][cols], where the cluster joins
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t cols = a.p.cols;
   const float inv = 1.f / (float)cols;
@@ -179,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
       }
     }
   }
-  if (!a.part) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * cols;
+  if (!a.part && !a.join) return;
+  float* part = a.join ? column : a.part + (int64_t)blockIdx.x * 2 * cols;
 #pragma unroll
   for (int j = 0; j < kVpt; ++j)
 #pragma unroll
@@ -188,6 +253,7 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
       const int64_t c = (int64_t)(tid + j * kThreads) * E + e;
       if (c < cols) part[c] = sg[j][e], part[cols + c] = sb[j][e];
     }
+  if (a.join) join_columns(column, (int)cols, a.dgamma, a.dbeta, true);
 }
 
 // A short row: kRow lanes of a warp, a vector each, kRows rows of a lane at a time with all their
@@ -195,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) k_ln_bwd(const BwdLnArgs a) {
 template <class T, int kRow, int kRows, bool kDrop, bool kRagged>
 __global__ void __launch_bounds__(512, 2) k_ln_bwd_warp(const BwdLnArgs a) {
   constexpr int E = Vec<T>::E, P = E / 2;
-  extern __shared__ float column[];  // [2][cols]
+  extern __shared__ float column[];  // [groups][2][cols]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % kRow, groups = blockDim.x / kRow;
   const int cols = (int)a.p.cols;
@@ -318,56 +384,17 @@ __global__ void __launch_bounds__(512, 2) k_ln_bwd_warp(const BwdLnArgs a) {
       }
     }
   }
-  if (!a.part) return;
-  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if constexpr (kRagged && kRow < 32) {
-    // the groups of lanes that share a warp may hold other columns: one after the other
-    for (int g = 0; g < groups; ++g) {
-      if ((int)threadIdx.x / kRow == g) {
+  if (!a.part && !a.join) return;
+  float* own = column + (threadIdx.x / kRow) * 2 * cols;
 #pragma unroll
-        for (int i = 0; i < P; ++i)
+  for (int i = 0; i < P; ++i)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int c = c0 + 2 * i + k;
-            if (c >= 0 && c < cols) {
-              column[c] = (g ? column[c] : 0.f) + (k ? sg[i].y : sg[i].x);
-              column[cols + c] = (g ? column[cols + c] : 0.f) + (k ? sb[i].y : sb[i].x);
-            }
-          }
-      }
-      __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+      const int c = c0 + 2 * i + k;
+      if (c >= 0 && c < cols) own[c] = k ? sg[i].y : sg[i].x, own[cols + c] = k ? sb[i].y : sb[i].x;
     }
-  } else {
-    // the groups of lanes that share a warp, then the block's warps one after the other
-    if constexpr (kRow < 32) {
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int o = kRow; o < 32; o *= 2) {
-          sg[i].x += __shfl_xor_sync(0xffffffffu, sg[i].x, o);
-          sg[i].y += __shfl_xor_sync(0xffffffffu, sg[i].y, o);
-          sb[i].x += __shfl_xor_sync(0xffffffffu, sb[i].x, o);
-          sb[i].y += __shfl_xor_sync(0xffffffffu, sb[i].y, o);
-        }
-    }
-    for (int w = 0; w < warps; ++w) {
-      if (warp == w && (threadIdx.x & 31) < kRow) {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int c = c0 + 2 * i + k;
-            if (c >= 0 && c < cols) {
-              column[c] = (w ? column[c] : 0.f) + (k ? sg[i].y : sg[i].x);
-              column[cols + c] = (w ? column[cols + c] : 0.f) + (k ? sb[i].y : sb[i].x);
-            }
-          }
-      }
-      __syncthreads();
-    }
-  }
-  float* part = a.part + (int64_t)blockIdx.x * 2 * cols;
-  for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) part[c] = column[c];
+  add_groups(column, groups, 2 * cols, cols, a.join ? nullptr : a.part + (int64_t)blockIdx.x * 2 * cols);
+  if (a.join) join_columns(column, cols, a.dgamma, a.dbeta, true);
 }
 
 // A longer row: kRow threads, kVpt vectors each.  A block holds kGroups such rows side by side;
@@ -377,15 +404,6 @@ __global__ void __launch_bounds__(512, 2) k_ln_bwd_warp(const BwdLnArgs a) {
 // then for dr), which leaves the registers to the columns' sums.  Waits are bounded: a
 // group that gives up records ATTN_ERR_DEVICE_TIMEOUT, waits (bounded) for its own copies and
 // stops, and its block leaves no partial sums.
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // x to the place of `here`, and 4 bytes to the count of the barrier at the place of `bar`, in the
 // block `rank` of the cluster.  (Not a cluster barrier: that would wait for the stores of dr and dx.)
 __device__ __forceinline__ void cluster_send(void* here, uint64_t* bar, uint32_t rank, float x) {
@@ -666,9 +684,9 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     __syncwarp();
     cluster_barrier();
   }
-  if (!a.part) return;
+  if (!a.part && !a.join) return;
   float* part = a.part + unit * 2 * cols;
-  if (kGroups == 1 || groups == 1) {
+  if (!a.join && groups == 1) {
     if (!ok) return;
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
@@ -693,48 +711,63 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
       }
     }
   } else {
-    if (!__syncthreads_and(ok)) return;  // and the ring is free: every copy has been waited for
-    float* column = reinterpret_cast<float*>(ring);  // [2][cols]
-    for (int g = 0; g < groups; ++g) {
-      if (group == g) {
+    const bool good = __syncthreads_and(ok);  // and the ring is free: every copy has been waited for
+    if (good) {  // a group's own stages hold its sums
+      float* own = reinterpret_cast<float*>(stage0);
 #pragma unroll
-        for (int j = 0; j < kVpt; ++j) {
-          if (v0 + tid + j * kRow >= v1) continue;
-          const int c0 = c_first + j * kRow * E;
+      for (int j = 0; j < kVpt; ++j) {
+        if (v0 + tid + j * kRow >= v1) continue;
+        const int c0 = c_first + j * kRow * E;
 #pragma unroll
-          for (int i = 0; i < P; ++i)
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int c = c0 + 2 * i + k;
-              if (kRagged && (c < 0 || c >= cols)) continue;
-              column[c] = (g ? column[c] : 0.f) + (k ? sg[j][i].y : sg[j][i].x);
-              column[cols + c] = (g ? column[cols + c] : 0.f) + (k ? sb[j][i].y : sb[j][i].x);
-            }
-        }
+          for (int k = 0; k < 2; ++k) {
+            const int c = c0 + 2 * i + k;
+            if (kRagged && (c < 0 || c >= cols)) continue;
+            own[c] = k ? sg[j][i].y : sg[j][i].x, own[cols + c] = k ? sb[j][i].y : sb[j][i].x;
+          }
       }
-      __syncthreads();
+      add_groups(reinterpret_cast<float*>(ring), groups, stages * (int)stage_bytes / 4, cols, a.join ? nullptr : part);
     }
-    for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) part[c] = column[c];
+    if constexpr (kCluster == 1)
+      if (a.join) join_columns(reinterpret_cast<float*>(ring), cols, a.dgamma, a.dbeta, good);
   }
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+template <class K, class... A>
+cudaError_t launch_cluster(K kernel, int blocks, int threads, size_t smem, int cluster, cudaStream_t st, A... args) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cluster, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A kernel's variants: with and without dropout, whole vectors and ragged rows.
 template <class T, int kRow, int kRows>
 cudaError_t launch_warp(const BwdLnArgs& a, bool drops, bool ragged, int* parts, cudaStream_t st) {
-  // as many warps a block as leave every SM a block, 16 at most
+  // as many warps a block as leave every SM (of the cluster, if one does it all) a block, 16 at most
   const int a_warp = 32 / kRow;
   int warps = 1;
-  while (warps < 16 && div_up(a.p.rows, (int64_t)warps * a_warp) > kLnSms) warps *= 2;
-  const int blocks = (int)std::min<int64_t>(div_up(a.p.rows, (int64_t)warps * a_warp), kLnMaxParts);
+  while (warps < 16 && div_up(a.p.rows, (int64_t)warps * a_warp) > (a.join ? kLnCluster : kLnSms)) warps *= 2;
+  const int blocks =
+      (int)std::min<int64_t>(div_up(a.p.rows, (int64_t)warps * a_warp), a.join ? kLnCluster : kLnMaxParts);
   *parts = blocks;
-  const size_t smem = a.part ? 2 * a.p.cols * sizeof(float) : 0;
+  const size_t smem = a.part || a.join ? (size_t)warps * a_warp * 2 * a.p.cols * sizeof(float) : 0;  // 32 KB at most
   auto kernel =
       ragged ? (drops ? k_ln_bwd_warp<T, kRow, kRows, true, true> : k_ln_bwd_warp<T, kRow, kRows, false, true>)
              : (drops ? k_ln_bwd_warp<T, kRow, kRows, true, false> : k_ln_bwd_warp<T, kRow, kRows, false, false>);
-  kernel<<<blocks, 32 * warps, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_cluster(kernel, blocks, 32 * warps, smem, a.join ? blocks : 1, st, a);
 }
 
 template <class T, int kRow, int kGroups, int kVpt, int kBlocks, int kCluster>
@@ -744,8 +777,11 @@ cudaError_t launch_ring(const BwdLnArgs& a, bool drops, bool ragged, int* parts,
   // form: 304 or 152 blocks, 76 clusters of two (period 4 of the 4-byte type) or 72.
   int most = kBlocks * kLnSms / kCluster;
   if (ragged && kGroups * most % (int)(16 / sizeof(T)) != 0) most = most / 8 * 8;
-  int groups = 1;  // where rows are few, on as many SMs as there are
-  while (groups < kGroups && div_up(a.p.rows, groups) > kLnSms) groups *= 2;
+  // where rows are few, on as many SMs as there are (the cluster has, if one does it all)
+  const bool join = kCluster == 1 && a.join;
+  if (join) most = kLnCluster;
+  int groups = 1;
+  while (groups < kGroups && div_up(a.p.rows, groups) > (join ? kLnCluster : kLnSms)) groups *= 2;
   *parts = (int)std::min<int64_t>(div_up(a.p.rows, groups), most);
   const int slots = (int)div_up(div_up(a.p.cols, Vec<T>::E) + (ragged ? 1 : 0), kCluster);
   const int stage = slots * 16 * (a.dh ? 3 : 2);
@@ -756,29 +792,16 @@ cudaError_t launch_ring(const BwdLnArgs& a, bool drops, bool ragged, int* parts,
                                 : k_ln_bwd_ring<T, kRow, kGroups, kVpt, kBlocks, kCluster, false, true>)
                        : (drops ? k_ln_bwd_ring<T, kRow, kGroups, kVpt, kBlocks, kCluster, true, false>
                                 : k_ln_bwd_ring<T, kRow, kGroups, kVpt, kBlocks, kCluster, false, false>);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)*parts * kCluster);
-  cfg.blockDim = dim3(kRow * groups);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute cluster{};
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = kCluster, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = kCluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, stages, slots, status, wait_ns);
+  return launch_cluster(kernel, *parts * kCluster, kRow * groups, smem, join ? *parts : kCluster, st, a, stages, slots,
+                        status, wait_ns);
 }
 
 template <class T, int kThreads, int kVpt>
 cudaError_t launch_rows(const BwdLnArgs& a, bool drops, int* parts, cudaStream_t st) {
-  *parts = (int)std::min<int64_t>(a.p.rows, kLnMaxParts);
-  if (drops)
-    k_ln_bwd<T, kThreads, kVpt, true><<<*parts, kThreads, 0, st>>>(a);
-  else
-    k_ln_bwd<T, kThreads, kVpt, false><<<*parts, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  *parts = (int)std::min<int64_t>(a.p.rows, a.join ? kLnCluster : kLnMaxParts);
+  const size_t smem = a.join ? 2 * a.p.cols * sizeof(float) : 0;
+  return launch_cluster(drops ? k_ln_bwd<T, kThreads, kVpt, true> : k_ln_bwd<T, kThreads, kVpt, false>, *parts, kThreads,
+                        smem, a.join ? *parts : 1, st, a);
 }
 
 }  // namespace
@@ -800,10 +823,10 @@ cudaError_t launch_ln_bwd(const BwdLnArgs& a, bool drops, int* parts, int* statu
     if (m <= 512) return launch_ring<T, 256, 1, 2, 2, 1>(a, drops, ragged, parts, status, wait_ns, st);
     if (m <= 1024) return launch_ring<T, 512, 1, 2, 1, 1>(a, drops, ragged, parts, status, wait_ns, st);
     if constexpr (E == 8) {
-      if (m <= 2048) return launch_ring<T, 512, 1, 2, 1, 2>(a, drops, ragged, parts, status, wait_ns, st);
+      if (m <= 2048 && !a.join) return launch_ring<T, 512, 1, 2, 1, 2>(a, drops, ragged, parts, status, wait_ns, st);
     } else {
       if (m <= 2048) return launch_ring<T, 512, 1, 4, 1, 1>(a, drops, ragged, parts, status, wait_ns, st);
-      if (m <= 4096) return launch_ring<T, 512, 1, 4, 1, 2>(a, drops, ragged, parts, status, wait_ns, st);
+      if (m <= 4096 && !a.join) return launch_ring<T, 512, 1, 4, 1, 2>(a, drops, ragged, parts, status, wait_ns, st);
     }
   }
   if (n <= 256) return launch_rows<T, 256, 1>(a, drops, parts, st);

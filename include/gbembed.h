@@ -52,8 +52,8 @@ attn_status_t attn_embedding_fwd(const attn_embedding_params_t* p, const void* w
  * per call.  A row's tokens are added in float32 in a fixed order that depends on ids
  * alone: the result is bit-identical from run to run.  workspace: device scratch, 256-byte
  * aligned, >= attn_embedding_bwd_workspace_size(p) bytes (SIZE_MAX if the parameters
- * are invalid); it keeps nothing from one call to the next, and calls that may overlap
- * need one each.
+ * are invalid; 0 for few tokens); it keeps nothing from one call to the next, and calls that
+ * may overlap need one each.
  */
 size_t attn_embedding_bwd_workspace_size(const attn_embedding_params_t* p);
 attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* dy, const void* ids, void* dweight,

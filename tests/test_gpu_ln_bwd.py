@@ -9,9 +9,9 @@ Tolerances, with u = 2^-24 (float32's half step), n columns, R rows, per element
         (|dr| + |dh|), and half a step of the type (finfo.eps / 2) of dr.
   dx    the same, times the factor, and three more roundings (3u |dx|).
   dgamma, dbeta
-        there are at least min(R, 152) blocks; a column's term passes at most R / 152 + 1 additions in a thread, 2 + 16
-        in a block, 608 / 8 + 8 in the join, and has at most 4 roundings of its own:
-        (R / 152 + 108) u sum|terms|.
+        a column's term passes at most R / 152 + 1 additions in a thread (R / 256 and more rows at once where one
+        cluster does it all and R is above 256), 64 in a block, 304 / 16 + 16 or 8 in the join, and has at most
+        4 roundings of its own: (R / 152 + 108) u sum|terms|.
   forward with dropout: as tests/test_gpu_ln.py, h in addition off by the factor's and the product's
         rounding: (eps / 2) |h| + 4u (|D(x)| + |h|).
 """
@@ -84,7 +84,7 @@ def run(inp, **kw):
     return layernorm_residual_bwd(d["dy"], d["h"], d["mean"], d["rstd"], d["gamma"], d["dh"], **kw)
 
 
-SHAPES = [(1, 1), (2, 3), (3, 7), (1, 16), (300, 64), (9, 100), (33, 256), (7, 257), (64, 1000), (17, 1024), (5, 1030),
+SHAPES = [(130000, 1), (64, 2048), (65, 2048), (128, 1024), (131, 1001), (8, 16380), (16, 4097), (1, 1), (2, 3), (3, 7), (1, 16), (300, 64), (9, 100), (33, 256), (7, 257), (64, 1000), (17, 1024), (5, 1030),
           (40, 2048), (23, 2049), (128, 4096), (33, 4104), (19, 5000), (12, 8192), (6, 8200), (4, 12289), (8, 16384),
           (5, 16383), (3000, 48), (700, 520)]
 

@@ -43,7 +43,7 @@ def ln_fwd(lib, p, d):
 
 
 def bwd_params(**kw):
-    p = LnBwdParamsC(8, 64, 64, 64, 64, 64, 64, _lib.ATTN_BF16)
+    p = LnBwdParamsC(8000, 64, 64, 64, 64, 64, 64, _lib.ATTN_BF16)
     for k, v in kw.items():
         setattr(p, k, v)
     return p
@@ -57,7 +57,7 @@ def bwd(lib, p, d=None, ws=FAKE, ws_bytes=1 << 40, **ptr):
 
 
 def embed_params(**kw):
-    p = EmbeddingParamsC(8, 100, 64, 64, 64, 1.0, _lib.ATTN_BF16, _lib.ATTN_BF16, 1, 0, -1)
+    p = EmbeddingParamsC(800, 100, 64, 64, 64, 1.0, _lib.ATTN_BF16, _lib.ATTN_BF16, 1, 0, -1)
     for k, v in kw.items():
         setattr(p, k, v)
     return p
@@ -149,10 +149,12 @@ def test_bwd_strides_pointers_and_workspace(lib):
     assert bwd(lib, bwd_params(), ws=FAKE + 16) == _lib.ATTN_ERR_WORKSPACE
     assert bwd(lib, bwd_params(), ws_bytes=need - 1) == _lib.ATTN_ERR_WORKSPACE
     assert bwd(lib, bwd_params(), ws=None, ws_bytes=0, dgamma=None, dbeta=None) == NO_GPU
+    few = bwd_params(rows=100)
+    assert lib.ln_residual_bwd_workspace_size(few) == 0 and bwd(lib, few, ws=None, ws_bytes=0) == NO_GPU
     none = dict.fromkeys(NAMES)
     assert bwd(lib, bwd_params(rows=0), ws=None, ws_bytes=0, **none) == _lib.ATTN_OK
     # the columns' partial sums: never more than the largest grid's
-    for rows in (1, 1000, 1 << 40):
+    for rows in (200000, 1 << 40):
         for cols in (1, 64, 1000, 16384):
             p = bwd_params(rows=rows, cols=cols)
             assert 8 * cols <= lib.ln_residual_bwd_workspace_size(p) < 5000 * cols
@@ -182,6 +184,8 @@ def test_embedding_pointers_and_workspace(lib):
     assert embed_bwd(lib, embed_params(), ws=None) == _lib.ATTN_ERR_WORKSPACE
     assert embed_bwd(lib, embed_params(), ws=FAKE + 16) == _lib.ATTN_ERR_WORKSPACE
     assert embed_bwd(lib, embed_params(), ws_bytes=need - 1) == _lib.ATTN_ERR_WORKSPACE
+    few = embed_params(tokens=8)
+    assert lib.attn_embedding_bwd_workspace_size(few) == 0 and embed_bwd(lib, few, ws=None, ws_bytes=0) == NO_GPU
     assert embed(lib, embed_params(tokens=0), None, None, None) == _lib.ATTN_OK
     assert embed(lib, embed_params(dim=0), None, None, None) == _lib.ATTN_OK
     assert embed_bwd(lib, embed_params(vocab=0), None, None, None, None, 0) == _lib.ATTN_OK
