@@ -106,8 +106,7 @@ struct EmbedArgs {
   uint32_t row_step, unit_step;  // fill: all threads' vectors on, as rows and vectors of a row
   float scale;
   int ids_64, accumulate;
-  uint32_t* keys[2];    // gradient: ids and places, before and after a pass
-  uint32_t* place[2];
+  uint2* pairs[2];      // gradient: ids and places, before and after a pass of the sort
   float* part;          // [pieces][2][dim]: sums of words that began before the piece, that go on after it
   // Words that several pieces share: how many of few partial sums and of many, and the pieces in which they
   // begin (in any order): the few from the front of [pieces] numbers, the many from the back.
@@ -183,9 +182,11 @@ __device__ __forceinline__ uint32_t key_at(const EmbedArgs& a, int64_t i) {
 // with equal digits find their order by a vote.  Ends in buffer passes % 2.  A warp's first kHeld * 32
 // places (65536 tokens of the cluster) stay in shared memory between the two; later ones are read twice.
 // Bound by the latency of its steps and by fetching its instructions, which run once or a
-// few times: loops stay rolled (a pass unrolled over a thread's places took 9 us, most of it fetches).
+// few times: loops stay rolled (unrolled over a thread's places most of a pass was fetches).  Then by
+// the scattered stores of the hand-over, one transaction each: id and place go as one.
 __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
-  __shared__ uint32_t total[1 << kMaxBits];
+  __shared__ uint32_t total[1 << kMaxBits];   // of the block, for the cluster
+  __shared__ uint32_t start[1 << kMaxBits];   // where the block's first of a digit goes
   __shared__ uint32_t warp_total[kSortWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -194,33 +195,35 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
   const uint32_t each = (tokens / (blocks * kSortWarps) / 32 + 1) * 32;
   const uint32_t begin = min(tokens, (rank * kSortWarps + warp) * each), end = min(tokens, begin + each);
   uint32_t* mine = count + warp * digits;
-  uint32_t* held_key = count + kSortWarps * digits + warp * kHeld * 32;
-  uint32_t* held_place = held_key + kSortWarps * kHeld * 32;
+  uint2* held = reinterpret_cast<uint2*>(count + kSortWarps * digits) + warp * kHeld * 32;
   if (rank == 0 && threadIdx.x < 2) a.shared[threadIdx.x] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
-    const uint32_t* keys = a.keys[pass & 1];
-    const uint32_t* place = a.place[pass & 1];
-    uint32_t* keys_to = a.keys[(pass + 1) & 1];
-    uint32_t* place_to = a.place[(pass + 1) & 1];
-#pragma unroll 1
-    for (uint32_t d = lane; d < digits; d += 32) mine[d] = 0;
+    const uint2* pairs = a.pairs[pass & 1];
+    uint2* pairs_to = a.pairs[(pass + 1) & 1];
+    auto pair_at = [&](uint32_t i) { return pass == 0 ? make_uint2(key_at(a, i), i) : __ldcg(pairs + i); };
+    for (uint32_t d = 4 * lane; d < digits; d += 128) *reinterpret_cast<uint4*>(mine + d) = make_uint4(0u, 0u, 0u, 0u);
     __syncwarp();
 #pragma unroll 4
     for (uint32_t i = begin + lane; i < end; i += 32) {
-      const uint32_t k = pass == 0 ? key_at(a, i) : __ldcg(keys + i);
-      const uint32_t f = pass == 0 ? i : __ldcg(place + i);
-      atomicAdd(&mine[(k >> shift) & (digits - 1)], 1u);
-      if (i - begin < kHeld * 32) held_key[i - begin] = k, held_place[i - begin] = f;
+      const uint2 p = pair_at(i);
+      atomicAdd(&mine[(p.x >> shift) & (digits - 1)], 1u);
+      if (i - begin < kHeld * 32) held[i - begin] = p;
     }
     __syncthreads();
     uint32_t sum = 0;  // of this thread's digit; counts become those of the warps in front
     if (threadIdx.x < digits) {
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t n = count[w * digits + threadIdx.x];
-        count[w * digits + threadIdx.x] = sum;
-        sum += n;
+#pragma unroll 1
+      for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+        uint32_t* at = count + w0 * digits + threadIdx.x;
+        uint32_t n[16];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) n[w] = at[w * digits];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+          at[w * digits] = sum;
+          sum += n[w];
+        }
       }
       total[threadIdx.x] = sum;
     }
@@ -247,27 +250,18 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
     __syncthreads();
     uint32_t in_front = lane < warp ? warp_total[lane] : 0;
     in_front = __reduce_add_sync(0xffffffffu, in_front);
-    if (threadIdx.x < digits) {
-      const uint32_t start = in_front + before + upto - all;
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) count[w * digits + threadIdx.x] += start;
-    }
+    if (threadIdx.x < digits) start[threadIdx.x] = in_front + before + upto - all;
     __syncthreads();
 #pragma unroll 1
     for (uint32_t i0 = begin; i0 < end; i0 += 32) {
       const uint32_t i = i0 + lane, at = i - begin;
       const unsigned active = __ballot_sync(0xffffffffu, i < end);
       if (i < end) {
-        const bool held = at < kHeld * 32;
-        const uint32_t k = held ? held_key[at] : pass == 0 ? key_at(a, i) : __ldcg(keys + i);
-        const uint32_t f = held ? held_place[at] : pass == 0 ? i : __ldcg(place + i);
-        const uint32_t d = (k >> shift) & (digits - 1);
+        const uint2 p = at < kHeld * 32 ? held[at] : pair_at(i);
+        const uint32_t d = (p.x >> shift) & (digits - 1);
         const unsigned same = __match_any_sync(active, d);
-        const uint32_t to = mine[d] + __popc(same & ((1u << lane) - 1));
-        if (bounds_ok(to < tokens, a.status)) {
-          keys_to[to] = k;
-          place_to[to] = f;
-        }
+        const uint32_t to = start[d] + mine[d] + __popc(same & ((1u << lane) - 1));
+        if (bounds_ok(to < tokens, a.status)) pairs_to[to] = p;
         __syncwarp(active);
         if (lane == __ffs(same) - 1) mine[d] += __popc(same);
       }
@@ -283,7 +277,7 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
 // The first cluster sorts, the other blocks write zeros.
 template <class W, int N>
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) {
-  extern __shared__ uint32_t count[];  // [kSortWarps][digits], and twice [kSortWarps][kHeld * 32]
+  extern __shared__ uint32_t count[];  // [kSortWarps][digits], and pairs [kSortWarps][kHeld * 32]
   const unsigned sorting = cg::this_cluster().num_blocks();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x < sorting)
@@ -305,21 +299,22 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
   __shared__ uint32_t place[kPiece];
   const uint32_t begin = blockIdx.x * kPiece, tokens = (uint32_t)a.tokens;
   const int n = (int)min(tokens - begin, (uint32_t)kPiece);
-  const uint32_t* keys = a.keys[a.passes & 1];
+  const uint2* pairs = a.pairs[a.passes & 1];
   const uint32_t none = (uint32_t)a.vocab;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // sorted, and zeros written
   if ((int)threadIdx.x < n + 2) {
     const uint32_t at = begin + threadIdx.x - 1;  // wraps in front of the first
-    key[threadIdx.x] = at < tokens ? keys[at] : none;
-    if (threadIdx.x >= 1 && (int)threadIdx.x <= n) place[threadIdx.x - 1] = a.place[a.passes & 1][at];
+    const uint2 p = at < tokens ? pairs[at] : make_uint2(none, 0);
+    key[threadIdx.x] = p.x;
+    if (threadIdx.x >= 1 && (int)threadIdx.x <= n) place[threadIdx.x - 1] = p.y;
   }
   __syncthreads();
   if (blockIdx.y == 0 && threadIdx.x == 0) {  // a word that begins here and goes on
     const uint32_t k = key[n];
     if (k < none && key[n + 1] == k && (key[1] != k || key[0] != k)) {
       const uint64_t far = (uint64_t)begin + (kFew + 1) * kPiece;
-      const bool many = far < tokens && keys[far] == k;
+      const bool many = far < tokens && pairs[far].x == k;
       const uint32_t at = atomicAdd(a.shared + many, 1u);
       a.shared[2 + (many ? gridDim.x - 1 - at : at)] = blockIdx.x;
     }
@@ -392,7 +387,7 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
 template <class W>
 __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) {
   __shared__ float sums[kJoinWarps][kJoinCols];
-  const uint32_t* keys = a.keys[a.passes & 1];
+  const uint2* pairs = a.pairs[a.passes & 1];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tokens = (uint32_t)a.tokens;
   const uint32_t dim = (uint32_t)a.dim, groups = (dim + kJoinCols - 1) / kJoinCols;
   const uint32_t pieces = (tokens + kPiece - 1) / kPiece;
@@ -432,20 +427,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) 
     const uint32_t at = (first + 1 + lane) * kPiece;  // below 2^32: tokens is below 2^31
     float s[4];
     begin(first, col, s);
-    const uint32_t k = keys[(first + 1) * kPiece];
+    const uint32_t k = pairs[(first + 1) * kPiece].x;
     // sorted: the pieces that begin with this word are the next ones
-    const uint32_t n = __popc(__ballot_sync(0xffffffffu, at < tokens && keys[at] == k));
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, at < tokens && pairs[at].x == k));
     add(first, 0, n, col, s);
     finish(k, col, s);
   }
 #pragma unroll 1
   for (uint64_t i = blockIdx.x; i < many; i += gridDim.x) {
     const uint32_t first = a.shared[2 + pieces - 1 - i / groups], col = (uint32_t)(i % groups) * kJoinCols + lane;
-    const uint32_t k = keys[(first + 1) * kPiece];
+    const uint32_t k = pairs[(first + 1) * kPiece].x;
     uint32_t n = 0, found;
     do {
       const uint64_t at = ((uint64_t)first + 1 + n + threadIdx.x) * kPiece;
-      found = __syncthreads_count(at < tokens && keys[at] == k);
+      found = __syncthreads_count(at < tokens && pairs[at].x == k);
       n += found;
     } while (found == kJoinThreads);
     const uint32_t each = (n + kJoinWarps - 1) / kJoinWarps, from = min(n, warp * each);
@@ -603,7 +598,7 @@ attn_status_t check_params(const attn_embedding_params_t* p, bool backward) {
 }
 
 struct Layout {
-  size_t keys[2], place[2], part, shared, total;
+  size_t pairs[2], part, shared, total;
 };
 
 Layout layout_of(const attn_embedding_params_t* p) {
@@ -615,7 +610,7 @@ Layout layout_of(const attn_embedding_params_t* p) {
     return here;
   };
   const size_t n = (size_t)p->tokens;
-  for (int i = 0; i < 2; ++i) l.keys[i] = take(4 * n), l.place[i] = take(4 * n);
+  for (int i = 0; i < 2; ++i) l.pairs[i] = take(8 * n);
   const size_t pieces = (n + kPiece - 1) / kPiece;
   l.part = take(pieces * 2 * (size_t)p->dim * 4);
   l.shared = take((2 + pieces) * 4);
@@ -816,16 +811,13 @@ attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* d
     if (p->tokens > kFewTokens) {
       const Layout l = layout_of(p);
       char* ws = static_cast<char*>(workspace);
-      for (int i = 0; i < 2; ++i) {
-        a.keys[i] = reinterpret_cast<uint32_t*>(ws + l.keys[i]);
-        a.place[i] = reinterpret_cast<uint32_t*>(ws + l.place[i]);
-      }
+      for (int i = 0; i < 2; ++i) a.pairs[i] = reinterpret_cast<uint2*>(ws + l.pairs[i]);
       a.part = reinterpret_cast<float*>(ws + l.part);
       a.shared = reinterpret_cast<uint32_t*>(ws + l.shared);
       int bits = 1;  // of the largest key, vocab
       while (p->vocab >> bits) ++bits;
       a.passes = (bits + kMaxBits - 1) / kMaxBits;
-      a.bits = (bits + a.passes - 1) / a.passes;
+      a.bits = std::max((bits + a.passes - 1) / a.passes, 7);  // 128 counts: a vector a lane
       e = for_table(wsize == 2, n_w, [&](auto w, auto n) { return launch_sort<decltype(w), decltype(n)::value>(a, st); });
       if (e != cudaSuccess) return efail(ATTN_ERR_CUDA, "sort launch failed");
     }

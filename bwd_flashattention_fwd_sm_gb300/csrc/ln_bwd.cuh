@@ -289,15 +289,19 @@ __global__ void __launch_bounds__(512, 2) k_ln_bwd_warp(const BwdLnArgs a) {
   // Places that are no columns get 0 in dy and a column's value in h (`fill`), so that they add
   // nothing to any sum.
   auto fetch = [&](const T* row, bool fill) -> uint4 {
-    if (inside) return *reinterpret_cast<const uint4*>(row + c0);
-    float2 v[P];
+    if constexpr (kRagged) {
+      if (!inside) {
+        float2 v[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int c = c0 + 2 * i;
-      v[i].x = fill || (c >= 0 && c < cols) ? Vec<T>::load1(row + min(max(c, 0), cols - 1)) : 0.f;
-      v[i].y = fill || (c + 1 >= 0 && c + 1 < cols) ? Vec<T>::load1(row + min(max(c + 1, 0), cols - 1)) : 0.f;
+        for (int i = 0; i < P; ++i) {
+          const int c = c0 + 2 * i;
+          v[i].x = fill || (c >= 0 && c < cols) ? Vec<T>::load1(row + min(max(c, 0), cols - 1)) : 0.f;
+          v[i].y = fill || (c + 1 >= 0 && c + 1 < cols) ? Vec<T>::load1(row + min(max(c + 1, 0), cols - 1)) : 0.f;
+        }
+        return Vec<T>::pack(v);
+      }
     }
-    return Vec<T>::pack(v);
+    return *reinterpret_cast<const uint4*>(row + c0);
   };
   auto store = [&](void* base, int64_t stride, int64_t row, uint4 v) {
     T* out = static_cast<T*>(base) + row * stride;
