@@ -71,18 +71,22 @@ struct Elems {
     if constexpr (sizeof(T) * N == 16) u.w16 = *reinterpret_cast<const uint4*>(p);
     else if constexpr (sizeof(T) * N == 8) u.w8 = *reinterpret_cast<const uint2*>(p);
     else if constexpr (sizeof(T) * N == 4) u.w4 = *reinterpret_cast<const uint32_t*>(p);
-    else u.t[0] = *p;
+    else u.w4 = *reinterpret_cast<const uint16_t*>(p);  // in a register of its own: packed, each load waits for the last
     return u;
   }
   __device__ static U zero() {
     U u;
+    u.w4 = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) u.t[i] = from_f32<T>(0.f);
+    for (int i = 0; i < N; ++i)
+      if constexpr (sizeof(T) * N > 4) u.t[i] = from_f32<T>(0.f);
     return u;
   }
   __device__ static void widen(const U& u, float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f32(u.t[i]);
+    for (int i = 0; i < N; ++i)
+      if constexpr (sizeof(T) * N == 2) v[i] = __uint_as_float(u.w4 << 16);  // bfloat16
+      else v[i] = to_f32(u.t[i]);
   }
   __device__ static void load(const T* p, float (&v)[N]) { widen(raw(p), v); }
   __device__ static void store(T* p, const float (&v)[N]) {
@@ -179,11 +183,11 @@ __device__ __forceinline__ uint32_t key_at(const EmbedArgs& a, int64_t i) {
 // significant first.  Every warp of the cluster owns a stretch of the input.  It counts its
 // digits; the counts of all warps in front of it and of all lower digits say where its
 // first of each digit goes; then it takes its stretch in order, 32 at a time, and those
-// with equal digits find their order by a vote.  Ends in buffer passes % 2.  A warp's first kHeld * 32
+// with equal digits find their order by votes.  Ends in buffer passes % 2.  A warp's first kHeld * 32
 // places (65536 tokens of the cluster) stay in shared memory between the two; later ones are read twice.
 // Bound by the latency of its steps and by fetching its instructions, which run once or a
-// few times: loops stay rolled (unrolled over a thread's places most of a pass was fetches).  Then by
-// the scattered stores of the hand-over, one transaction each: id and place go as one.
+// few times: loops stay rolled (unrolled over a thread's places most of a pass was fetches).  16384 tokens of
+// a table of 50000 (two passes): 30,000 cycles, half of them votes; 40001 of 1000 (one): 22,000.
 __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
   __shared__ uint32_t total[1 << kMaxBits];   // of the block, for the cluster
   __shared__ uint32_t start[1 << kMaxBits];   // where the block's first of a digit goes
@@ -255,16 +259,22 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
 #pragma unroll 1
     for (uint32_t i0 = begin; i0 < end; i0 += 32) {
       const uint32_t i = i0 + lane, at = i - begin;
-      const unsigned active = __ballot_sync(0xffffffffu, i < end);
-      if (i < end) {
-        const uint2 p = at < kHeld * 32 ? held[at] : pair_at(i);
-        const uint32_t d = (p.x >> shift) & (digits - 1);
-        const unsigned same = __match_any_sync(active, d);
-        const uint32_t to = start[d] + mine[d] + __popc(same & ((1u << lane) - 1));
-        if (bounds_ok(to < tokens, a.status)) pairs_to[to] = p;
-        __syncwarp(active);
-        if (lane == __ffs(same) - 1) mine[d] += __popc(same);
+      const bool there = i < end;
+      uint2 p = make_uint2(0u, 0u);
+      if (there) p = at < kHeld * 32 ? held[at] : pair_at(i);
+      const uint32_t d = (p.x >> shift) & (digits - 1);
+      // which lanes have the same digit: a vote for each bit (1700 cycles for 32 warps; __match_any_sync 2600)
+      unsigned same = __ballot_sync(0xffffffffu, there);
+#pragma unroll
+      for (int b = 0; b < kMaxBits; ++b) {
+        const bool one = d >> b & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, one);
+        same &= one ? ones : ~ones;
       }
+      const uint32_t first = mine[d], to = start[d] + first + __popc(same & ((1u << lane) - 1));
+      if (there && bounds_ok(to < tokens, a.status)) pairs_to[to] = p;
+      __syncwarp();
+      if (there && lane == __ffs(same) - 1) mine[d] = first + __popc(same);
       __syncwarp();
     }
     if (blocks > 1)
