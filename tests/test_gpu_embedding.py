@@ -113,6 +113,27 @@ def test_gradient_added_to_another(tokens, dim, dtype):
         embedding_bwd(dy, ids, 400, out=out, dtype=torch.float16)
 
 
+@pytest.mark.parametrize("dtype, dim", [("bf16", 1000), ("f32", 777)])
+@pytest.mark.parametrize("tokens, kind", [(600, "few"), (3000, "uniform"), (9000, "few")])
+def test_gradient_of_a_large_table(tokens, kind, dtype, dim):
+    """Tables whose zeros take longer than the sort, over memory that holds NaN;
+    float64 sums on the GPU."""
+    vocab, dt = 150000, DTYPES[dtype]
+    g = torch.Generator().manual_seed(tokens)
+    dy = torch.randn(tokens, dim, generator=g).to(dt).cuda()
+    ids = words(tokens, vocab, kind, 3).cuda()
+    ids[:4] = torch.tensor([0, vocab - 1, vocab - 1, 0], device="cuda")
+    del_me = torch.full((vocab, dim), float("nan"), dtype=dt, device="cuda")
+    at = del_me.data_ptr()
+    del del_me
+    got = embedding_bwd(dy, ids, vocab, scale=0.5)
+    assert got.data_ptr() == at  # the same memory: every row has been written
+    ref = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda").index_add_(0, ids, 0.5 * dy.double())
+    size = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda").index_add_(0, ids, 0.5 * dy.double().abs())
+    tol = (140 + tokens / 32) * U * size + torch.finfo(dt).eps / 2 * ref.abs()
+    assert bool(((got.double() - ref).abs() <= tol).all())
+
+
 def test_ids_outside_the_table():
     """They give rows of zeros and no gradient, and are recorded; everything else is as without them."""
     g = torch.Generator().manual_seed(5)
