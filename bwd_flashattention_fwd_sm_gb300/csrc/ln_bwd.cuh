@@ -742,7 +742,7 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <class K, class... A>
 cudaError_t launch_cluster(K kernel, int blocks, int threads, size_t smem, int cluster, cudaStream_t st, A... args) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared(kernel, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)blocks);

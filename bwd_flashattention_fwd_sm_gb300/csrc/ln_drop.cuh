@@ -290,7 +290,7 @@ bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long lo
   const int blocks = (int)std::min<int64_t>((a.p.rows + groups - 1) / groups, kBlocks * kSms);
   const size_t smem = (size_t)groups * stages * stage;
   auto kernel = ragged ? k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, true> : k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, false>;
-  *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  *error = allow_shared(kernel, smem);
   if (*error != cudaSuccess) return true;
   kernel<<<blocks, kRow * groups, smem, st>>>(a, stages, slots, status, wait_ns);
   *error = cudaGetLastError();

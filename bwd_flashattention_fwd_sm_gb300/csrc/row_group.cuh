@@ -2,11 +2,20 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace gbattn {
 
 constexpr int kMaxStages = 8;  // of a group's ring
+
+// Lets a kernel take `smem` bytes of dynamic shared memory.  Always the same limit, because calls from two
+// threads may set it in turn before either launches.
+template <class K>
+cudaError_t allow_shared(K kernel, size_t smem) {
+  if (smem <= 32 * 1024) return cudaSuccess;  // 48 KB, its static shared memory included, need no leave
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+}
 
 // Whether x holds for any of a group's kRow threads; a barrier of the group.
 template <int kRow, int kGroups>

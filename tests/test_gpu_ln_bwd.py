@@ -17,6 +17,7 @@ Tolerances, with u = 2^-24 (float32's half step), n columns, R rows, per element
 """
 
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -311,6 +312,85 @@ def test_two_streams_and_two_graphs():
             g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for g, r in zip(outs, ref) for x, y in zip(g, r))
+
+
+def test_a_captured_layer_follows_the_pair_on_the_device():
+    """Forward and backward pass captured once; each replay drops by the pair's values of its time."""
+    x = torch.randn(40, 520, device="cuda").to(torch.bfloat16)
+    dy, rng = torch.randn_like(x), torch.zeros(2, dtype=torch.int64, device="cuda")
+
+    def layer(**kw):
+        y, h, mean, rstd = layernorm_residual(x, None, return_stats=True, dropout_p=0.3, **kw)
+        return (y, h, *layernorm_residual_bwd(dy, h, mean, rstd, dropout_p=0.3, **kw))
+
+    layer(rng=rng, offset=5)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer(rng=rng, offset=5)
+    for seed, offset in ((3, 4), (-9, 2 ** 40)):
+        rng.copy_(torch.tensor([seed, offset]))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, layer(seed=seed, offset=offset + 5)))
+
+
+def test_two_threads():
+    """Calls of different sizes from two host threads at once: each launch finds its kernel's limits set for it."""
+    args, kw = [], dict(dropout_p=0.1, seed=1)
+    for rows, cols in ((300, 4096), (200, 2000), (300, 2056), (160, 8192), (700, 70), (20, 16384)):
+        d = {n: None if t is None else t.cuda() for n, t in make(rows, cols, "bf16", seed=rows).items()}
+        args.append([d[n] for n in ("dy", "h", "mean", "rstd", "gamma", "dh")])
+
+    def both(a):
+        return (*layernorm_residual_bwd(*a, **kw), *layernorm_residual(a[0], a[1], a[4], **kw))
+
+    ref = [both(a) for a in args]
+    torch.cuda.synchronize()
+    wrong, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def work(which):
+        try:
+            with torch.cuda.stream(streams[which]):
+                for i in range(60):
+                    k = (i * (which + 1) + which) % len(args)
+                    if not all(torch.equal(x, y) for x, y in zip(both(args[k]), ref[k])):
+                        wrong.append(k)
+        except Exception as e:  # what a thread raises would be lost
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(w,)) for w in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@pytest.mark.parametrize("cols", [4096, 4099, 40])
+def test_offsets_beyond_31_bits(cols):
+    """Tensors of more elements than 31 bits count; sampled rows, the last among them, and the sums' magnitude."""
+    rows = ((1 << 31) + (1 << 20)) // cols
+    dy = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    dy.normal_()
+    h = torch.empty_like(dy).normal_(0.5, 2.0)
+    mean, rstd = torch.full((rows,), 0.5, device="cuda"), torch.full((rows,), 0.5, device="cuda")
+    dx, dr, dgamma, dbeta = layernorm_residual_bwd(dy, h, mean, rstd, dropout_p=0.1, seed=1, offset=2)
+    at = torch.tensor([0, 1, 7, 8, rows // 2, rows - 9, rows - 1])
+    inp = dict(dy=dy[at], h=h[at], mean=mean[at], rstd=rstd[at], gamma=None, dh=None)
+    check((dx[at], dr[at], None, None), {n: None if t is None else t.cpu() for n, t in inp.items()}, 0.1, 1, 2,
+          rows=at.numpy())
+    # sums of about 2^31 / cols terms: against the same in 64 bits, by pieces
+    ref, size = torch.zeros(cols, dtype=torch.float64, device="cuda"), torch.zeros(cols, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, rows // 64 + 1):
+        part = dy[i:i + rows // 64 + 1].double()
+        ref += part.sum(0)
+        size += part.abs().sum(0)
+    assert bool(((dbeta.double() - ref).abs() <= (rows / 152 + 108) * U * size).all())
+    del dx, dr
+    x, out = dy, layernorm_residual(dy, h, dropout_p=0.1, seed=1, offset=2)
+    y, hh = out
+    ref = R.dropout(f64(x[at]), 0.1, 1, 2, at.numpy()) + f64(h[at])
+    assert np.all(np.abs(f64(hh[at]) - ref) <= 2.0 ** -8 * np.abs(ref) + 8 * U * (np.abs(f64(x[at])) + np.abs(ref)))
+    assert bool(torch.isfinite(y[-1].float()).all()) and get_status() == 0
 
 
 def test_a_small_model_forward_and_backward():
