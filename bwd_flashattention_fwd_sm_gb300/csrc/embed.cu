@@ -6,7 +6,7 @@
 //
 // Gradient.  One launch sorts the tokens' places by id (a stable radix sort by one cluster of
 // blocks, all in shared memory but the hand-over between passes) while its other blocks write
-// zeros over the table.  The sorted places are cut in pieces of kPiece, and each block adds the rows of
+// zeros over the table.  The sorted places are cut in pieces of 16 to 64, and each block adds the rows of
 // one piece over a stretch of columns: equal work however often a word comes.  A word
 // that lies inside one piece is written to the table at once; of one that
 // several pieces share each piece leaves a partial sum, and k_embed_join adds those in order.
@@ -36,7 +36,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256;     // lookup, fill
 template <class T, int N>
 constexpr int kAtOnce = sizeof(T) * N >= 8 ? 4 : 8;  // accesses of a thread in flight
-constexpr int kPiece = 32;        // sorted places of one block of the gradient's sums
+constexpr int kMostPiece = 64;    // sorted places of one block of the gradient's sums (a.piece), at most
 constexpr int kSumThreads = 128;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -115,7 +115,7 @@ struct EmbedArgs {
   // Words that several pieces share: how many of few partial sums and of many, and the pieces in which they
   // begin (in any order): the few from the front of [pieces] numbers, the many from the back.
   uint32_t* shared;
-  int passes, bits;
+  int passes, bits, piece;
   int* status;
 };
 
@@ -305,10 +305,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_fill(const EmbedArgs a) {
 // columns a thread, kRows rows of dy in flight.
 template <class T, class W, int N, int kLoads, int kRows>
 __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
-  __shared__ uint32_t key[kPiece + 2];  // with the neighbours on both sides
-  __shared__ uint32_t place[kPiece];
-  const uint32_t begin = blockIdx.x * kPiece, tokens = (uint32_t)a.tokens;
-  const int n = (int)min(tokens - begin, (uint32_t)kPiece);
+  __shared__ uint32_t key[kMostPiece + 2];  // with the neighbours on both sides
+  __shared__ uint32_t place[kMostPiece];
+  const uint32_t piece = a.piece, begin = blockIdx.x * piece, tokens = (uint32_t)a.tokens;
+  const int n = (int)min(tokens - begin, piece);
   const uint2* pairs = a.pairs[a.passes & 1];
   const uint32_t none = (uint32_t)a.vocab;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const EmbedArgs a) {
   if (blockIdx.y == 0 && threadIdx.x == 0) {  // a word that begins here and goes on
     const uint32_t k = key[n];
     if (k < none && key[n + 1] == k && (key[1] != k || key[0] != k)) {
-      const uint64_t far = (uint64_t)begin + (kFew + 1) * kPiece;
+      const uint64_t far = (uint64_t)begin + (kFew + 1) * piece;
       const bool many = far < tokens && pairs[far].x == k;
       const uint32_t at = atomicAdd(a.shared + many, 1u);
       a.shared[2 + (many ? gridDim.x - 1 - at : at)] = blockIdx.x;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) 
   const uint2* pairs = a.pairs[a.passes & 1];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tokens = (uint32_t)a.tokens;
   const uint32_t dim = (uint32_t)a.dim, groups = (dim + kJoinCols - 1) / kJoinCols;
-  const uint32_t pieces = (tokens + kPiece - 1) / kPiece;
+  const uint32_t piece = a.piece, pieces = (tokens + piece - 1) / piece;
   // partial sums `from` .. `to` - 1 after the first of the word that begins in piece `first`
   auto add = [&](uint32_t first, uint32_t from, uint32_t to, uint32_t col, float (&s)[4]) {
     const float* p = a.part + 2 * (int64_t)(first + 1 + from) * dim + col;
@@ -434,10 +434,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) 
 #pragma unroll 1
   for (uint64_t i = (uint64_t)blockIdx.x * kJoinWarps + warp; i < few; i += (uint64_t)gridDim.x * kJoinWarps) {
     const uint32_t first = a.shared[2 + i / groups], col = (uint32_t)(i % groups) * kJoinCols + lane;
-    const uint32_t at = (first + 1 + lane) * kPiece;  // below 2^32: tokens is below 2^31
+    const uint32_t at = (first + 1 + lane) * piece;  // below 2^32: tokens is below 2^31
     float s[4];
     begin(first, col, s);
-    const uint32_t k = pairs[(first + 1) * kPiece].x;
+    const uint32_t k = pairs[(first + 1) * piece].x;
     // sorted: the pieces that begin with this word are the next ones
     const uint32_t n = __popc(__ballot_sync(0xffffffffu, at < tokens && pairs[at].x == k));
     add(first, 0, n, col, s);
@@ -446,10 +446,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const EmbedArgs a) 
 #pragma unroll 1
   for (uint64_t i = blockIdx.x; i < many; i += gridDim.x) {
     const uint32_t first = a.shared[2 + pieces - 1 - i / groups], col = (uint32_t)(i % groups) * kJoinCols + lane;
-    const uint32_t k = pairs[(first + 1) * kPiece].x;
+    const uint32_t k = pairs[(first + 1) * piece].x;
     uint32_t n = 0, found;
     do {
-      const uint64_t at = ((uint64_t)first + 1 + n + threadIdx.x) * kPiece;
+      const uint64_t at = ((uint64_t)first + 1 + n + threadIdx.x) * piece;
       found = __syncthreads_count(at < tokens && pairs[at].x == k);
       n += found;
     } while (found == kJoinThreads);
@@ -607,6 +607,18 @@ attn_status_t check_params(const attn_embedding_params_t* p, bool backward) {
   return ATTN_OK;
 }
 
+// Sorted places of a block: as many as leave some 1000 blocks (2000, where accesses are narrower and a place costs
+// more).  16384 tokens of [50000, 4096] bf16 take 105, 104 and 101 us with 16, 32 and 64; 20000 of [5000, 777] 32, 38 and
+// 50.  By sizes and types alone, because the workspace's size follows it.
+int piece_of(const attn_embedding_params_t* p) {
+  const bool bf16 = p->dtype == ATTN_BF16, same = p->dtype == p->w_dtype;
+  int64_t n = p->dim % 4 == 0 ? 4 : bf16 && same && p->dim % 2 == 0 ? 2 : 1;
+  if (bf16 && same && p->dim % 8 == 0) n = 8;
+  const int64_t bytes = n * (bf16 ? 2 : 4), cols = kSumThreads * n * (bytes >= 8 ? 1 : 4);
+  const int64_t rows = p->tokens * ((p->dim + cols - 1) / cols), blocks = bytes == 16 ? 1000 : 2000;
+  return rows >= 64 * blocks ? 64 : rows >= 32 * blocks ? 32 : 16;
+}
+
 struct Layout {
   size_t pairs[2], part, shared, total;
 };
@@ -621,7 +633,7 @@ Layout layout_of(const attn_embedding_params_t* p) {
   };
   const size_t n = (size_t)p->tokens;
   for (int i = 0; i < 2; ++i) l.pairs[i] = take(8 * n);
-  const size_t pieces = (n + kPiece - 1) / kPiece;
+  const size_t piece = piece_of(p), pieces = (n + piece - 1) / piece;
   l.part = take(pieces * 2 * (size_t)p->dim * 4);
   l.shared = take((2 + pieces) * 4);
   l.total = at;
@@ -678,7 +690,7 @@ cudaError_t launch_sums(const EmbedArgs& a, cudaStream_t st) {
     k_embed_few<T, W, N, kLoads><<<(unsigned)(a.tokens * stretches + filling), kFewThreads, 0, st>>>(a, stretches);
     return cudaGetLastError();
   }
-  const unsigned pieces = (unsigned)((a.tokens + kPiece - 1) / kPiece);
+  const unsigned pieces = (unsigned)((a.tokens + a.piece - 1) / a.piece);
   const unsigned stretches = (unsigned)((a.dim + kSumThreads * N * kLoads - 1) / (kSumThreads * N * kLoads));
   const cudaError_t e = launch_after(k_embed_sum<T, W, N, kLoads, kRows>, dim3(pieces, stretches), kSumThreads, a, st);
   if (e != cudaSuccess || pieces == 1) return e;
@@ -822,6 +834,7 @@ attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* d
       const Layout l = layout_of(p);
       char* ws = static_cast<char*>(workspace);
       for (int i = 0; i < 2; ++i) a.pairs[i] = reinterpret_cast<uint2*>(ws + l.pairs[i]);
+      a.piece = piece_of(p);
       a.part = reinterpret_cast<float*>(ws + l.part);
       a.shared = reinterpret_cast<uint32_t*>(ws + l.shared);
       int bits = 1;  // of the largest key, vocab

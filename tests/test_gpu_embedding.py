@@ -3,8 +3,9 @@ against the float64 oracle.
 
 Tolerances, with u = 2^-24: the lookup is one float32 product (u) rounded to the type (finfo.eps / 2).
 A word's gradient is a sum of float32 terms.  Up to 512 tokens: at most 128 one after the other, then four sums.
-More: at most 32 one after the other in a piece and then one partial sum for each piece that the word reaches,
-so that every term passes at most 32 + tokens / 32 + 1 additions.  The scale and (with `out`) the old value are two
+More: at most 64 one after the other in a piece of 16 or more, and then one partial sum for each piece that the word
+reaches, an eighth of them one after the other where they are more than 17, and eight sums: at most
+64 + 17 + tokens / 128 + 8 additions.  The scale and (with `out`) the old value are two
 more operations: (140 + tokens / 32) u sum|terms| covers both, and eps / 2 of the result's type.
 """
 
