@@ -552,9 +552,9 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   int s = 0, last = 0;  // this row's stage, and the one before
   uint32_t phase = 0;
   int turn = 0;
-  bool ok = true;
+  bool ok = true, late = false;
   for (; turn < turns; ++turn) {
-    bool mine = ptx::mbar_wait(&full[s], phase, &abort, status, wait_ns);
+    const bool mine = ptx::mbar_wait(&full[s], phase, &abort, status, wait_ns);
     const uint4* dy = reinterpret_cast<const uint4*>(stage0 + (size_t)s * stage_bytes) + tid;
     const uint4* h = dy + slots;
     const uint4* dh = h + slots;
@@ -600,13 +600,13 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
         if constexpr (kCluster > 1) cluster_send(to, &met[turn & 1], rank ^ 1, m);
       }
     }
-    if (group_any<kRow, kGroups>(group, !mine)) { ok = false; break; }
+    if (group_any<kRow, kGroups>(group, !mine || late)) { ok = false; break; }
     // the barrier also said that every warp is done with the last row's stage
     const bool refill = turn > 0 && turn + stages - 1 < turns;
     if (tid == 0 && refill) issue(last, issued++);
     if constexpr (kCluster > 1) {
-      mine = ptx::mbar_wait(&met[turn & 1], (uint32_t)(turn >> 1) & 1, &abort, status, wait_ns);
-      if (__syncthreads_or(!mine)) { ok = false; break; }
+      // a thread that gives up here goes on with what there is and says so at the next barrier
+      late = !ptx::mbar_wait(&met[turn & 1], (uint32_t)(turn >> 1) & 1, &abort, status, wait_ns);
       if (tid == 0) ptx::mbar_arrive_expect_tx(&met[turn & 1], 2 * kWarps * sizeof(float));
     }
     if constexpr (kParts == 1) {
@@ -678,6 +678,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     last = s;
     if (++s == stages) s = 0, phase ^= 1;
   }
+  if constexpr (kCluster > 1) ok = !__syncthreads_or(late) && ok;
   if (!ok && tid == 0) {  // copies that this group issued and did not wait for
     ptx::Abort none;
     none.flag = 0;

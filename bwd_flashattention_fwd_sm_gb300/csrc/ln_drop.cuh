@@ -2,7 +2,7 @@
 // type; ln.cu has the entry, and the form without dropout.
 //
 // A row belongs to a group of kRow threads, kVpt vectors each, and a block holds kGroups such
-// groups.  Rows stream through a ring of stages in shared memory that bulk copies fill some rows
+// groups (rows of up to 32 vectors: to some lanes of a warp).  Rows stream through a ring of stages in shared memory that bulk copies fill some rows
 // ahead.  h is made once and stays in registers; its mean and then the sum of its squared
 // distances from that mean are two sums over the group, so nothing cancels.  Bound by device memory
 // at long rows; the mask (some 60 instructions for eight elements) and the two barriers a row are next.
@@ -275,6 +275,145 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   }
 }
 
+// A short row: kRow lanes of a warp, a vector each, kRows rows of a lane at a time, loaded straight to registers.
+template <class T, int kRow, int kRows, bool kRagged>
+__global__ void __launch_bounds__(512, 2) k_ln_drop_warp(const LnDropArgs a) {
+  constexpr int E = Vec<T>::E, P = E / 2;
+  const int lane = threadIdx.x % kRow, groups = blockDim.x / kRow;
+  const int cols = (int)a.p.cols;
+  const float inv = 1.f / (float)cols;
+  const DropKey key = drop_key(a.drop);
+  const DropRate rate = drop_rate(a.drop);
+  const float2 factor = make_float2(rate.factor, rate.factor);
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t first = (int64_t)blockIdx.x * groups + threadIdx.x / kRow;
+  const T* X = static_cast<const T*>(a.x);
+  const T* R = static_cast<const T*>(a.r);
+  int shift = 0;
+  if constexpr (kRagged) shift = (int)(reinterpret_cast<uintptr_t>(X + first * a.p.x_stride) & 15) / (int)sizeof(T);
+  const int c0 = lane * E - shift;
+  const bool mine = c0 < cols, inside = c0 >= 0 && c0 + E <= cols;
+  float2 gamma[P], beta[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c = c0 + 2 * i;
+    const bool x = c >= 0 && c < cols, y = c + 1 >= 0 && c + 1 < cols;
+    gamma[i] = make_float2(a.gamma && x ? a.gamma[c] : 1.f, a.gamma && y ? a.gamma[c + 1] : 1.f);
+    beta[i] = make_float2(a.beta && x ? a.beta[c] : 0.f, a.beta && y ? a.beta[c + 1] : 0.f);
+  }
+  auto fetch = [&](const T* row) -> uint4 {  // 0 where there is no column
+    if constexpr (kRagged) {
+      if (!inside) {
+        float2 v[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int c = c0 + 2 * i;
+          v[i].x = c >= 0 && c < cols ? Vec<T>::load1(row + c) : 0.f;
+          v[i].y = c + 1 >= 0 && c + 1 < cols ? Vec<T>::load1(row + c + 1) : 0.f;
+        }
+        return Vec<T>::pack(v);
+      }
+    }
+    return *reinterpret_cast<const uint4*>(row + c0);
+  };
+  auto store = [&](void* base, int64_t stride, int64_t row, uint4 v) {
+    T* out = static_cast<T*>(base) + row * stride;
+    if (!kRagged || inside) {
+      *reinterpret_cast<uint4*>(out + c0) = v;
+    } else {
+      float2 d[P];
+      Vec<T>::pairs(v, d);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int c = c0 + 2 * i;
+        if (c >= 0 && c < cols) Vec<T>::store1(out + c, d[i].x);
+        if (c + 1 >= 0 && c + 1 < cols) Vec<T>::store1(out + c + 1, d[i].y);
+      }
+    }
+  };
+  // every lane of a warp takes the same number of turns
+  const int64_t warp_first = (int64_t)blockIdx.x * groups + (threadIdx.x & ~31) / kRow;
+  for (int64_t turn = warp_first, row = first; turn < a.p.rows; turn += kRows * step, row += kRows * step) {
+    uint4 x[kRows], r[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t at = row + u * step;
+      x[u] = r[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at < a.p.rows && mine) {
+        x[u] = fetch(X + at * a.p.x_stride);
+        if (R) r[u] = fetch(R + at * a.p.r_stride);
+      }
+    }
+    float2 h[kRows][P];
+    float m[kRows], mean[kRows];
+    auto total = [&] {
+#pragma unroll
+      for (int o = kRow / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) m[u] += __shfl_xor_sync(0xffffffffu, m[u], o);
+    };
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      float2 w[P], sum = make_float2(0.f, 0.f);
+      Vec<T>::pairs(drop_mask_at<T, kRagged>(x[u], c0, (uint32_t)(row + u * step), key, rate), h[u]);
+      Vec<T>::pairs(r[u], w);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        h[u][i] = pair_fma(h[u][i], factor, w[i]);
+        sum = pair_add(h[u][i], sum);
+      }
+      m[u] = sum.x + sum.y;
+    }
+    total();
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t at = row + u * step;
+      if (a.h && at < a.p.rows && mine) store(a.h, a.p.h_stride, at, Vec<T>::pack(h[u]));
+      mean[u] = m[u] * inv;
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        h[u][i] = pair_add(h[u][i], make_float2(-mean[u], -mean[u]));
+        if (!inside) {
+          const int c = c0 + 2 * i;
+          if (c < 0 || c >= cols) h[u][i].x = 0.f;
+          if (c + 1 < 0 || c + 1 >= cols) h[u][i].y = 0.f;
+        }
+        sum = pair_fma(h[u][i], h[u][i], sum);
+      }
+      m[u] = sum.x + sum.y;
+    }
+    total();
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t at = row + u * step;
+      if (at >= a.p.rows || !mine) continue;
+      const float rstd = 1.f / sqrtf(m[u] * inv + a.p.eps);
+      if (lane == 0) {
+        if (a.mean) a.mean[at] = mean[u];
+        if (a.rstd) a.rstd[at] = rstd;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) h[u][i] = pair_fma(pair_mul(h[u][i], make_float2(rstd, rstd)), gamma[i], beta[i]);
+      store(a.y, a.p.y_stride, at, Vec<T>::pack(h[u]));
+    }
+  }
+}
+
+template <class T, int kRow, int kRows>
+void launch_drop_warp(const LnDropArgs& a, bool ragged, cudaStream_t st, cudaError_t* error) {
+  constexpr int kSms = 152, kGroup = 32 / kRow;
+  // as many warps a block as leave every SM a block, 16 at most; rows of a lane are a multiple of 8 apart
+  int warps = 1;
+  while (warps < 16 && (a.p.rows + warps * kGroup - 1) / (warps * kGroup) > kSms) warps *= 2;
+  const int blocks = (int)std::min<int64_t>((a.p.rows + warps * kGroup - 1) / (warps * kGroup), 2 * kSms);
+  if (ragged)
+    k_ln_drop_warp<T, kRow, kRows, true><<<blocks, 32 * warps, 0, st>>>(a);
+  else
+    k_ln_drop_warp<T, kRow, kRows, false><<<blocks, 32 * warps, 0, st>>>(a);
+  *error = cudaGetLastError();
+}
+
 template <class T, int kRow, int kGroups, int kVpt, int kBlocks>
 bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
                  cudaError_t* error) {
@@ -303,7 +442,10 @@ template <class T>
 bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
                     cudaError_t* error) {
   const int64_t m = (a.p.cols + Vec<T>::E - 1) / Vec<T>::E + (ragged ? 1 : 0);  // vectors of a row, at most
-  if (m <= 32) return launch_drop<T, 32, 8, 1, 2>(a, ragged, status, wait_ns, st, error);
+  constexpr int kRows = Vec<T>::E == 8 ? 2 : 4;  // what 64 registers hold
+  if (m <= 8) return launch_drop_warp<T, 8, kRows>(a, ragged, st, error), true;
+  if (m <= 16) return launch_drop_warp<T, 16, kRows>(a, ragged, st, error), true;
+  if (m <= 32) return launch_drop_warp<T, 32, kRows>(a, ragged, st, error), true;
   if (m <= 64) return launch_drop<T, 32, 8, 2, 2>(a, ragged, status, wait_ns, st, error);
   if (m <= 128) return launch_drop<T, 64, 4, 2, 2>(a, ragged, status, wait_ns, st, error);
   if (m <= 256) return launch_drop<T, 128, 2, 2, 2>(a, ragged, status, wait_ns, st, error);
