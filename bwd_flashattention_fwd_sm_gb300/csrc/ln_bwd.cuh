@@ -72,16 +72,6 @@ cudaError_t launch_ln_bwd(const BwdLnArgs& a, bool drops, int* parts, int* statu
 
 namespace {
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // dgamma and dbeta from the blocks' columns [2][cols] in shared memory, the blocks in order.  All threads of all
 // blocks of the cluster come here; good: this block's columns hold sums.
 __device__ __forceinline__ void join_columns(const float* column, int cols, float* dgamma, float* dbeta, bool good) {
@@ -408,17 +398,6 @@ __global__ void __launch_bounds__(512, 2) k_ln_bwd_warp(const BwdLnArgs a) {
 // then for dr), which leaves the registers to the columns' sums.  Waits are bounded: a
 // group that gives up records ATTN_ERR_DEVICE_TIMEOUT, waits (bounded) for its own copies and
 // stops, and its block leaves no partial sums.
-// x to the place of `here`, and 4 bytes to the count of the barrier at the place of `bar`, in the
-// block `rank` of the cluster.  (Not a cluster barrier: that would wait for the stores of dr and dx.)
-__device__ __forceinline__ void cluster_send(void* here, uint64_t* bar, uint32_t rank, float x) {
-  uint32_t to, count;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(here)), "r"(rank));
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(count) : "r"(ptx::smem_u32(bar)), "r"(rank));
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(to),
-               "r"(__float_as_uint(x)), "r"(count)
-               : "memory");
-}
-
 template <class T, int kRow, int kGroups, int kVpt, int kBlocks, int kCluster, bool kDrop, bool kRagged>
 __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     k_ln_bwd_ring(const BwdLnArgs a, int stages, int slots, int* status, unsigned long long wait_ns) {

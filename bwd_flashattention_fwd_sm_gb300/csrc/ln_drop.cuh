@@ -6,6 +6,7 @@
 // ahead.  h is made once and stays in registers; its mean and then the sum of its squared
 // distances from that mean are two sums over the group, so nothing cancels.  Bound by device memory
 // at long rows; the mask (some 60 instructions for eight elements) and the two barriers a row are next.
+// Rows of more than 8192 columns: two blocks of a cluster, which send each other their warps' sums.
 // Rows that are no whole vectors are moved as shifted aligned vectors, as in the backward pass
 // (ln_bwd.cuh), where the rows of all tensors begin at the same place within 16 bytes.
 #pragma once
@@ -45,21 +46,24 @@ bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long
 
 namespace {
 
-template <class T, int kRow, int kGroups, int kVpt, int kBlocks, bool kRagged>
+template <class T, int kRow, int kGroups, int kVpt, int kBlocks, int kCluster, bool kRagged>
 __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     k_ln_drop(const LnDropArgs a, int stages, int slots, int* status, unsigned long long wait_ns) {
-  constexpr int E = Vec<T>::E, P = E / 2, kWarps = kRow / 32;
+  constexpr int E = Vec<T>::E, P = E / 2, kWarps = kRow / 32, kParts = kCluster * kWarps;
+  static_assert(kCluster == 1 || kGroups == 1, "one row of a cluster");
   constexpr bool kKeep = kVpt * E <= 16;            // gamma and beta in registers
   constexpr int kEdge = (4 * E + kRow - 1) / kRow;  // elements at a row's ends, of one thread
   extern __shared__ __align__(128) uint8_t ring[];  // [groups][stages][1 or 2][slots] vectors
   __shared__ uint64_t full_all[kGroups][kMaxStages];
-  __shared__ float sums_all[kGroups][2][kWarps];
+  __shared__ float sums_all[kGroups][2][kParts];
+  __shared__ uint64_t met[2];  // the other block's sums have come: of h, of its squares
   __shared__ ptx::Abort abort;
   const int group = threadIdx.x / kRow, tid = threadIdx.x % kRow, lane = tid & 31, warp = tid >> 5;
   const int groups = blockDim.x / kRow;  // kGroups, or fewer where there are few rows
   uint64_t* full = full_all[group];
-  float (&sums)[2][kWarps] = sums_all[group];
-  const int64_t first = (int64_t)blockIdx.x * groups + group, step = (int64_t)gridDim.x * groups;
+  float (&sums)[2][kParts] = sums_all[group];
+  const uint32_t rank = kCluster > 1 ? cluster_rank() : 0;
+  const int64_t first = (int64_t)(blockIdx.x / kCluster) * groups + group, step = (int64_t)(gridDim.x / kCluster) * groups;
   const int turns = first < a.p.rows ? (int)((a.p.rows - first + step - 1) / step) : 0;
   const int cols = (int)a.p.cols;
   const float inv = 1.f / (float)cols;
@@ -70,13 +74,15 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   const int64_t ahead[2] = {step * a.p.x_stride, step * a.p.r_stride};
   int shift = 0;
   if constexpr (kRagged) shift = (int)(reinterpret_cast<uintptr_t>(in[0]) & 15) / (int)sizeof(T);
-  const int vectors = (shift + cols + E - 1) / E;  // <= slots
-  const int whole0 = shift > 0 ? 1 : 0, whole1 = (shift + cols) / E;
+  const int vectors = (shift + cols + E - 1) / E;
+  const int each = (vectors + kCluster - 1) / kCluster;           // <= slots
+  const int v0 = (int)rank * each, v1 = min(vectors, v0 + each);  // this block's
+  const int whole0 = max(v0, shift > 0 ? 1 : 0), whole1 = min(v1, (shift + cols) / E);
   const uint32_t slot_bytes = (uint32_t)slots * 16, copy_bytes = whole1 > whole0 ? (uint32_t)(whole1 - whole0) * 16 : 0;
   const uint32_t stage_bytes = slot_bytes * tensors;
   uint8_t* stage0 = ring + (size_t)group * stages * stage_bytes;
   auto issue = [&](int s, int turn) {  // thread 0 only
-    uint8_t* to = stage0 + (size_t)s * stage_bytes + whole0 * 16;
+    uint8_t* to = stage0 + (size_t)s * stage_bytes + (whole0 - v0) * 16;
     ptx::mbar_arrive_expect_tx(&full[s], copy_bytes * tensors);
     if (copy_bytes) {
       const int c = whole0 * E - shift;
@@ -94,8 +100,8 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
       const int i = tid + k * kRow, t = i / (2 * E), e = i % E;
       const bool right = (i / E) & 1;
       const int v = right ? (shift + cols) / E : 0, c = v * E - shift + e;
-      const bool there = i < 2 * E * tensors && (right ? (shift + cols) % E != 0 : shift > 0);
-      edge_to[k] = there ? (int)(t * slot_bytes) + (v * E + e) * (int)sizeof(T) : -1;
+      const bool there = i < 2 * E * tensors && (right ? (shift + cols) % E != 0 : shift > 0) && v >= v0 && v < v1;
+      edge_to[k] = there ? (int)(t * slot_bytes) + ((v - v0) * E + e) * (int)sizeof(T) : -1;
       edge_from[k] = there && c >= 0 && c < cols ? (t == 0 ? in[0] : in[1]) + c : nullptr;
     }
   }
@@ -106,11 +112,17 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     if (edge_to[k] >= 0) *reinterpret_cast<T*>(stage0 + (size_t)s * stage_bytes + edge_to[k]) = x;
   };
   int issued = 0;  // thread 0: turns whose copies are on their way
-  if (threadIdx.x == 0) abort.flag = 0;
+  if (threadIdx.x == 0) {
+    abort.flag = 0;
+    if constexpr (kCluster > 1)
+      for (int i = 0; i < 2; ++i) ptx::mbar_init(&met[i], 1);
+  }
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
     ptx::fence_mbar_init();
     for (; issued < stages && issued < turns; ++issued) issue(issued, issued);
+    if constexpr (kCluster > 1)
+      for (int i = 0; i < 2; ++i) ptx::mbar_arrive_expect_tx(&met[i], kWarps * sizeof(float));
   }
   if constexpr (kRagged) {
     for (int s = 0; s < stages && s < turns; ++s)
@@ -120,7 +132,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   const DropKey key = drop_key(a.drop);
   const DropRate rate = drop_rate(a.drop);
   const float2 factor = make_float2(rate.factor, rate.factor);
-  const int c_first = tid * E - shift;
+  const int c_first = (v0 + tid) * E - shift;
   auto columns = [&](const float* from, float other, int c0, float2 (&g)[P]) {  // of gamma or beta
     if (!kRagged) {
 #pragma unroll
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   if constexpr (kKeep) {
 #pragma unroll
     for (int j = 0; j < kVpt; ++j)
-      if (tid + j * kRow < vectors) {
+      if (v0 + tid + j * kRow < v1) {
         columns(a.gamma, 1.f, c_first + j * kRow * E, gamma[j]);
         columns(a.beta, 0.f, c_first + j * kRow * E, beta[j]);
       }
@@ -150,11 +162,16 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   T* y = static_cast<T*>(a.y) + first * a.p.y_stride + c_first;
   T* h_to = a.h ? static_cast<T*>(a.h) + first * a.p.h_stride + c_first : nullptr;
   const int64_t y_step = step * a.p.y_stride, h_step = step * a.p.h_stride;
-  __syncthreads();
+  if constexpr (kCluster > 1) {
+    __syncwarp();
+    cluster_barrier();  // the other block's barriers are there too
+  } else {
+    __syncthreads();
+  }
   int s = 0;
   uint32_t phase = 0, row = (uint32_t)first;
   int turn = 0;
-  bool ok = true;
+  bool ok = true, late = false;
   for (; turn < turns; ++turn) {
     const bool mine = ptx::mbar_wait(&full[s], phase, &abort, status, wait_ns);
     const uint4* x = reinterpret_cast<const uint4*>(stage0 + (size_t)s * stage_bytes) + tid;
@@ -176,7 +193,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     float2 h[kVpt][P], sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
-      if (tid + j * kRow >= vectors) continue;
+      if (v0 + tid + j * kRow >= v1) continue;
       const int c0 = c_first + j * kRow * E;
       float2 w[P];
       Vec<T>::pairs(drop_mask_at<T, kRagged>(x[j * kRow], c0, row, key, rate), h[j]);
@@ -190,19 +207,27 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     auto total = [&](float m, int kind) {  // over the group; the barrier is the caller's
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (kRow > 32 && lane == 0) sums[kind][warp] = m;
+      if (kRow > 32 && lane == 0) {
+        sums[kind][rank * kWarps + warp] = m;
+        if constexpr (kCluster > 1) cluster_send(&sums[kind][rank * kWarps + warp], &met[kind], rank ^ 1, m);
+      }
       return m;
     };
     auto joined = [&](float m, int kind) {
       if constexpr (kRow == 32) return m;
+      if constexpr (kCluster > 1) {
+        // a thread that gives up here goes on with what there is and says so at the next barrier
+        late = !ptx::mbar_wait(&met[kind], (uint32_t)turn & 1, &abort, status, wait_ns) || late;
+        if (tid == 0) ptx::mbar_arrive_expect_tx(&met[kind], kWarps * sizeof(float));
+      }
       m = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m += sums[kind][w];
+      for (int w = 0; w < kParts; ++w) m += sums[kind][w];
       return m;
     };
     float m = total(sum.x + sum.y, 0);
     // the barrier also says that every warp is done with the stage
-    if (group_any<kRow, kGroups>(group, !mine)) { ok = false; break; }
+    if (group_any<kRow, kGroups>(group, !mine || late)) { ok = false; break; }
     const bool refill = turn + stages < turns;
     if (tid == 0 && refill) issue(s, issued++);
     T edge[kEdge];
@@ -216,7 +241,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
-      if (tid + j * kRow >= vectors) continue;
+      if (v0 + tid + j * kRow >= v1) continue;
       const int c0 = c_first + j * kRow * E;
       if (h_to) {
         store(h_to + j * kRow * E, c0, Vec<T>::pack(h[j]));
@@ -238,13 +263,13 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     group_any<kRow, kGroups>(group, false);
     const float rstd = 1.f / sqrtf(joined(m, 1) * inv + a.p.eps);
     const float2 scale2 = make_float2(rstd, rstd);
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
       if (a.mean) a.mean[first + turn * step] = mean;
       if (a.rstd) a.rstd[first + turn * step] = rstd;
     }
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) {
-      if (tid + j * kRow >= vectors) continue;
+      if (v0 + tid + j * kRow >= v1) continue;
       const int c0 = c_first + j * kRow * E;
       float2 g[P], b[P];
       if constexpr (!kKeep) {
@@ -267,11 +292,16 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     row += (uint32_t)step;
     if (++s == stages) s = 0, phase ^= 1;
   }
+  if constexpr (kCluster > 1) ok = !__syncthreads_or(late) && ok;
   if (!ok && tid == 0) {  // copies that this group issued and did not wait for
     ptx::Abort none;
     none.flag = 0;
     for (int j = turn; j < issued; ++j)
       ptx::mbar_wait(&full[j % stages], (uint32_t)((j / stages) & 1), &none, status, wait_ns);
+  }
+  if constexpr (kCluster > 1) {  // the other block may still send its sums here
+    __syncwarp();
+    cluster_barrier();
   }
 }
 
@@ -414,25 +444,39 @@ void launch_drop_warp(const LnDropArgs& a, bool ragged, cudaStream_t st, cudaErr
   *error = cudaGetLastError();
 }
 
-template <class T, int kRow, int kGroups, int kVpt, int kBlocks>
+template <class T, int kRow, int kGroups, int kVpt, int kBlocks, int kCluster>
 bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
                  cudaError_t* error) {
   constexpr int kSms = 152;
-  const int slots = (int)((a.p.cols + Vec<T>::E - 1) / Vec<T>::E) + (ragged ? 1 : 0);
+  const int vectors = (int)((a.p.cols + Vec<T>::E - 1) / Vec<T>::E) + (ragged ? 1 : 0);
+  const int slots = (vectors + kCluster - 1) / kCluster;
   const int stage = slots * 16 * (a.r ? 2 : 1);
   // an SM's shared memory over its blocks, less what they hold beside the ring
   const int stages = std::min(kMaxStages, (224 * 1024 / kBlocks - 2048) / kGroups / stage);
   if (stages < 2) return false;
   int groups = 1;  // where rows are few, on as many SMs as there are
   while (groups < kGroups && (a.p.rows + groups - 1) / groups > kSms) groups *= 2;
-  // rows of a group are a multiple of 8 apart wherever it has more than one: the grids are multiples of 8
-  const int blocks = (int)std::min<int64_t>((a.p.rows + groups - 1) / groups, kBlocks * kSms);
+  // rows of a group are a multiple of 8 apart (4 of the 4-byte type) wherever it has more than one: 304 or 152
+  // blocks, 76 clusters or 72
+  int most = kBlocks * kSms / kCluster;
+  if (ragged && most % (int)(16 / sizeof(T)) != 0) most = most / 8 * 8;
+  const int units = (int)std::min<int64_t>((a.p.rows + groups - 1) / groups, most);
   const size_t smem = (size_t)groups * stages * stage;
-  auto kernel = ragged ? k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, true> : k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, false>;
+  auto kernel = ragged ? k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, kCluster, true>
+                       : k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, kCluster, false>;
   *error = allow_shared(kernel, smem);
   if (*error != cudaSuccess) return true;
-  kernel<<<blocks, kRow * groups, smem, st>>>(a, stages, slots, status, wait_ns);
-  *error = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)units * kCluster);
+  cfg.blockDim = dim3(kRow * groups);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = kCluster, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = kCluster > 1 ? 1 : 0;
+  *error = cudaLaunchKernelEx(&cfg, kernel, a, stages, slots, status, wait_ns);
   return true;
 }
 
@@ -446,12 +490,17 @@ bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long
   if (m <= 8) return launch_drop_warp<T, 8, kRows>(a, ragged, st, error), true;
   if (m <= 16) return launch_drop_warp<T, 16, kRows>(a, ragged, st, error), true;
   if (m <= 32) return launch_drop_warp<T, 32, kRows>(a, ragged, st, error), true;
-  if (m <= 64) return launch_drop<T, 32, 8, 2, 2>(a, ragged, status, wait_ns, st, error);
-  if (m <= 128) return launch_drop<T, 64, 4, 2, 2>(a, ragged, status, wait_ns, st, error);
-  if (m <= 256) return launch_drop<T, 128, 2, 2, 2>(a, ragged, status, wait_ns, st, error);
-  if (m <= 512) return launch_drop<T, 256, 1, 2, 2>(a, ragged, status, wait_ns, st, error);
-  if (m <= 1024) return launch_drop<T, 512, 1, 2, 1>(a, ragged, status, wait_ns, st, error);
-  if (m <= 2048) return launch_drop<T, 512, 1, 4, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 64) return launch_drop<T, 32, 8, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 128) return launch_drop<T, 64, 4, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 256) return launch_drop<T, 128, 2, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 512) return launch_drop<T, 256, 1, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 1024) return launch_drop<T, 512, 1, 2, 1, 1>(a, ragged, status, wait_ns, st, error);
+  if constexpr (Vec<T>::E == 8) {
+    if (m <= 2048) return launch_drop<T, 512, 1, 2, 1, 2>(a, ragged, status, wait_ns, st, error);
+  } else {
+    if (m <= 2048) return launch_drop<T, 512, 1, 4, 1, 1>(a, ragged, status, wait_ns, st, error);
+    if (m <= 4096) return launch_drop<T, 512, 1, 4, 1, 2>(a, ragged, status, wait_ns, st, error);
+  }
   return false;
 }
 

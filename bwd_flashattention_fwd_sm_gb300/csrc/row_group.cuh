@@ -1,9 +1,11 @@
-// Groups of threads that share a row, several of them in a block.
+// Groups of threads that share a row, several of them in a block; blocks of a cluster that do.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+
+#include "ptx.cuh"
 
 namespace gbattn {
 
@@ -36,6 +38,27 @@ __device__ __forceinline__ bool group_any(int group, bool x) {
         : "memory");
     return r != 0;
   }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// x to the place of `here`, and 4 bytes to the count of the barrier at the place of `bar`, in the
+// block `rank` of the cluster.  (Not a cluster barrier: that would wait for the stores of dr and dx.)
+__device__ __forceinline__ void cluster_send(void* here, uint64_t* bar, uint32_t rank, float x) {
+  uint32_t to, count;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(here)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(count) : "r"(ptx::smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(to),
+               "r"(__float_as_uint(x)), "r"(count)
+               : "memory");
 }
 
 }  // namespace gbattn

@@ -256,7 +256,8 @@ def inp_dtype(dt):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(3, 7), (64, 1000), (128, 4096), (33, 4104), (8, 16384), (5, 2049), (11, 8192),
-                                   (2000, 64), (1001, 101), (700, 128), (5000, 250), (40, 30), (3, 16), (9, 300), (50, 520)],
+                                   (2000, 64), (1001, 101), (700, 128), (5000, 250), (40, 30), (3, 16), (9, 300), (50, 520), (400, 16384), (301, 16370), (90, 12290),
+                                   (3, 9000)],
                          ids=lambda s: f"{s[0]}x{s[1]}")
 def test_forward_with_dropout(shape, dtype):
     rows, cols = shape
