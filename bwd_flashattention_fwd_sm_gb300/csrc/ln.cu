@@ -238,18 +238,15 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
             v[j][e] = 0.f;
             if (c0 + e < cols) {
               v[j][e] = Vec<T>::load1(xr + c0 + e);
+              if (!kDrop) v[j][e] += rr ? Vec<T>::load1(rr + c0 + e) : 0.f;
               ++cnt;
             }
           }
           if constexpr (kDrop) {
             Vec<T>::unpack(drop_mask<T>(Vec<T>::pack(v[j]), (uint32_t)c0, (uint32_t)row, key, rate), v[j]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[j][e] *= rate.factor;
-          }
-          if (rr) {
-#pragma unroll
             for (int e = 0; e < E; ++e)
-              if (c0 + e < cols) v[j][e] += Vec<T>::load1(rr + c0 + e);
+              if (c0 + e < cols) v[j][e] = v[j][e] * rate.factor + (rr ? Vec<T>::load1(rr + c0 + e) : 0.f);
           }
         }
       }
