@@ -686,7 +686,8 @@ cudaError_t launch_sums(const EmbedArgs& a, cudaStream_t st) {
     const int stretches = (int)((a.dim + kSumThreads * N * kLoads - 1) / (kSumThreads * N * kLoads));
     // zeros: four vectors a thread at least
     const int64_t bytes = a.vocab * a.dim * (int64_t)sizeof(W);  // below 2^53
-    const int64_t filling = a.accumulate ? 0 : std::min<int64_t>((bytes + 64 * kFewThreads - 1) / (64 * kFewThreads), 4 * kSms);
+    const int64_t most = a.accumulate ? 0 : 4 * kSms;
+    const int64_t filling = std::min<int64_t>((bytes + 64 * kFewThreads - 1) / (64 * kFewThreads), most);
     k_embed_few<T, W, N, kLoads><<<(unsigned)(a.tokens * stretches + filling), kFewThreads, 0, st>>>(a, stretches);
     return cudaGetLastError();
   }
@@ -841,7 +842,8 @@ attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* d
       while (p->vocab >> bits) ++bits;
       a.passes = (bits + kMaxBits - 1) / kMaxBits;
       a.bits = std::max((bits + a.passes - 1) / a.passes, 7);  // 128 counts: a vector a lane
-      e = for_table(wsize == 2, n_w, [&](auto w, auto n) { return launch_sort<decltype(w), decltype(n)::value>(a, st); });
+      e = for_table(wsize == 2, n_w,
+                    [&](auto w, auto n) { return launch_sort<decltype(w), decltype(n)::value>(a, st); });
       if (e != cudaSuccess) return efail(ATTN_ERR_CUDA, "sort launch failed");
     }
     // one width for dy's elements and the table's: both addresses have to allow it

@@ -140,7 +140,6 @@ struct LnArgs {
   float* mean;
   float* rstd;
   int vec;  // every pointer (gamma, beta included) 16-byte aligned and every stride a whole number of vectors
-  DropArgs drop;  // of x, where the kernel's kDrop says so
 };
 
 // gamma and beta of columns c0 .. c0 + E - 1 (1 and 0 when absent), as float4
@@ -170,7 +169,7 @@ __device__ __forceinline__ void affine(const LnArgs& a, int64_t c0, int64_t cols
 // kVpt: 16-byte vectors per thread (cols <= 256 * kVpt * E).  Short rows leave
 // registers to spare: several CTAs per SM then keep more loads in flight.
 template <class T, int kVpt, bool kDrop>
-__global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4)) k_ln_residual(const LnArgs a) {
+__global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4)) k_ln_residual(const LnArgs a, const DropArgs drop) {
   constexpr int E = Vec<T>::E;
   __shared__ Stats warp_stats[kThreadsLn / 32];
   __shared__ Stats row_stats;
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
   T* H = static_cast<T*>(a.h);
   DropKey key{};
   DropRate rate{};
-  if constexpr (kDrop) key = drop_key(a.drop), rate = drop_rate(a.drop);
+  if constexpr (kDrop) key = drop_key(drop), rate = drop_rate(drop);
   for (int64_t row = blockIdx.x; row < a.p.rows; row += gridDim.x) {
     const T* xr = X + row * a.p.x_stride;
     const T* rr = R ? R + row * a.p.r_stride : nullptr;
@@ -237,8 +236,7 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
           for (int e = 0; e < E; ++e) {
             v[j][e] = 0.f;
             if (c0 + e < cols) {
-              v[j][e] = Vec<T>::load1(xr + c0 + e);
-              if (!kDrop) v[j][e] += rr ? Vec<T>::load1(rr + c0 + e) : 0.f;
+              v[j][e] = Vec<T>::load1(xr + c0 + e) + (rr && !kDrop ? Vec<T>::load1(rr + c0 + e) : 0.f);
               ++cnt;
             }
           }
@@ -305,13 +303,13 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
 
 // Persistent grid: as many CTAs as fit on the SMs at once (at most one per row).
 template <class T, int kVpt, bool kDrop>
-cudaError_t launch_ln_v(const LnArgs& a, int sms, cudaStream_t st) {
+cudaError_t launch_ln_v(const LnArgs& a, const DropArgs& drop, int sms, cudaStream_t st) {
   int per_sm = 1;
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_ln_residual<T, kVpt, kDrop>, kThreadsLn, 0);
   if (e != cudaSuccess) return e;
   const int64_t want = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
   const int grid = (int)(a.p.rows < want ? a.p.rows : want);
-  k_ln_residual<T, kVpt, kDrop><<<grid, kThreadsLn, 0, st>>>(a);
+  k_ln_residual<T, kVpt, kDrop><<<grid, kThreadsLn, 0, st>>>(a, drop);
   return cudaGetLastError();
 }
 
@@ -443,7 +441,8 @@ __global__ void __launch_bounds__(kThreadsLn, ring_ctas<kVpt>()) k_ln_ring(const
 }
 
 template <class T, bool kDrop>
-cudaError_t launch_ln(const LnArgs& a, int sms, int* status, unsigned long long wait_ns, cudaStream_t st) {
+cudaError_t launch_ln(const LnArgs& a, const DropArgs& drop, int sms, int* status, unsigned long long wait_ns,
+                      cudaStream_t st) {
   constexpr int E = Vec<T>::E;
   const int64_t per = (a.p.cols + (int64_t)kThreadsLn * E - 1) / ((int64_t)kThreadsLn * E);
   const uint32_t row_bytes = (uint32_t)(a.p.cols * (int64_t)sizeof(T));
@@ -474,11 +473,11 @@ cudaError_t launch_ln(const LnArgs& a, int sms, int* status, unsigned long long 
     if (per <= 4) return launch(k_ln_ring<T, 4>);
     return launch(k_ln_ring<T, 8>);
   }
-  if (per <= 1) return launch_ln_v<T, 1, kDrop>(a, sms, st);
-  if (per <= 2) return launch_ln_v<T, 2, kDrop>(a, sms, st);
-  if (per <= 4) return launch_ln_v<T, 4, kDrop>(a, sms, st);
-  if (per <= 8) return launch_ln_v<T, 8, kDrop>(a, sms, st);
-  if (per <= 16) return launch_ln_v<T, 16, kDrop>(a, sms, st);
+  if (per <= 1) return launch_ln_v<T, 1, kDrop>(a, drop, sms, st);
+  if (per <= 2) return launch_ln_v<T, 2, kDrop>(a, drop, sms, st);
+  if (per <= 4) return launch_ln_v<T, 4, kDrop>(a, drop, sms, st);
+  if (per <= 8) return launch_ln_v<T, 8, kDrop>(a, drop, sms, st);
+  if (per <= 16) return launch_ln_v<T, 16, kDrop>(a, drop, sms, st);
   return cudaErrorInvalidValue;
 }
 
@@ -512,9 +511,10 @@ extern "C" attn_status_t ln_dropout_residual_fwd(const ln_params_t* p, const ln_
   if (bad_stride(p->x_stride, true) || bad_stride(p->y_stride, true) || bad_stride(p->r_stride, residual != nullptr) ||
       bad_stride(p->h_stride, h != nullptr))
     return ln_fail(ATTN_ERR_INVALID_ARG, "ln_residual_fwd: a row stride is below cols");
-  LnArgs a{*p, x, residual, gamma, beta, y, h, mean, rstd, 0, {}};
+  LnArgs a{*p, x, residual, gamma, beta, y, h, mean, rstd, 0};
+  DropArgs drop{};
   bool drops = false;
-  if (const char* wrong = resolve_dropout(d, &a.drop, &drops)) return ln_fail(ATTN_ERR_INVALID_ARG, wrong);
+  if (const char* wrong = resolve_dropout(d, &drop, &drops)) return ln_fail(ATTN_ERR_INVALID_ARG, wrong);
   if (drops && p->rows >= (int64_t)1 << 32)
     return ln_fail(ATTN_ERR_UNSUPPORTED, "ln_residual_fwd: dropout of 2^32 rows or more");
   if (p->rows == 0) return ATTN_OK;
@@ -544,18 +544,18 @@ extern "C" attn_status_t ln_dropout_residual_fwd(const ln_params_t* p, const ln_
                     stride == p->x_stride);
     };
     if (whole || (alike(residual, p->r_stride) && alike(y, p->y_stride) && alike(h, p->h_stride))) {
-      const LnDropArgs d{*p, x, residual, gamma, beta, y, h, mean, rstd, a.drop};
+      const LnDropArgs d{*p, x, residual, gamma, beta, y, h, mean, rstd, drop};
       const bool taken = p->dtype == ATTN_BF16 ? launch_ln_drop<__nv_bfloat16>(d, !whole, status, wait_ns, st, &e)
                                                : launch_ln_drop<float>(d, !whole, status, wait_ns, st, &e);
       if (taken) return e == cudaSuccess ? ATTN_OK : ln_fail(ATTN_ERR_CUDA, "ln_residual_fwd: launch failed");
     }
   }
   if (p->dtype == ATTN_BF16)
-    e = drops ? launch_ln<__nv_bfloat16, true>(a, sms, status, wait_ns, st)
-              : launch_ln<__nv_bfloat16, false>(a, sms, status, wait_ns, st);
+    e = drops ? launch_ln<__nv_bfloat16, true>(a, drop, sms, status, wait_ns, st)
+              : launch_ln<__nv_bfloat16, false>(a, drop, sms, status, wait_ns, st);
   else
-    e = drops ? launch_ln<float, true>(a, sms, status, wait_ns, st)
-              : launch_ln<float, false>(a, sms, status, wait_ns, st);
+    e = drops ? launch_ln<float, true>(a, drop, sms, status, wait_ns, st)
+              : launch_ln<float, false>(a, drop, sms, status, wait_ns, st);
   if (e != cudaSuccess) return ln_fail(ATTN_ERR_CUDA, "ln_residual_fwd: launch failed");
   return ATTN_OK;
 }

@@ -2,8 +2,8 @@
 // type; ln.cu has the entry, and the form without dropout.
 //
 // A row belongs to a group of kRow threads, kVpt vectors each, and a block holds kGroups such
-// groups (rows of up to 32 vectors: to some lanes of a warp).  Rows stream through a ring of stages in shared memory that bulk copies fill some rows
-// ahead.  h is made once and stays in registers; its mean and then the sum of its squared
+// groups (rows of up to 32 vectors: some lanes of a warp, without the ring).  Rows stream through a
+// ring of stages in shared memory that bulk copies fill some rows ahead.  h is made once and stays in registers; its mean and then the sum of its squared
 // distances from that mean are two sums over the group, so nothing cancels.  Bound by device memory
 // at long rows; the mask (some 60 instructions for eight elements) and the two barriers a row are next.
 // Rows of more than 8192 columns: two blocks of a cluster, which send each other their warps' sums.

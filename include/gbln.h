@@ -79,8 +79,9 @@ typedef struct {
 /*
  * y = D(x) over [rows, cols] (x_stride, y_stride; the other strides and eps are not
  * looked at), and, on a gradient, dropout's backward pass.  y may be x itself (with
- * y_stride == x_stride); other rows that share an element are refused.  rows and cols below 2^32.  d must not be NULL.  D is taken
- * in float32 and rounded once.  16-byte vectors as above.
+ * y_stride == x_stride); other rows that share an element are refused.  rows and cols
+ * below 2^32.  d must not be NULL.  D is taken in float32 and rounded once.  16-byte
+ * vectors as above.
  */
 attn_status_t ln_dropout(const ln_params_t* p, const ln_dropout_t* d, const void* x, void* y, void* stream);
 

@@ -85,8 +85,8 @@ def run(inp, **kw):
     return layernorm_residual_bwd(d["dy"], d["h"], d["mean"], d["rstd"], d["gamma"], d["dh"], **kw)
 
 
-SHAPES = [(130000, 1), (64, 2048), (65, 2048), (128, 1024), (131, 1001), (8, 16380), (16, 4097), (1, 1), (2, 3), (3, 7), (1, 16), (300, 64), (9, 100), (33, 256), (7, 257), (64, 1000), (17, 1024), (5, 1030),
-          (40, 2048), (23, 2049), (128, 4096), (33, 4104), (19, 5000), (12, 8192), (6, 8200), (4, 12289), (8, 16384),
+SHAPES = [(130000, 1), (64, 2048), (65, 2048), (128, 1024), (131, 1001), (8, 16380), (16, 4097), (1, 1), (2, 3), (3, 7),
+          (1, 16), (300, 64), (9, 100), (33, 256), (7, 257), (64, 1000), (17, 1024), (5, 1030), (40, 2048), (23, 2049), (128, 4096), (33, 4104), (19, 5000), (12, 8192), (6, 8200), (4, 12289), (8, 16384),
           (5, 16383), (3000, 48), (700, 520)]
 
 
@@ -256,8 +256,8 @@ def inp_dtype(dt):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(3, 7), (64, 1000), (128, 4096), (33, 4104), (8, 16384), (5, 2049), (11, 8192),
-                                   (2000, 64), (1001, 101), (700, 128), (5000, 250), (40, 30), (3, 16), (9, 300), (50, 520), (400, 16384), (301, 16370), (90, 12290),
-                                   (3, 9000)],
+                                   (2000, 64), (1001, 101), (700, 128), (5000, 250), (40, 30), (3, 16), (9, 300),
+                                   (50, 520), (400, 16384), (301, 16370), (90, 12290), (3, 9000)],
                          ids=lambda s: f"{s[0]}x{s[1]}")
 def test_forward_with_dropout(shape, dtype):
     rows, cols = shape

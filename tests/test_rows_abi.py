@@ -214,7 +214,8 @@ def test_bindings_refuse_host_tensors_and_bad_arguments():
 def test_rows_of_a_view():
     """A tensor whose rows are a fixed number of elements apart is used as it is, another copied."""
     base = torch.arange(2 * 3 * 4 * 10.0).reshape(2, 3, 4, 10)
-    for view, step in ((base, 10), (base[..., :7], 10), (base[:, :, 1], 40), (base[:, 1, 2], 120), (base[0, 0, 0], 10), (base[:1, :1, :1, :5], 5), (base[..., :1], 10)):
+    for view, step in ((base, 10), (base[..., :7], 10), (base[:, :, 1], 40), (base[:, 1, 2], 120),
+                       (base[0, 0, 0], 10), (base[:1, :1, :1, :5], 5), (base[..., :1], 10)):
         rows, stride = as_rows(view, view.shape[-1])
         flat = view.reshape(-1, view.shape[-1])
         got = rows.as_strided(flat.shape, (stride, 1)) if flat.shape[0] > 1 else rows.reshape(flat.shape)
