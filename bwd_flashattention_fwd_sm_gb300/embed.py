@@ -69,7 +69,8 @@ def embedding_bwd(dy, ids, num_embeddings: int, *, scale: float = 1.0, padding_i
     _check_ids(ids, device)
     if dy.shape[:-1] != ids.shape:
         raise ValueError(f"dy {tuple(dy.shape)} does not match ids {tuple(ids.shape)}")
-
+    if padding_id is not None and padding_id < 0:
+        raise ValueError(f"padding_id={padding_id}: must be a token (not counted from the table's end) or None")
     if stream is not None or device.index != current_device():
         with elsewhere(device, stream, (dy, ids, workspace, out)):
             return embedding_bwd(dy, ids, num_embeddings, scale=scale, padding_id=padding_id, dtype=grad,

@@ -269,3 +269,12 @@ def test_streams_and_graphs():
         assert torch.equal(y, w[ids])
         assert torch.equal(dw, embedding_bwd(dy, ids, vocab))
     assert get_status() == 0
+
+
+def test_refuses_a_padding_token_below_zero():
+    """It would name no token, nor the table's last row."""
+    dy, ids = torch.ones(3, 8, device="cuda"), torch.tensor([0, 3, 1], device="cuda")
+    for pad in (-1, -100):
+        with pytest.raises(ValueError, match="padding_id"):
+            embedding_bwd(dy, ids, 4, padding_id=pad)
+    check_grad(embedding_bwd(dy, ids, 4, padding_id=3), dy, ids, 4, 1.0, 3)
