@@ -405,6 +405,9 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
   constexpr bool kKeepGamma = kVpt * E <= 16;       // registers allow it
   constexpr int kEdge = (6 * E + kRow - 1) / kRow;  // elements at a row's ends, of one thread
   static_assert(kCluster == 1 || kGroups == 1, "one row of a cluster");
+  // of the longest rows, with dh; two: float32 rows of more than 6308 columns of a block, or 12620 of two
+  constexpr int kLeastStages = ring_stages(kBlocks, kGroups, kRow * kVpt * 16 * 3);
+  static_assert(kLeastStages >= 2, "a stage is read while another is filled");
   extern __shared__ __align__(128) uint8_t ring[];  // [groups][stages][2 or 3][slots] vectors
   __shared__ uint64_t full_all[kGroups][kMaxStages];
   __shared__ uint64_t met[2];  // the other block's sums have come, by the row's parity
@@ -646,10 +649,15 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
         store(dx + j * kRow * E, out);
       }
     }
-    if constexpr (kRagged) {  // read only after the next barriers
-      if (refill)
+    if constexpr (kRagged) {
+      if (refill) {
 #pragma unroll
         for (int k = 0; k < kEdge; ++k) edge_store(k, last, edge[k]);
+        // Other threads read these elements.  The next turn's barrier stands between where the stage is that of a
+        // later turn; of two stages it is the next turn's, which is read in front of that barrier.
+        if constexpr (kLeastStages < 3)
+          if (stages < 3) group_any<kRow, kGroups>(group, false);
+      }
     }
     if (dr) dr += dr_step;
     if (dx) dx += dx_step;
@@ -769,8 +777,7 @@ cudaError_t launch_ring(const BwdLnArgs& a, bool drops, bool ragged, int* parts,
   *parts = (int)std::min<int64_t>(div_up(a.p.rows, groups), most);
   const int slots = (int)div_up(div_up(a.p.cols, Vec<T>::E) + (ragged ? 1 : 0), kCluster);
   const int stage = slots * 16 * (a.dh ? 3 : 2);
-  // an SM's shared memory over its blocks, less what they hold beside the ring
-  const int stages = std::min(kMaxStages, (224 * 1024 / kBlocks - 2048) / kGroups / stage);
+  const int stages = ring_stages(kBlocks, kGroups, stage);
   const size_t smem = (size_t)groups * stages * stage;
   auto kernel = ragged ? (drops ? k_ln_bwd_ring<T, kRow, kGroups, kVpt, kBlocks, kCluster, true, true>
                                 : k_ln_bwd_ring<T, kRow, kGroups, kVpt, kBlocks, kCluster, false, true>)

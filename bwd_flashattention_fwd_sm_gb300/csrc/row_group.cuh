@@ -11,6 +11,13 @@ namespace gbattn {
 
 constexpr int kMaxStages = 8;  // of a group's ring
 
+// Stages of a ring whose stage takes `stage_bytes`: an SM's shared memory over its blocks, less what they hold beside
+// the ring, over a block's groups.
+__host__ __device__ constexpr int ring_stages(int blocks, int groups, int stage_bytes) {
+  const int n = (224 * 1024 / blocks - 2048) / groups / stage_bytes;
+  return n < kMaxStages ? n : kMaxStages;
+}
+
 // Lets a kernel take `smem` bytes of dynamic shared memory.  Always the same limit, because calls from two
 // threads may set it in turn before either launches.
 template <class K>
