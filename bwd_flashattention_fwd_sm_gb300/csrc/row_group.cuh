@@ -26,10 +26,11 @@ cudaError_t allow_shared(K kernel, size_t smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
 }
 
-// Whether x holds for any of a group's kRow threads; a barrier of the group.
+// Whether x holds for any of a group's kRow threads; a barrier of the group, which orders their memory too.
 template <int kRow, int kGroups>
 __device__ __forceinline__ bool group_any(int group, bool x) {
   if constexpr (kRow == 32) {
+    __syncwarp();  // a vote orders no memory
     return __any_sync(0xffffffffu, x);
   } else if constexpr (kGroups == 1) {
     return __syncthreads_or(x);
