@@ -458,7 +458,7 @@ cudaError_t launch_ln(const LnArgs& a, const DropArgs& drop, int sms, int* statu
   if (!kDrop && a.vec && a.p.cols % E == 0 && stages >= 2 && per > 2 && per <= 8) {
     auto launch = [&](auto kernel) -> cudaError_t {
       const size_t smem = (size_t)stages * stage_bytes;
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaError_t e = allow_shared(kernel, smem);
       if (e != cudaSuccess) return e;
       int per_sm = 1;
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreadsLn, smem);
