@@ -51,12 +51,15 @@ class elsewhere:
         if stream is not None:
             self._tensors = [t for t in tensors if t is not None]
             self._on = stream
+            for t in self._tensors:
+                if t.device != device:
+                    raise ValueError(f"a tensor is on {t.device}, the others on {device}")
 
     def __enter__(self):
+        for t in self._tensors:  # first: what raises here must leave device and stream as they were
+            t.record_stream(self._on)
         self._device.__enter__()
         self._stream.__enter__()
-        for t in self._tensors:
-            t.record_stream(self._on)
 
     def __exit__(self, *error):
         self._stream.__exit__(*error)
