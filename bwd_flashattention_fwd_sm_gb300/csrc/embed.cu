@@ -287,7 +287,7 @@ __device__ void sort_places(const EmbedArgs& a, uint32_t* count) {
 // The first cluster sorts, the other blocks write zeros.
 template <class W, int N>
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedArgs a) {
-  extern __shared__ uint32_t count[];  // [kSortWarps][digits], and pairs [kSortWarps][kHeld * 32]
+  extern __shared__ __align__(16) uint32_t count[];  // [kSortWarps][digits], and pairs [kSortWarps][kHeld * 32]
   const unsigned sorting = cg::this_cluster().num_blocks();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x < sorting)
