@@ -35,7 +35,8 @@ def dropout(x, p: float, *, seed: int = 0, offset: int = 0, rng=None, stream=Non
     together) and the column: the same numbers give the same mask, here and in layernorm_residual and its
     backward pass; each dropout of a step needs an offset of its own.  rng: an int64 CUDA
     tensor (seed, offset), added to the two (modulo 2^64) and read on the device when the kernel runs, so
-    that a captured graph follows new values in it.  out: a contiguous tensor like x, which may be x itself."""
+    that a captured graph follows new values in it.  The sums decide: where a step's dropouts have the offsets
+    0 .. n - 1, rng's offset has to grow by n at least from step to step, or masks come again.  out: a contiguous tensor like x, which may be x itself."""
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     dtype = DTYPES.get(x.dtype)

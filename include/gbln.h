@@ -69,6 +69,9 @@ attn_status_t ln_residual_fwd(const ln_params_t* p, const void* x, const void* r
  * NULL, of the pair {seed, offset} in device memory that the kernel reads when it
  * runs: a captured graph drops anew when that pair is changed between replays.  The
  * backward pass needs the values of the forward pass.
+ * The same sums give the same mask, so every dropout of every step needs sums of its own.  With
+ * member offsets 0 .. n - 1 in a step's dropouts, the pair's offset has to grow by n at least from
+ * step to step (2^32 is simple): growing by 1, dropout k of a step has the mask of dropout k - 1 of the next.
  */
 typedef struct {
   double p;            /* probability of being dropped, 0 <= p <= 1 */
