@@ -15,6 +15,7 @@
 #include "../../include/gbln.h"
 #include "common.cuh"
 #include "dropout.cuh"
+#include "overlap.h"
 #include "rowvec.cuh"
 
 namespace gbattn {
@@ -165,21 +166,6 @@ cudaError_t launch_dropout(DropoutArgs a, bool whole, int sms, cudaStream_t st) 
   return launch_places(k_dropout_any<T>, a, kWarps, sms, st);
 }
 
-// Whether rows of x and y (of cols elements of `size` bytes) share an element, x and y not being the same rows.
-bool share(const void* x, int64_t xs, const void* y, int64_t ys, int64_t rows, int64_t cols, int64_t size) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  if (rows == 1) xs = ys = cols;
-  if (a == b && xs == ys) return false;
-  const __int128 a_end = (__int128)a + ((__int128)(rows - 1) * xs + cols) * size;
-  const __int128 b_end = (__int128)b + ((__int128)(rows - 1) * ys + cols) * size;
-  if (a_end <= (__int128)b || b_end <= (__int128)a) return false;
-  if (xs != ys) return true;
-  // rows of one lie between those of the other, or they meet
-  const __int128 step = (__int128)xs * size, apart = ((__int128)b - (__int128)a) % step;
-  const __int128 ahead = apart < 0 ? apart + step : apart;
-  return ahead < cols * size || step - ahead < cols * size;
-}
-
 attn_status_t dfail(attn_status_t s, const char* msg) {
   set_last_error_text(msg);
   return s;
@@ -206,7 +192,9 @@ extern "C" attn_status_t ln_dropout(const ln_params_t* p, const ln_dropout_t* d,
   const uintptr_t esize = p->dtype == ATTN_BF16 ? 2 : 4;
   const uintptr_t at = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y);
   if (at & (esize - 1)) return dfail(ATTN_ERR_INVALID_ARG, "ln_dropout: a pointer is not aligned to its element size");
-  if (share(x, p->x_stride, y, p->y_stride, p->rows, p->cols, (int64_t)esize))
+  const int64_t width = p->cols * (int64_t)esize;
+  const RowSpan from{x, p->rows, p->x_stride * (int64_t)esize, width}, to{y, p->rows, p->y_stride * (int64_t)esize, width};
+  if (rows_meet(from, to) && !same_rows(from, to))
     return dfail(ATTN_ERR_INVALID_ARG, "ln_dropout: x and y overlap and are not the same rows");
   const bool whole =
       p->cols % 8 == 0 && ((at | (uintptr_t)p->x_stride * esize | (uintptr_t)p->y_stride * esize) & 15) == 0;

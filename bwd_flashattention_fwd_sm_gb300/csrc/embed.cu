@@ -24,6 +24,7 @@
 
 #include "../../include/gbembed.h"
 #include "common.cuh"
+#include "overlap.h"
 
 namespace gbattn {
 void set_last_error_text(const char* text);
@@ -607,6 +608,12 @@ attn_status_t check_params(const attn_embedding_params_t* p, bool backward) {
   return ATTN_OK;
 }
 
+// Whether rows `to`, which a call writes, share memory with the ids or with the rows `x` that it reads.
+bool meets_inputs(const attn_embedding_params_t& p, const RowSpan& to, const RowSpan& x, const void* ids) {
+  const int64_t bytes = p.tokens * (p.ids_64 ? 8 : 4);
+  return rows_meet(to, x) || rows_meet(to, RowSpan{ids, 1, bytes, bytes});
+}
+
 // Sorted places of a block: as many as leave some 1000 blocks (2000, where accesses are narrower and a place costs
 // more).  16384 tokens of [50000, 4096] bf16 take 105, 104 and 101 us with 16, 32 and 64; 20000 of [5000, 777] 32, 38 and
 // 50.  By sizes and types alone, because the workspace's size follows it.
@@ -774,6 +781,10 @@ attn_status_t attn_embedding_fwd(const attn_embedding_params_t* p, const void* w
   int sms = 0;
   unsigned long long wait_ns = 0;
   if ((s = device_status(&a.status, &sms, &wait_ns))) return s;
+  const int64_t width_y = p->dim * (int64_t)esize;
+  if (meets_inputs(*p, RowSpan{y, p->tokens, p->x_stride * (int64_t)esize, width_y},
+                   RowSpan{weight, p->vocab, p->w_stride * (int64_t)esize, width_y}, ids))
+    return efail(ATTN_ERR_INVALID_ARG, "y overlaps weight or ids");
   a.ids = ids, a.x = weight, a.y = y;
   a.tokens = p->tokens, a.vocab = p->vocab, a.dim = p->dim;
   a.x_stride = p->w_stride, a.y_stride = p->x_stride;
@@ -817,6 +828,12 @@ attn_status_t attn_embedding_bwd(const attn_embedding_params_t* p, const void* d
   int sms = 0;
   unsigned long long wait_ns = 0;
   if ((s = device_status(&a.status, &sms, &wait_ns))) return s;
+  const RowSpan dy_rows{dy, p->tokens, p->x_stride * (int64_t)esize, p->dim * (int64_t)esize};
+  const RowSpan dw_rows{dweight, p->vocab, p->w_stride * (int64_t)wsize, p->dim * (int64_t)wsize};
+  const RowSpan scratch{workspace, 1, (int64_t)need, (int64_t)need};
+  if (meets_inputs(*p, dw_rows, dy_rows, ids)) return efail(ATTN_ERR_INVALID_ARG, "dweight overlaps dy or ids");
+  if (meets_inputs(*p, scratch, dy_rows, ids) || rows_meet(scratch, dw_rows))
+    return efail(ATTN_ERR_WORKSPACE, "workspace overlaps another argument");
   a.ids = ids, a.x = dy, a.y = dweight;
   a.tokens = p->tokens, a.vocab = p->vocab, a.dim = p->dim;
   a.x_stride = p->x_stride, a.y_stride = p->w_stride;

@@ -14,7 +14,8 @@
  * aligned and every stride and dim whole vectors, else as 4-byte words or elements.
  *
  * Constraints.  tokens and vocab below 2^31 - 1, dim at most 2^20; strides >= dim; scale
- * finite; pointers aligned to their elements; outputs must not overlap inputs.  Offsets
+ * finite; pointers aligned to their elements; outputs and workspace must not overlap inputs or
+ * one another (refused; rows that lie between another tensor's rows do not overlap).  Offsets
  * are 64-bit.  Errors and asynchrony are as for gbattn.h.  An id outside [0, vocab) is
  * recorded as ATTN_ERR_DEVICE_BOUNDS (attn_get_status()) and nothing is read or written
  * for it: its row of y is 0, and no row of dW gets its dy.
