@@ -2,6 +2,8 @@
 // partial sums.  ln_bwd.cuh has the kernels.
 #include "ln_bwd.cuh"
 
+#include "overlap.h"
+
 namespace gbattn {
 void set_last_error_text(const char* text);
 attn_status_t device_status(int** status, int* sms, unsigned long long* wait_ns);
@@ -75,6 +77,27 @@ attn_status_t check_params(const ln_bwd_params_t* p) {
   return ATTN_OK;
 }
 
+// Whether something that the call writes shares memory with something else of it: the outputs dx and dr in place of
+// dy or dh are allowed, and one in place of the other where they are equal (drops is false).
+bool outputs_meet(const BwdLnArgs& a, bool drops, float* dgamma, float* dbeta, const void* workspace, size_t need) {
+  const int64_t size = a.p.dtype == ATTN_BF16 ? 2 : 4, width = a.p.cols * size, rows = a.p.rows;
+  auto line = [](const void* at, int64_t bytes) { return RowSpan{at, 1, bytes, bytes}; };
+  const int64_t stats = rows * 4, columns = a.p.cols * 4;
+  const RowSpan written[5] = {{a.dx, rows, a.p.dx_stride * size, width}, {a.dr, rows, a.p.dr_stride * size, width},
+                              line(dgamma, columns), line(dbeta, columns), line(workspace, (int64_t)need)};
+  const RowSpan read[6] = {{a.dy, rows, a.p.dy_stride * size, width}, {a.dh, rows, a.p.dh_stride * size, width},
+                           {a.h, rows, a.p.h_stride * size, width}, line(a.mean, stats), line(a.rstd, stats),
+                           line(a.gamma, columns)};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (rows_meet(written[i], read[j]) && !(i < 2 && j < 2 && same_rows(written[i], read[j]))) return true;
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(written[i], written[j]) && !(i == 1 && j == 0 && !drops && same_rows(written[i], written[j])))
+        return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace gbattn
 
@@ -126,6 +149,8 @@ attn_status_t ln_residual_bwd(const ln_bwd_params_t* p, const ln_dropout_t* d, c
   int sms = 0;
   unsigned long long wait_ns = 0;
   if ((s = device_status(&status, &sms, &wait_ns))) return s;
+  if (outputs_meet(a, drops, dgamma, dbeta, workspace, need))
+    return bfail(ATTN_ERR_INVALID_ARG, "ln_residual_bwd: an output or the workspace overlaps another argument");
   a.vec = ((at | reinterpret_cast<uintptr_t>(gamma)) & 15) == 0;
   if (weights && p->rows > 0) {
     if (ln_bwd_joins(*p))

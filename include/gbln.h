@@ -115,8 +115,8 @@ typedef struct {
  * order that sizes and alignment decide (the results are bit-identical from run to run).  A dy, h,
  * mean or rstd that is not finite reaches its row and the columns' sums; a dh its own element.
  *
- * Constraints as for ln_residual_fwd; outputs must not overlap inputs or one another,
- * except that dx or dr may be dy or dh itself, with the same stride.  workspace:
+ * Constraints as for ln_residual_fwd; outputs and workspace must not overlap inputs or one another
+ * (refused), except that dx or dr may be dy or dh itself, with the same stride, and without dropout dr itself dx.  workspace:
  * device scratch, 256-byte aligned, >= ln_residual_bwd_workspace_size(p) bytes (SIZE_MAX
  * if the parameters are invalid), not needed if dgamma and dbeta are NULL; calls that
  * may overlap need one each.
