@@ -165,7 +165,7 @@ __device__ __forceinline__ void affine(const LnArgs& a, int64_t c0, int64_t cols
   }
 }
 
-// kDrop: x goes through the dropout; for rows that k_ln_drop does not take (ln_drop.cuh).
+// kDrop: x goes through the dropout; for rows that k_ln_drop does not take (ln_drop.cuh), never whole vectors all along.
 // kVpt: 16-byte vectors per thread (cols <= 256 * kVpt * E).  Short rows leave
 // registers to spare: several CTAs per SM then keep more loads in flight.
 template <class T, int kVpt, bool kDrop>
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreadsLn, kVpt >= 8 ? 1 : (kVpt >= 4 ? 2 : 4
   const int64_t nvec = (cols + E - 1) / E;
   const bool ragged = cols % E != 0 || !a.vec;  // element loads where vectors do not fit
   // every thread holds kVpt whole vectors: summaries of equal counts throughout
-  const bool uniform = !ragged && nvec == (int64_t)kThreadsLn * kVpt;
+  const bool uniform = !kDrop && !ragged && nvec == (int64_t)kThreadsLn * kVpt;
   const T* X = static_cast<const T*>(a.x);
   const T* R = static_cast<const T*>(a.r);
   T* Y = static_cast<T*>(a.y);

@@ -445,15 +445,14 @@ void launch_drop_warp(const LnDropArgs& a, bool ragged, cudaStream_t st, cudaErr
 }
 
 template <class T, int kRow, int kGroups, int kVpt, int kBlocks, int kCluster>
-bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
+void launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
                  cudaError_t* error) {
   constexpr int kSms = 152;
+  static_assert(ring_stages(kBlocks, kGroups, kRow * kVpt * 16 * 2) >= 2, "a stage is read while another is filled");
   const int vectors = (int)((a.p.cols + Vec<T>::E - 1) / Vec<T>::E) + (ragged ? 1 : 0);
   const int slots = (vectors + kCluster - 1) / kCluster;
   const int stage = slots * 16 * (a.r ? 2 : 1);
-  // an SM's shared memory over its blocks, less what they hold beside the ring
-  const int stages = std::min(kMaxStages, (224 * 1024 / kBlocks - 2048) / kGroups / stage);
-  if (stages < 2) return false;
+  const int stages = ring_stages(kBlocks, kGroups, stage);
   int groups = 1;  // where rows are few, on as many SMs as there are
   while (groups < kGroups && (a.p.rows + groups - 1) / groups > kSms) groups *= 2;
   // rows of a group are a multiple of 8 apart (4 of the 4-byte type) wherever it has more than one: 304 or 152
@@ -465,7 +464,7 @@ bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long lo
   auto kernel = ragged ? k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, kCluster, true>
                        : k_ln_drop<T, kRow, kGroups, kVpt, kBlocks, kCluster, false>;
   *error = allow_shared(kernel, smem);
-  if (*error != cudaSuccess) return true;
+  if (*error != cudaSuccess) return;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)units * kCluster);
   cfg.blockDim = dim3(kRow * groups);
@@ -477,7 +476,6 @@ bool launch_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long lo
   cfg.attrs = &cluster;
   cfg.numAttrs = kCluster > 1 ? 1 : 0;
   *error = cudaLaunchKernelEx(&cfg, kernel, a, stages, slots, status, wait_ns);
-  return true;
 }
 
 }  // namespace
@@ -490,16 +488,16 @@ bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long
   if (m <= 8) return launch_drop_warp<T, 8, kRows>(a, ragged, st, error), true;
   if (m <= 16) return launch_drop_warp<T, 16, kRows>(a, ragged, st, error), true;
   if (m <= 32) return launch_drop_warp<T, 32, kRows>(a, ragged, st, error), true;
-  if (m <= 64) return launch_drop<T, 32, 8, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
-  if (m <= 128) return launch_drop<T, 64, 4, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
-  if (m <= 256) return launch_drop<T, 128, 2, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
-  if (m <= 512) return launch_drop<T, 256, 1, 2, 2, 1>(a, ragged, status, wait_ns, st, error);
-  if (m <= 1024) return launch_drop<T, 512, 1, 2, 1, 1>(a, ragged, status, wait_ns, st, error);
+  if (m <= 64) return launch_drop<T, 32, 8, 2, 2, 1>(a, ragged, status, wait_ns, st, error), true;
+  if (m <= 128) return launch_drop<T, 64, 4, 2, 2, 1>(a, ragged, status, wait_ns, st, error), true;
+  if (m <= 256) return launch_drop<T, 128, 2, 2, 2, 1>(a, ragged, status, wait_ns, st, error), true;
+  if (m <= 512) return launch_drop<T, 256, 1, 2, 2, 1>(a, ragged, status, wait_ns, st, error), true;
+  if (m <= 1024) return launch_drop<T, 512, 1, 2, 1, 1>(a, ragged, status, wait_ns, st, error), true;
   if constexpr (Vec<T>::E == 8) {
-    if (m <= 2048) return launch_drop<T, 512, 1, 2, 1, 2>(a, ragged, status, wait_ns, st, error);
+    if (m <= 2048) return launch_drop<T, 512, 1, 2, 1, 2>(a, ragged, status, wait_ns, st, error), true;
   } else {
-    if (m <= 2048) return launch_drop<T, 512, 1, 4, 1, 1>(a, ragged, status, wait_ns, st, error);
-    if (m <= 4096) return launch_drop<T, 512, 1, 4, 1, 2>(a, ragged, status, wait_ns, st, error);
+    if (m <= 2048) return launch_drop<T, 512, 1, 4, 1, 1>(a, ragged, status, wait_ns, st, error), true;
+    if (m <= 4096) return launch_drop<T, 512, 1, 4, 1, 2>(a, ragged, status, wait_ns, st, error), true;
   }
   return false;
 }
