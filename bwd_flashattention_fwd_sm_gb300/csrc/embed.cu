@@ -10,7 +10,7 @@
 // one piece over a stretch of columns: equal work however often a word comes.  A word
 // that lies inside one piece is written to the table at once; of one that
 // several pieces share each piece leaves a partial sum, and k_embed_join adds those in order.
-// No atomics on sums: their order follows from the ids alone.
+// No atomics on sums: their order follows from the ids, the sizes and the types.
 // Up to kFewTokens tokens take one launch and no workspace (k_embed_few): each block finds its word's places
 // by reading all ids.
 #include <cooperative_groups.h>

@@ -51,8 +51,8 @@ def embedding_bwd(dy, ids, num_embeddings: int, *, scale: float = 1.0, padding_i
     dy: bf16 or float32 [..., dim], ids: as in the lookup, of dy's leading shape.  padding_id: a token that
     gives no gradient.  dtype: the gradient's type, dy's own by default.  out: a tensor [num_embeddings, dim]
     with contiguous rows, apart from dy and ids, to add the gradient to (tied weights, several steps in one gradient); rows
-    that no token names are left as they are.  Sums are float32 in an order that ids alone decide: the same bits every
-    time.  An id outside the table is recorded as in the lookup and gives nothing.  workspace: as for attn_bwd."""
+    that no token names are left as they are.  Sums are float32 in an order that ids, sizes and types decide: the same bits
+    every time.  An id outside the table is recorded as in the lookup and gives nothing.  workspace: as for attn_bwd."""
     if not dy.is_cuda:
         raise ValueError("dy must be a CUDA tensor")
     device = dy.device

@@ -18,7 +18,8 @@
  * one another (refused; rows that lie between another tensor's rows do not overlap).  Offsets
  * are 64-bit.  Errors and asynchrony are as for gbattn.h.  An id outside [0, vocab) is
  * recorded as ATTN_ERR_DEVICE_BOUNDS (attn_get_status()) and nothing is read or written
- * for it: its row of y is 0, and no row of dW gets its dy.
+ * for it: its row of y is 0, and no row of dW gets its dy.  Where nothing is to be written (dim 0, dW of
+ * vocab 0) no id is looked at.
  */
 #ifndef GBEMBED_H
 #define GBEMBED_H
@@ -51,8 +52,8 @@ attn_status_t attn_embedding_fwd(const attn_embedding_params_t* p, const void* w
 /*
  * dweight of the lookup.  Without accumulate every row is written, 0 where no token
  * names it; with it only rows that a token names are read and written, one rounding
- * per call.  A row's tokens are added in float32 in a fixed order that depends on ids
- * alone: the result is bit-identical from run to run.  workspace: device scratch, 256-byte
+ * per call.  A row's tokens are added in float32 in a fixed order that ids, sizes and types
+ * decide: the result is bit-identical from run to run.  workspace: device scratch, 256-byte
  * aligned, >= attn_embedding_bwd_workspace_size(p) bytes (SIZE_MAX if the parameters
  * are invalid; 0 for few tokens); it keeps nothing from one call to the next, and calls that
  * may overlap need one each.
