@@ -804,7 +804,10 @@ cudaError_t launch_ln_bwd(const BwdLnArgs& a, bool drops, int* parts, int* statu
   const bool ragged = !(a.vec && a.p.cols % E == 0);
   const int64_t n = div_up(a.p.cols, E), m = n + (ragged ? 1 : 0);  // vectors of a row, at most
   if (!ragged || a.alike) {
-    constexpr int kRows = E == 8 ? 1 : 2;  // what 64 registers hold
+    // Rows of a lane in flight.  64 registers hold them in the plain form; dropping and ragged forms spill 24 to 168 bytes.
+    // bf16: [262144, 128] 49 us, 72 with two.  float32: [131072, 128] 44, 47 with one and 70 with four; dropping 62, 57 and
+    // 95; ragged [166000, 101] 68, 58 and 133.
+    constexpr int kRows = E == 8 ? 1 : 2;
     if (m <= 8) return launch_warp<T, 8, kRows>(a, drops, ragged, parts, st);
     if (m <= 16) return launch_warp<T, 16, kRows>(a, drops, ragged, parts, st);
     if (m <= 32) return launch_warp<T, 32, kRows>(a, drops, ragged, parts, st);

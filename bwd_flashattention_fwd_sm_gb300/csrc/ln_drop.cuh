@@ -484,7 +484,10 @@ template <class T>
 bool launch_ln_drop(const LnDropArgs& a, bool ragged, int* status, unsigned long long wait_ns, cudaStream_t st,
                     cudaError_t* error) {
   const int64_t m = (a.p.cols + Vec<T>::E - 1) / Vec<T>::E + (ragged ? 1 : 0);  // vectors of a row, at most
-  constexpr int kRows = Vec<T>::E == 8 ? 2 : 4;  // what 64 registers hold
+  // Rows of a lane in flight.  64 registers do not hold them: all but one form spill, 36 to 140 bytes.  Against half as
+  // many: [131072, 256] bf16 48 us and 53, but [262144, 128] 65 and 53, float32 [131072, 128] 49 and 45; twice as many
+  // bf16 rows 58 and 71, float32 ones 49 with one row.
+  constexpr int kRows = Vec<T>::E == 8 ? 2 : 4;
   if (m <= 8) return launch_drop_warp<T, 8, kRows>(a, ragged, st, error), true;
   if (m <= 16) return launch_drop_warp<T, 16, kRows>(a, ragged, st, error), true;
   if (m <= 32) return launch_drop_warp<T, 32, kRows>(a, ragged, st, error), true;
