@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
     if (tid == 0 && refill) issue(last, issued++);
     if constexpr (kCluster > 1) {
       // a thread that gives up here goes on with what there is and says so at the next barrier
-      late = !ptx::mbar_wait(&met[turn & 1], (uint32_t)(turn >> 1) & 1, &abort, status, wait_ns);
+      late = !ptx::mbar_wait<true>(&met[turn & 1], (uint32_t)(turn >> 1) & 1, &abort, status, wait_ns);
       if (tid == 0) ptx::mbar_arrive_expect_tx(&met[turn & 1], 2 * kWarps * sizeof(float));
     }
     if constexpr (kParts == 1) {

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kRow* kGroups, kBlocks)
       if constexpr (kRow == 32) return m;
       if constexpr (kCluster > 1) {
         // a thread that gives up here goes on with what there is and says so at the next barrier
-        late = !ptx::mbar_wait(&met[kind], (uint32_t)turn & 1, &abort, status, wait_ns) || late;
+        late = !ptx::mbar_wait<true>(&met[kind], (uint32_t)turn & 1, &abort, status, wait_ns) || late;
         if (tid == 0) ptx::mbar_arrive_expect_tx(&met[kind], kWarps * sizeof(float));
       }
       m = 0.f;
